@@ -22,6 +22,7 @@ STATUS_BAD_PLAN_INPUT = 4
 STATUS_LAYER_MISMATCH = 8
 
 OK, EINVAL, EALIGN, EPAGE, ECAPACITY, ERANGE, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5, -6, -7
+ENOMEM = -8
 SCRATCH_BYTES = 64 * 1024 * 1024  # GPB_SCRATCH_BYTES
 
 _I32P = ctypes.POINTER(ctypes.c_int32)
@@ -75,6 +76,54 @@ class gpb_layer_group(ctypes.Structure):
     _fields_ = [("d_dense", ctypes.c_void_p), ("table", ctypes.POINTER(gpb_sources)),
                 ("d_staging", ctypes.c_void_p), ("n_staging_rows", ctypes.c_int64),
                 ("d_cur_rows", ctypes.c_void_p), ("row_bytes", ctypes.c_int32)]
+
+
+MAX_AXES = 4
+BF16, FP16 = 1, 2
+
+
+class gpb_row_format(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "n_kv_heads", "k_dim", "v_dim", "values_in_key", "row_bytes")]
+
+
+class gpb_append(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("d_pool", ctypes.c_void_p), ("n_pool_rows", ctypes.c_int64),
+                ("d_pool_locs", ctypes.c_void_p), ("d_rows", ctypes.c_void_p),
+                ("d_q", ctypes.c_void_p), ("d_q_out", ctypes.c_void_p),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("qo_token_stride", ctypes.c_int64), ("qo_head_stride", ctypes.c_int64),
+                ("rot_start", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("section", ctypes.c_int32 * MAX_AXES),
+                ("d_inv_freq", ctypes.c_void_p), ("d_positions", ctypes.c_void_p),
+                ("positions_stride", ctypes.c_int64)]
+
+
+class gpb_attend_shape(ctypes.Structure):
+    _fields_ = [("bs", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("page_rows", ctypes.c_int32), ("h_q_lens", ctypes.c_void_p),
+                ("h_kv_lens", ctypes.c_void_p), ("n_groups", ctypes.c_int32),
+                ("h_groups", ctypes.c_void_p)]
+
+
+class gpb_attend_plan(ctypes.Structure):
+    _fields_ = [("format", gpb_row_format)] + [(n, ctypes.c_int32) for n in (
+        "bs", "n_heads", "window", "sinks", "page_rows", "n_groups", "n_tokens", "max_keys",
+        "n_items", "n_joins", "n_refs", "n_partial_rows", "joins_at", "refs_at",
+        "positions_at", "list_ints")] + [("workspace_bytes", ctypes.c_int64)]
+
+
+class gpb_attend_io(ctypes.Structure):
+    _fields_ = [("d_q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("d_out", ctypes.c_void_p),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("d_lse", ctypes.c_void_p), ("scale", ctypes.c_float)]
 
 
 def _hip_runtimes():
@@ -140,6 +189,17 @@ def _load(path):
     lib.gpb_compose_layer_groups.argtypes = [ctypes.POINTER(gpb_layer_group), i32,
                                              ctypes.POINTER(gpb_plan), i32, i32, i32, i32,
                                              vp, vp]
+    lib.gpb_row_append.argtypes = [ctypes.POINTER(gpb_row_format), ctypes.POINTER(gpb_append),
+                                   vp, vp]
+    lib.gpb_attend_plan_build.argtypes = [ctypes.POINTER(gpb_row_format),
+                                          ctypes.POINTER(gpb_attend_shape),
+                                          ctypes.POINTER(gpb_attend_plan), vp, i64]
+    lib.gpb_attend_dense.argtypes = [ctypes.POINTER(gpb_attend_plan), vp,
+                                     ctypes.POINTER(gpb_attend_io), vp, i64, vp, vp, i64, vp,
+                                     vp]
+    lib.gpb_attend_paged.argtypes = [ctypes.POINTER(gpb_attend_plan), vp,
+                                     ctypes.POINTER(gpb_attend_io), vp, i64, vp, i64, vp, i64,
+                                     vp, i64, vp, vp]
     lib.gpb_strerror.argtypes = [ctypes.c_int]
     lib.gpb_strerror.restype = ctypes.c_char_p
     for f in EXPORTS:
@@ -155,7 +215,8 @@ EXPORTS = ("gpb_plan_sizes", "gpb_plan_build", "gpb_plan_build_clear",
            "gpb_compose_layer_ahead", "gpb_compose_layer_noalloc",
            "gpb_compose_consume_fill", "gpb_compose_layer_ahead_fill",
            "gpb_current_row_fill", "gpb_current_row_scatter_groups",
-           "gpb_compose_gather_groups", "gpb_compose_layer_groups", "gpb_strerror")
+           "gpb_compose_gather_groups", "gpb_compose_layer_groups", "gpb_row_append",
+           "gpb_attend_plan_build", "gpb_attend_dense", "gpb_attend_paged", "gpb_strerror")
 
 lib = _load(LIB_PATH)
 
@@ -545,3 +606,291 @@ def compose_layer_groups(groups, plan, n_slots, n_cur_pages, n_rows, page_rows, 
                                         int(n_cur_pages), int(n_rows), int(page_rows),
                                         _ptr(status), _stream(stream)),
            "gpb_compose_layer_groups")
+
+
+# ---- making the rows, and reading them ---------------------------------------
+
+
+class RowFormat:
+    """What a token row holds: ``n_kv_heads`` key heads of ``k_dim`` values, then
+    as many value heads of ``v_dim``; with ``values_in_key`` one key head whose
+    first ``v_dim`` values are the value (a latent row).  ``dtype`` is "bf16" or
+    "fp16" (or the torch dtype), ``row_bytes`` the distance between rows."""
+
+    def __init__(self, dtype, n_kv_heads, k_dim, v_dim, values_in_key=False, row_bytes=None):
+        import torch
+        codes = {"bf16": BF16, "fp16": FP16, torch.bfloat16: BF16, torch.float16: FP16}
+        if dtype not in codes:
+            raise ValueError("a row's type is bf16 or fp16, not %r" % (dtype,))
+        self.dtype = torch.bfloat16 if codes[dtype] == BF16 else torch.float16
+        self.n_kv_heads, self.k_dim, self.v_dim = int(n_kv_heads), int(k_dim), int(v_dim)
+        self.values_in_key = bool(values_in_key)
+        payload = 2 * self.n_kv_heads * (self.k_dim + (0 if values_in_key else self.v_dim))
+        self.row_bytes = payload if row_bytes is None else int(row_bytes)
+        self.c = gpb_row_format(codes[dtype], self.n_kv_heads, self.k_dim, self.v_dim,
+                                int(self.values_in_key), self.row_bytes)
+
+
+class Rotation:
+    """Rotation of the values [start, start + 2 * len(inv_freq)) of every key and
+    query head (``inv_freq`` float32 device tensor, one entry per pair).
+    ``interleaved``: pairs are neighbours, else half the rotated values apart.
+    ``sections``: pairs per position axis (their sum the number of pairs); one
+    axis by default."""
+
+    def __init__(self, inv_freq, start=0, interleaved=False, sections=None):
+        import torch
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq: a contiguous float32 vector, got %s %s"
+                             % (inv_freq.dtype, tuple(inv_freq.shape)))
+        self.inv_freq, self.start, self.interleaved = inv_freq, int(start), bool(interleaved)
+        pairs = inv_freq.numel()
+        self.sections = [pairs] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(self.sections) <= MAX_AXES or sum(self.sections) != pairs:
+            raise ValueError("sections %s do not name the axis of %d pairs (at most %d axes)"
+                             % (self.sections, pairs, MAX_AXES))
+
+
+def _same_device(device, **tensors):
+    """Every tensor on ``device``; the launch goes there whatever the current
+    device is."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, the call runs on %s" % (name, t.device, device))
+
+
+def _heads(t, n_tokens, n_heads, dim, dtype, what):
+    """Strides (token, head) in elements of a [tokens, heads, dim] tensor whose
+    last dimension is contiguous."""
+    if t.dim() != 3 or t.dtype != dtype or t.shape[0] < n_tokens or t.shape[1] != n_heads \
+            or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+        raise ValueError("%s: need %s [>= %d, %d, %d] with its last dimension contiguous, got "
+                         "%s %s, strides %s" % (what, dtype, n_tokens, n_heads, dim, t.dtype,
+                                                tuple(t.shape), t.stride()))
+    return t.stride(0), t.stride(1)
+
+
+def _int32(t, numel, what):
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError("%s: need a contiguous int32 tensor of %d, got %s %s"
+                         % (what, numel, t.dtype, tuple(t.shape)))
+    return t
+
+
+def _rows_of(t, row_bytes, what):
+    """Number of whole rows in a contiguous tensor of any type."""
+    if not t.is_contiguous():
+        raise ValueError("%s: need a contiguous tensor" % what)
+    return t.numel() * t.element_size() // row_bytes
+
+
+class _on:
+    """The device of a call made current, and the stream it is given."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError("the rows are made and read on the GPU: device %s is not a GPU "
+                             "device" % device)
+        self.guard = torch.cuda.device(device)
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
+            self.stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+                torch.cuda.default_stream(device)
+        else:
+            if stream.device != device:
+                raise ValueError("the stream is on %s, the tensors on %s"
+                                 % (stream.device, device))
+            self.stream = stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *a):
+        return self.guard.__exit__(*a)
+
+
+def row_append(fmt, k, v, pool, pool_locs, rotation=None, positions=None, rows=None, q=None,
+               q_out=None, status=None, stream=None):
+    """Make rows from keys ``k`` [T, n_kv_heads, k_dim] and values ``v`` (None where
+    they are in the key), rotate the keys at ``positions`` (int32 [T], or [axes, T])
+    and store row t at pool row ``pool_locs[t]`` (int32 [T]; -1 stores none) and, with
+    ``rows``, at row t there.  ``pool`` may be None (then pool_locs too).  Queries
+    ``q`` [T, heads, k_dim] are rotated into ``q_out`` (``q`` itself by default).
+    One launch.  T is the length of ``pool_locs`` (of ``k`` without a pool)."""
+    T = k.shape[0] if pool_locs is None else pool_locs.numel()
+    dev = k.device
+    if q is not None and q_out is None:
+        q_out = q
+    _same_device(dev, v=v, pool=pool, pool_locs=pool_locs, rows=rows, q=q, q_out=q_out,
+                 positions=positions, status=status,
+                 inv_freq=None if rotation is None else rotation.inv_freq)
+    a = gpb_append()
+    a.n_rows = T
+    a.d_k = _ptr(k)
+    a.k_token_stride, a.k_head_stride = _heads(k, T, fmt.n_kv_heads, fmt.k_dim, fmt.dtype, "k")
+    if not fmt.values_in_key:
+        if v is None:
+            raise ValueError("v: the row format holds values apart from the keys")
+        a.d_v = _ptr(v)
+        a.v_token_stride, a.v_head_stride = _heads(v, T, fmt.n_kv_heads, fmt.v_dim, fmt.dtype,
+                                                   "v")
+    elif v is not None:
+        raise ValueError("v: the row format holds the values in the keys")
+    if pool is not None:
+        if pool_locs is None:
+            raise ValueError("pool_locs: a pool needs the rows to store at")
+        a.d_pool, a.n_pool_rows = _ptr(pool), _rows_of(pool, fmt.row_bytes, "pool")
+        a.d_pool_locs = _ptr(_int32(pool_locs, T, "pool_locs"))
+    elif pool_locs is not None:
+        raise ValueError("pool_locs without a pool")
+    if rows is not None:
+        if _rows_of(rows, fmt.row_bytes, "rows") < T:
+            raise ValueError("rows: %d rows of %d bytes do not fit" % (T, fmt.row_bytes))
+        a.d_rows = _ptr(rows)
+    if q is not None:
+        a.n_q_heads = q.shape[1] if q.dim() == 3 else 0
+        a.d_q, a.d_q_out = _ptr(q), _ptr(q_out)
+        a.q_token_stride, a.q_head_stride = _heads(q, T, a.n_q_heads, fmt.k_dim, fmt.dtype, "q")
+        a.qo_token_stride, a.qo_head_stride = _heads(q_out, T, a.n_q_heads, fmt.k_dim,
+                                                     fmt.dtype, "q_out")
+    if rotation is not None and rotation.inv_freq.numel():
+        if positions is None:
+            raise ValueError("positions: a rotation needs them")
+        n = len(rotation.sections)
+        if positions.dim() == 1:
+            positions = positions.unsqueeze(0)
+        import torch
+        if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[0] != n \
+                or positions.shape[1] < T or (T > 1 and positions.stride(1) != 1):
+            raise ValueError("positions: need int32 [%d, >= %d], got %s %s"
+                             % (n, T, positions.dtype, tuple(positions.shape)))
+        a.rot_start, a.rot_dim = rotation.start, 2 * rotation.inv_freq.numel()
+        a.interleaved, a.n_axes = int(rotation.interleaved), n
+        for i, s in enumerate(rotation.sections):
+            a.section[i] = s
+        a.d_inv_freq, a.d_positions = _ptr(rotation.inv_freq), _ptr(positions)
+        a.positions_stride = positions.stride(0)
+    with _on(dev, stream) as st:
+        _check(lib.gpb_row_append(ctypes.byref(fmt.c), ctypes.byref(a), _ptr(status), st),
+               "gpb_row_append")
+
+
+class AttendPlan:
+    """The work list of an attention over one batch, on the device: request r has
+    ``q_lens[r]`` queries, the last of its ``kv_lens[r]`` keys.  A query sees the
+    keys up to its own position, with ``window`` only the last ``window`` of them
+    and the first ``sinks`` of the sequence.  ``groups`` lists (first request,
+    number of requests, shared keys): consecutive requests that begin with the same
+    whole pages, read once for all of them (paged attention only).  One plan serves
+    every layer of the batch."""
+
+    def __init__(self, fmt, n_heads, q_lens, kv_lens, window=0, sinks=0, page_size=64,
+                 groups=(), device="cuda"):
+        import torch
+        h_q, h_kv, h_g = _host_i32(q_lens), _host_i32(kv_lens), _host_i32(list(groups))
+        if h_q.size != h_kv.size:
+            raise ValueError("%d q_lens, %d kv_lens" % (h_q.size, h_kv.size))
+        if h_g.size % 3:
+            raise ValueError("groups: (first request, number of requests, shared keys) each")
+        shape = gpb_attend_shape(h_q.size, int(n_heads), int(window), int(sinks),
+                                 int(page_size), h_q.ctypes.data if h_q.size else None,
+                                 h_kv.ctypes.data if h_q.size else None, h_g.size // 3,
+                                 h_g.ctypes.data if h_g.size else None)
+        self.fmt, self.n_heads = fmt, int(n_heads)
+        self.c = gpb_attend_plan()
+        _check(lib.gpb_attend_plan_build(ctypes.byref(fmt.c), ctypes.byref(shape),
+                                         ctypes.byref(self.c), None, 0),
+               "gpb_attend_plan_build")
+        self.list_host = np.zeros(max(self.c.list_ints, 4), np.int32)
+        _check(lib.gpb_attend_plan_build(ctypes.byref(fmt.c), ctypes.byref(shape),
+                                         ctypes.byref(self.c), self.list_host.ctypes.data,
+                                         self.list_host.size), "gpb_attend_plan_build")
+        self.n_tokens, self.bs = self.c.n_tokens, self.c.bs
+        self.workspace_bytes = self.c.workspace_bytes
+        dev = _gpu_device(device)
+        self.device = torch.device("cuda", torch.cuda.current_device()) \
+            if dev.index is None else dev
+        self.list = torch.from_numpy(self.list_host).to(self.device)
+
+    def workspace(self):
+        """A workspace for one call at a time."""
+        import torch
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+
+
+def _attend(plan, q, scale, out, lse, workspace, status, stream, call, what, **tensors):
+    import torch
+    fmt, T, dev = plan.fmt, plan.n_tokens, plan.device
+    _same_device(dev, q=q, out=out, lse=lse if torch.is_tensor(lse) else None,
+                 workspace=workspace, status=status, **tensors)
+    io = gpb_attend_io()
+    io.q_token_stride, io.q_head_stride = _heads(q, T, plan.n_heads, fmt.k_dim, fmt.dtype, "q")
+    io.scale = float(scale)
+    on = _on(dev, stream)
+    with on as st:
+        # what is allocated here belongs to the stream the kernels run on
+        with torch.cuda.stream(on.stream):
+            if out is None:
+                out = torch.empty(T, plan.n_heads, fmt.v_dim, dtype=fmt.dtype, device=dev)
+            if lse is True:
+                lse = torch.empty(T, plan.n_heads, dtype=torch.float32, device=dev)
+            if workspace is None and plan.workspace_bytes:
+                workspace = plan.workspace()
+        io.out_token_stride, io.out_head_stride = _heads(out, T, plan.n_heads, fmt.v_dim,
+                                                         fmt.dtype, "out")
+        if torch.is_tensor(lse):
+            if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.dim() != 2 or \
+                    lse.shape[0] < T or lse.shape[1] != plan.n_heads:
+                raise ValueError("lse: need a contiguous float32 [>= %d, %d], got %s %s"
+                                 % (T, plan.n_heads, lse.dtype, tuple(lse.shape)))
+            io.d_lse = _ptr(lse)
+        else:
+            lse = None
+        io.d_q, io.d_out = _ptr(q), _ptr(out)
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace: need a contiguous tensor")
+        n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(call(io, _ptr(workspace) if n else None, n, _ptr(status), st), what)
+    return out, lse
+
+
+def attend_dense(plan, q, dense, k_bases, scale, out=None, lse=True, workspace=None,
+                 status=None, stream=None):
+    """Attention of the packed queries ``q`` [T, heads, k_dim] over the dense buffer of
+    a compose: key x of request r is row ``k_bases[r] + x`` of ``dense``.  Returns
+    (out [T, heads, v_dim], lse [T, heads] float32, or None with ``lse=None``).
+    Without a workspace one is allocated for the call."""
+    rows = _rows_of(dense, plan.fmt.row_bytes, "dense")
+    _int32(k_bases, plan.bs, "k_bases")
+    return _attend(plan, q, scale, out, lse, workspace, status, stream,
+                   lambda io, ws, n, st, s: lib.gpb_attend_dense(
+                       ctypes.byref(plan.c), _ptr(plan.list), ctypes.byref(io), _ptr(dense),
+                       rows, _ptr(k_bases), ws, n, st, s),
+                   "gpb_attend_dense", dense=dense, k_bases=k_bases)
+
+
+def attend_paged(plan, q, pool, pages, scale, page_base=None, out=None, lse=True,
+                 workspace=None, status=None, stream=None):
+    """Attention of the packed queries over the paged pool.  ``pages`` is a table
+    [bs, pages] of int32 pool pages, or with ``page_base`` (int32 [bs]) one list in
+    which request r's pages start at entry ``page_base[r]`` (a compose plan's
+    slot_pages and slot_base).  Returns as attend_dense."""
+    rows = _rows_of(pool, plan.fmt.row_bytes, "pool")
+    stride = 0
+    if page_base is None:
+        if pages.dim() != 2 or pages.shape[0] < plan.bs:
+            raise ValueError("pages: need a table [>= %d, pages], got %s"
+                             % (plan.bs, tuple(pages.shape)))
+        stride = pages.shape[1]
+    else:
+        _int32(page_base, plan.bs, "page_base")
+    _int32(pages, 0, "pages")
+    return _attend(plan, q, scale, out, lse, workspace, status, stream,
+                   lambda io, ws, n, st, s: lib.gpb_attend_paged(
+                       ctypes.byref(plan.c), _ptr(plan.list), ctypes.byref(io), _ptr(pool),
+                       rows, _ptr(pages), pages.numel(), _ptr(page_base), stride, ws, n, st, s),
+                   "gpb_attend_paged", pool=pool, pages=pages, page_base=page_base)

@@ -1,0 +1,47 @@
+// The work list that gpb_attend_plan_build writes and the attention kernels
+// read, and the shapes both agree on.
+#pragma once
+
+#include "row_format.h"
+
+namespace gpb {
+
+// One workgroup: query rows [row0, row0 + n_rows) of one KV head over n_tiles
+// tiles of keys.  A query row is token * G + head within the KV head's group
+// of G heads, so the heads that share keys are neighbours.  Tile v is tile0 +
+// v for v < n_first and tile1 + v - n_first after it (a window leaves out the
+// keys between the first tokens and itself); keys outside [key_lo, key_hi)
+// are masked.  With partial >= 0 the item's sums go to that row of the
+// workspace, else its results go out.
+struct AttendItem {
+  int32_t req, row0, n_rows, kv_head;
+  int32_t key_lo, key_hi, n_tiles, tile0;
+  int32_t n_first, tile1, partial, wide;
+  int32_t pos_min, pos_max, pad0, pad1;
+};
+
+// Rows [row0, row0 + n_rows) of one KV head, all of one token, whose parts
+// start at workspace rows refs[ref0 .. ref0 + n_refs).
+struct AttendJoin {
+  int32_t row0, n_rows, kv_head, ref0, n_refs, pad0, pad1, pad2;
+};
+
+constexpr int kItemInts = sizeof(AttendItem) / 4;
+constexpr int kJoinInts = sizeof(AttendJoin) / 4;
+
+// A wide item's four waves take 32 query rows each of one tile of 64 keys; a
+// narrow item's four waves hold the same 32 rows or fewer, each over tiles of
+// 32 keys of its own.  Over latent rows every item is wide and has 64 rows,
+// two waves to each 32 of them.
+constexpr int kWideRows = 128, kNarrowRows = 32, kLatentRows = 64;
+constexpr int kWideTile = 64, kNarrowTile = 32;
+
+// Which attention kernel a format has, or -1.
+inline int attend_kernel(const gpb_row_format &f) {
+  if (f.k_dim == 64 && f.v_dim == 64 && !f.values_in_key) return 0;
+  if (f.k_dim == 128 && f.v_dim == 128 && !f.values_in_key) return 1;
+  if (f.k_dim == 576 && f.v_dim == 512 && f.values_in_key) return 2;
+  return -1;
+}
+
+}  // namespace gpb

@@ -1,0 +1,888 @@
+// attend.hip -- attention over composed or paged rows (gfx950).
+//
+// For a query q at position p and the keys k_x, values v_x it sees:
+// s_x = scale q.k_x, out = sum exp(s_x) v_x / sum exp(s_x), and
+// lse = log sum exp(s_x).  One pass over the keys with a running maximum m
+// and sum l (the sums of earlier keys are multiplied by 2^(m_old - m_new) when
+// m grows), scores in units of log2 so that exp is one v_exp_f32.
+//
+// Both products run on the 32x32x16 matrix instruction, transposed: the
+// scores as K Q^T, so a lane holds 16 keys' scores of one query row and the
+// row's maximum and sum need one exchange, with lane + 32; and the output as
+// V^T P^T, whose right operand then is what the lane holds already, and whose
+// rescaling is by a number of the lane's own.  The product over keys does not
+// mind their order, so V^T is read in the order the scores came out in:
+// operand element j of lane half h is key 8 (j / 4) + 4 h + j % 4 of 16, two
+// transposing LDS reads (ds_read_b64_tr_b16) of four keys each.
+//
+// Keys and values go to LDS by direct loads, 16 bytes a lane, a row's 16-byte
+// chunks permuted within the row (swizzle) so that neither the reads of K (16
+// rows at one chunk) nor those of V (4 rows at 4 chunks) meet in a bank: the
+// direct load fixes the LDS place of a lane, so the lane picks its source.
+//
+// Scores, m, l and the sums are fp32; P is rounded to the row's type for the
+// second product (its errors, at most half a step each, average out; l sums
+// the unrounded ones).
+#include <cmath>
+
+#include "attend.h"
+
+namespace gpb {
+namespace {
+
+struct AttendArgs {
+  const int32_t *list;
+  const uint16_t *q;
+  int64_t q_ts, q_hs;
+  const uint8_t *rows;      // dense buffer or pool
+  int64_t n_rows;           // rows of it; paged: of its whole pages
+  const int32_t *pages;     // NULL: dense
+  const int32_t *base;      // k_bases (dense), page_base or NULL (paged)
+  int64_t n_listed, pages_stride;
+  uint16_t *out;
+  int64_t o_ts, o_hs;
+  float *lse;
+  float *sums, *ml;         // workspace: sums [partial rows][DV], (m, l) pairs
+  int32_t *status;
+  float c;                  // scale * log2(e)
+  int32_t row_bytes, page_rows, window, sinks;
+  int32_t G, hkv, n_heads, n_tokens, bs, max_keys;
+  int32_t n_items, n_joins, n_refs, n_partial_rows, joins_at, refs_at, positions_at;
+};
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+__device__ __forceinline__ f32x16 mma(typename Vec<T>::x8 a, typename Vec<T>::x8 b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mma<__bf16>(Vec<__bf16>::x8 a, Vec<__bf16>::x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mma<_Float16>(Vec<_Float16>::x8 a, Vec<_Float16>::x8 b,
+                                                f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// The value of lane ^ 32.
+__device__ __forceinline__ float other_half(float x, int half) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x),
+                                                  __builtin_bit_cast(unsigned, x), false, false);
+  return __builtin_bit_cast(float, half ? r[0] : r[1]);
+}
+
+// Place of chunk c of row r.  Rows of 128 bytes start half way through the
+// banks in turn: the row's bits 1 .. 3 move the chunk among eight.  Rows of
+// whole 256 bytes all start at bank 0: its bits 0 .. 3 move it among sixteen.
+// The lowest of those bits go to the chunk bits in which the four rows of a
+// transposing read have to differ.
+template <int ROW_BYTES>
+__device__ __forceinline__ constexpr int swizzle(int r) {
+  return ROW_BYTES % 256 ? ((r << 1) & 4) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
+}
+
+template <typename T, int DK, int DV, bool IN_KEY>
+struct Attend {
+  static constexpr int KB = DK * 2, VB = DV * 2;              // bytes of a key, a value
+  // A tile of n keys in LDS: n rows of K0 bytes (a key, or the value part of a
+  // latent), then n rows of R1 bytes (a value, or the rest of a latent).
+  static constexpr int R0 = IN_KEY ? VB : KB, R1 = IN_KEY ? KB - VB : VB;
+  static constexpr int ROW = R0 + R1;                          // LDS bytes per key
+  static constexpr int TILES_LDS = 4 * kNarrowTile * ROW;      // = 2 * kWideTile * ROW
+  static constexpr int WAVE_XCHG = 2048 + 128;                 // latent: a wave's weights, maxima
+  static constexpr int LDS = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kWideRows);
+  static constexpr int NT = DV / 32 / (IN_KEY ? 2 : 1);        // output tiles of a wave
+  // chunks among which a row's are moved, and steps of 16 values they make
+  static constexpr int VS = IN_KEY ? R0 : R1;                  // LDS stride of values
+  static constexpr int G0 = R0 % 256 ? 8 : 16, G1 = R1 % 256 ? 8 : 16;
+  typedef typename Vec<T>::x8 x8;
+  typedef typename Vec<T>::x4 x4;
+  // P of fp16 is held times 2^6 (at most 2^6, l with it): weights down to
+  // 2^-31 of the largest keep a value, where fp16 alone ends at 2^-25
+  static constexpr float SHIFT = sizeof(T) == 2 && __is_same(T, _Float16) ? 6.0f : 0.0f;
+
+  // Row of the rows array that holds key `key` of the item's request.
+  static __device__ __forceinline__ uint32_t row_of(const AttendArgs &a, const AttendItem &it,
+                                                    int64_t base, int key) {
+    key = min(max(key, it.key_lo), it.key_hi - 1);
+    int64_t row;
+    bool ok;
+    if (a.pages) {
+      const int idx = static_cast<unsigned>(key) / static_cast<unsigned>(a.page_rows);
+      const int64_t at = base + idx;
+      ok = at >= 0 && at < a.n_listed;
+      const int page = ok ? a.pages[at] : 0;
+      row = static_cast<int64_t>(page) * a.page_rows + (key - idx * a.page_rows);
+      ok = ok && row >= 0 && row < a.n_rows && page >= 0;
+      if (!ok) row = key - idx * a.page_rows;
+    } else {
+      row = base + key;
+      ok = row >= 0 && row < a.n_rows;
+      if (!ok) row = 0;
+    }
+    if (!ok && a.status) atomicOr(a.status, GPB_STATUS_BAD_DESCRIPTOR);
+    return static_cast<uint32_t>(row);
+  }
+
+  // Direct loads of wave `wave` of WAVES into TILE LDS rows of B bytes from
+  // src: an instruction fills 64 chunks, a whole row or several.  Lane r of
+  // rid holds the source row of key r.
+  template <int B, int TILE, int WAVES>
+  static __device__ __forceinline__ void load_rows(const uint8_t *src, int row_bytes, uint32_t rid,
+                                                   lds_u8 *to, int wave, int lane) {
+    constexpr int C = B / 16, N = TILE * C / 64 / WAVES;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint8_t *from;
+      const int at = wave * N + i;  // instruction of the tile
+      if constexpr (C == 64) {
+        const uint32_t row = __builtin_amdgcn_readlane(rid, at);
+        from = src + static_cast<uint64_t>(row) * row_bytes;
+        from += static_cast<uint32_t>((lane ^ swizzle<B>(at)) * 16);
+      } else {
+        const int r = at * (64 / C) + lane / C;
+        const uint32_t row = __shfl(rid, r, 64);
+        from = src + static_cast<uint64_t>(row) * row_bytes + ((lane % C) ^ swizzle<B>(r)) * 16;
+      }
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void *)(from),
+          (__attribute__((address_space(3))) void *)(to + at * 1024), 16, 0, 0);
+    }
+  }
+
+  // One tile of TILE keys: WAVES waves share the load.
+  template <int TILE, int WAVES>
+  static __device__ __forceinline__ void load_tile(const AttendArgs &a, const AttendItem &it,
+                                                   uint32_t rid, lds_u8 *to, int wave, int lane) {
+    const uint8_t *k = a.rows + static_cast<int64_t>(it.kv_head) * KB;
+    const uint8_t *v = IN_KEY ? k + VB
+                              : a.rows + static_cast<int64_t>(a.hkv) * KB +
+                                    static_cast<int64_t>(it.kv_head) * VB;
+    load_rows<R0, TILE, WAVES>(k, a.row_bytes, rid, to, wave, lane);
+    load_rows<R1, TILE, WAVES>(v, a.row_bytes, rid, to + TILE * R0, wave, lane);
+  }
+
+  struct State {
+    f32x16 o[NT];
+    float m, l;
+  };
+
+  // Where in a tile the lane reads its operands.  The swizzle moves a chunk
+  // within its group only, so a few places serve every step, the rest being
+  // constant offsets.
+  struct Places {
+    uint32_t k0[G0 / 2], k1[IN_KEY ? G1 / 2 : 1];
+    uint32_t v[2][(IN_KEY ? G0 : G1) / 4];
+  };
+  static constexpr int VG = IN_KEY ? G0 : G1;  // group of a row of values
+
+  static __device__ __forceinline__ void find_places(Places &w, int lane) {
+    const int n = lane & 31, half = lane >> 5, i = lane & 15;
+#pragma unroll
+    for (int d = 0; d < G0 / 2; ++d) w.k0[d] = n * R0 + ((2 * d + half) ^ swizzle<R0>(n)) * 16;
+    if constexpr (IN_KEY)
+#pragma unroll
+      for (int d = 0; d < G1 / 2; ++d) w.k1[d] = n * R1 + ((2 * d + half) ^ swizzle<R1>(n)) * 16;
+    // V^T operand of 16 keys and 32 values: lane l gets value l % 32 of keys
+    // 4 half .. + 3 and 8 + 4 half .. + 3; of each 16 lanes, lane i reads four
+    // values of key i / 4
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int t = 0; t < VG / 4; ++t) {
+        const int row = 8 * x + 4 * half + (i >> 2);
+        const int chunk = 4 * t + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+        w.v[x][t] = row * VS + (chunk ^ swizzle<VS>(row)) * 16 + (i & 1) * 8;
+      }
+  }
+
+  static __device__ __forceinline__ x8 value_operand(const lds_u8 *v, const Places &w, int key0,
+                                                     int t) {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const int off = key0 * VS + t / (VG / 4) * VG * 16;
+    const s16x4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(v + w.v[0][t % (VG / 4)] + off));
+    const s16x4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(v + w.v[1][t % (VG / 4)] + off));
+    return __builtin_bit_cast(x8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+
+  static __device__ __forceinline__ bool sees(const AttendArgs &a, const AttendItem &it, int pos,
+                                              int key) {
+    return key <= pos && key >= it.key_lo && key < it.key_hi &&
+           (a.window == 0 || pos - key < a.window || key < a.sinks);
+  }
+
+  // Scores of the 32 keys in LDS rows row0 .. of a tile of TILE and the lane's
+  // query row, in units of log2, keys that it does not see at -infinity.
+  template <int TILE>
+  static __device__ __forceinline__ f32x16 scores(const AttendArgs &a, const AttendItem &it,
+                                                  const x8 *q, const lds_u8 *tile, int row0,
+                                                  const Places &w, int key0, bool whole, int pos,
+                                                  int half) {
+    typedef __attribute__((address_space(3))) x8 lds8;
+    f32x16 s = {};
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) {
+      constexpr int D0 = R0 / 32;  // steps in the rows of R0 bytes
+      const lds_u8 *at;
+      if (d < D0)
+        at = tile + row0 * R0 + w.k0[d % (G0 / 2)] + d / (G0 / 2) * G0 * 16;
+      else
+        at = tile + TILE * R0 + row0 * R1 + w.k1[IN_KEY ? (d - D0) % (G1 / 2) : 0] +
+             (d - D0) / (G1 / 2) * G1 * 16;
+      s = mma<T>(*(const lds8 *)at, q[d], s);
+    }
+    s *= a.c;
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = key0 + 8 * (i / 4) + 4 * half + i % 4;
+        s[i] = sees(a, it, pos, key) ? s[i] : -INFINITY;
+      }
+    }
+    return s;
+  }
+
+  static __device__ __forceinline__ float largest(f32x16 s) {
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    return top;
+  }
+
+  // Weights 2^(s - ref) of 32 keys, as two right operands of the second
+  // product; returns their sum.
+  static __device__ __forceinline__ float weights(f32x16 s, float ref, x8 *p) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = __builtin_amdgcn_exp2f(s[i] - (ref - SHIFT));
+      sum += x;
+      p[i / 8][i % 8] = static_cast<T>(x);
+    }
+    return sum;
+  }
+
+  // Sums of N output tiles (values 32 t0 ..) += weights of 16 * NP keys (LDS
+  // rows 0 .. of v).
+  template <int NP, int N>
+  static __device__ __forceinline__ void add_values(const x8 *p, const lds_u8 *v, const Places &w,
+                                                    int t0, f32x16 *o) {
+#pragma unroll
+    for (int b = 0; b < NP; ++b)
+#pragma unroll
+      for (int t = 0; t < N; ++t)
+        o[t] = mma<T>(value_operand(v + t0 / (VG / 4) * VG * 16, w, 16 * b, t), p[b], o[t]);
+  }
+
+  // A key that one row sees and another does not has weight 0 in the other's
+  // product, and 0 times infinity or NaN is NaN.  Tiles that are not whole are
+  // therefore looked through: one with such a value is left out of the
+  // products, and `careful` adds it at the end, row by row.  These lanes'
+  // share (id of ids) of the keys' values:
+  template <int TILE>
+  static __device__ __forceinline__ bool odd_values(const lds_u8 *tile, int id, int ids) {
+    typedef __attribute__((address_space(3))) u32x4 lds16;
+    const lds_u8 *v = IN_KEY ? tile : tile + TILE * R0;
+    bool odd = false;
+    for (int c = id; c < TILE * VS / 16; c += ids) {
+      const u32x4 x = *(const lds16 *)(v + c * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) odd |= not_finite(x[j]) || not_finite(x[j] >> 16);
+    }
+    return odd;
+  }
+  static __device__ __forceinline__ bool not_finite(unsigned bits) {
+    constexpr unsigned kExp = __is_same(T, _Float16) ? 0x7c00u : 0x7f80u;
+    return (bits & kExp) == kExp;
+  }
+
+  template <int N>
+  static __device__ __forceinline__ void rescale(f32x16 *o, float *l, float f) {
+    *l *= f;
+#pragma unroll
+    for (int t = 0; t < N; ++t) o[t] *= f;
+  }
+
+  // A tile of 32 * NB keys, the first at position key0.
+  template <int NB>
+  static __device__ __forceinline__ void keys(const AttendArgs &a, const AttendItem &it,
+                                              const x8 *q, const lds_u8 *tile, const Places &w,
+                                              int key0, bool whole, int pos, State &st, int lane) {
+    f32x16 s[NB];
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      s[b] = scores<32 * NB>(a, it, q, tile, 32 * b, w, key0 + 32 * b, whole, pos, lane >> 5);
+      top = fmaxf(top, largest(s[b]));
+    }
+    const float m = fmaxf(st.m, fmaxf(top, other_half(top, lane >> 5)));
+    const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 0
+    if (__any(m > st.m)) {
+      rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(st.m - ref));
+      st.m = m;
+    }
+    x8 p[2 * NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) st.l += weights(s[b], ref, p + 2 * b);
+    add_values<2 * NB, NT>(p, tile + 32 * NB * R0, w, 0, st.o);
+  }
+
+  static __device__ __forceinline__ bool whole_tile(const AttendArgs &a, const AttendItem &it,
+                                                    int key0, int n) {
+    return key0 >= it.key_lo && key0 + n <= it.key_hi && key0 + n - 1 <= it.pos_min &&
+           (a.window == 0 || it.pos_max - key0 < a.window || key0 + n <= a.sinks);
+  }
+
+  static __device__ __forceinline__ int first_key(const AttendItem &it, int v, int tile) {
+    return (v < it.n_first ? it.tile0 + v : it.tile1 + v - it.n_first) * tile;
+  }
+
+  // The lane's query row: its token, its head, its queries in registers.
+  static __device__ __forceinline__ void load_queries(const AttendArgs &a, const AttendItem &it,
+                                                      int row, int half, x8 *q, int *pos) {
+    const bool has = row < it.n_rows;
+    const int g = it.row0 + (has ? row : 0);
+    const int t = g / a.G, h = g - t * a.G + it.kv_head * a.G;
+    *pos = has ? a.list[a.positions_at + t] : -1;
+    const uint16_t *src = a.q + t * a.q_ts + h * a.q_hs + half * 8;
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d)
+      q[d] = has ? *reinterpret_cast<const x8 *>(src + d * 16) : x8{};
+  }
+
+  // What turns a row's sums and its m and l into results; a row that sees
+  // nothing has l = 0.
+  static __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+  static __device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.0f ? -INFINITY
+                     : (m + __builtin_amdgcn_logf(l) - SHIFT) * 0.69314718055994531f;
+  }
+
+  // The row's sums (or results) of output tiles t0 ..; the first also its m
+  // and l (or its log-sum).
+  static __device__ __forceinline__ void store(const AttendArgs &a, const AttendItem &it, int row,
+                                               int half, const State &st, float l, int t0) {
+    if (row >= it.n_rows) return;
+    if (it.partial >= 0) {
+      const int64_t at = static_cast<int64_t>(it.partial) + row;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          f32x4 x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = st.o[t][4 * y + j];
+          *reinterpret_cast<f32x4 *>(a.sums + at * DV + 32 * (t0 + t) + 8 * y + 4 * half) = x;
+        }
+      if (half == 0 && t0 == 0) *reinterpret_cast<f32x2 *>(a.ml + 2 * at) = f32x2{st.m, l};
+      return;
+    }
+    const int g = it.row0 + row;
+    const int token = g / a.G, h = g - token * a.G + it.kv_head * a.G;
+    uint16_t *dst = a.out + token * a.o_ts + h * a.o_hs;
+    const float inv = inverse(l);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        x4 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = static_cast<T>(st.o[t][4 * y + j] * inv);
+        *reinterpret_cast<x4 *>(dst + 32 * (t0 + t) + 8 * y + 4 * half) = x;
+      }
+    if (half == 0 && t0 == 0 && a.lse)
+      a.lse[static_cast<int64_t>(token) * a.n_heads + h] = log_sum(st.m, l);
+  }
+
+  static __device__ __forceinline__ int64_t request_base(const AttendArgs &a, int req) {
+    return a.base ? a.base[req] : req * a.pages_stride;
+  }
+
+  // The end of an item whose products left tiles out (see odd_values): the
+  // sums so far go to LDS, and a wave takes a row at a time through the left
+  // tiles, key by key, only those that the row sees.
+  static __device__ void careful(const AttendArgs &a, const AttendItem &it, lds_u8 *lds, int row,
+                                 int half, const State &st, float l, int t0, bool holds) {
+    typedef __attribute__((address_space(3))) float lds_float;
+    lds_float *sums = (lds_float *)lds, *ml = (lds_float *)(lds + TILES_LDS);
+    const int lane = threadIdx.x & 63;
+    constexpr int PK = DK / 64, PV = DV / 64;
+    __syncthreads();
+    if (holds && row < it.n_rows) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          sums[row * DV + 32 * (t0 + t) + 8 * (i / 4) + 4 * half + i % 4] = st.o[t][i];
+      if (half == 0 && t0 == 0) {
+        ml[2 * row] = st.m;
+        ml[2 * row + 1] = l;
+      }
+    }
+    __syncthreads();
+    const int tile = it.wide ? kWideTile : kNarrowTile;
+    const int64_t base = request_base(a, it.req);
+    const T *keys = reinterpret_cast<const T *>(a.rows) + static_cast<int64_t>(it.kv_head) * DK;
+    const T *vals = IN_KEY ? keys : reinterpret_cast<const T *>(a.rows) +
+                                        static_cast<int64_t>(a.hkv) * DK +
+                                        static_cast<int64_t>(it.kv_head) * DV;
+    const int64_t row_values = a.row_bytes / 2;
+    for (int r = threadIdx.x >> 6; r < it.n_rows; r += 4) {
+      const int g = it.row0 + r;
+      const int token = g / a.G, h = g - token * a.G + it.kv_head * a.G;
+      const int pos = a.list[a.positions_at + token];
+      const T *src = reinterpret_cast<const T *>(a.q + token * a.q_ts + h * a.q_hs);
+      float q[PK], o[PV], m = ml[2 * r], sum = ml[2 * r + 1];
+#pragma unroll
+      for (int e = 0; e < PK; ++e) q[e] = static_cast<float>(src[e * 64 + lane]);
+#pragma unroll
+      for (int e = 0; e < PV; ++e) o[e] = sums[r * DV + e * 64 + lane];
+      for (int v = 0; v < it.n_tiles; ++v) {
+        const int key0 = first_key(it, v, tile);
+        if (whole_tile(a, it, key0, tile)) continue;
+        bool odd = false;
+        for (int x = 0; x < tile; ++x) {
+          const T *val = vals + row_of(a, it, base, key0 + x) * row_values;
+          for (int e = lane; e < DV; e += 64)
+            odd |= not_finite(__builtin_bit_cast(uint16_t, val[e]));
+        }
+        if (!__any(odd)) continue;
+        for (int x = 0; x < tile; ++x) {
+          const int key = key0 + x;
+          if (!sees(a, it, pos, key)) continue;
+          const int64_t at = row_of(a, it, base, key) * row_values;
+          float s = 0.0f;
+#pragma unroll
+          for (int e = 0; e < PK; ++e) s += q[e] * static_cast<float>(keys[at + e * 64 + lane]);
+#pragma unroll
+          for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+          s *= a.c;
+          const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.0f : top;
+          const float f = __builtin_amdgcn_exp2f(m - ref);
+          const float w = __builtin_amdgcn_exp2f(s - (ref - SHIFT));
+          sum = sum * f + w;
+#pragma unroll
+          for (int e = 0; e < PV; ++e)
+            o[e] = o[e] * f + w * static_cast<float>(vals[at + e * 64 + lane]);
+          m = top;
+        }
+      }
+      if (it.partial >= 0) {
+        const int64_t at = static_cast<int64_t>(it.partial) + r;
+#pragma unroll
+        for (int e = 0; e < PV; ++e) a.sums[at * DV + e * 64 + lane] = o[e];
+        if (lane == 0) *reinterpret_cast<f32x2 *>(a.ml + 2 * at) = f32x2{m, sum};
+      } else {
+        T *dst = reinterpret_cast<T *>(a.out + token * a.o_ts + h * a.o_hs);
+        const float inv = inverse(sum);
+#pragma unroll
+        for (int e = 0; e < PV; ++e) dst[e * 64 + lane] = static_cast<T>(o[e] * inv);
+        if (lane == 0 && a.lse)
+          a.lse[static_cast<int64_t>(token) * a.n_heads + h] = log_sum(m, sum);
+      }
+    }
+  }
+
+  // Four waves, 32 rows each, tiles of 64 keys in two LDS buffers.
+  static __device__ __forceinline__ void wide(const AttendArgs &a, const AttendItem &it,
+                                              lds_u8 *lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = wave * 32 + (lane & 31), half = lane >> 5;
+    constexpr int BUF = kWideTile * ROW;
+    x8 q[DK / 16];
+    int pos;
+    load_queries(a, it, row, half, q, &pos);
+    Places w;
+    find_places(w, lane);
+    State st;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) st.o[t] = f32x16{};
+    st.m = -INFINITY;
+    st.l = 0.0f;
+    bool left = false;  // a tile is left to `careful`
+    if (it.n_tiles > 0) {
+      const int64_t base = request_base(a, it.req);
+      uint32_t rid = row_of(a, it, base, first_key(it, 0, kWideTile) + lane);
+      load_tile<kWideTile, 4>(a, it, rid, lds, wave, lane);
+      rid = row_of(a, it, base, first_key(it, min(1, it.n_tiles - 1), kWideTile) + lane);
+      for (int v = 0; v < it.n_tiles; ++v) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        lds_u8 *now = lds + (v & 1) * BUF;
+        if (v + 1 < it.n_tiles) {
+          load_tile<kWideTile, 4>(a, it, rid, lds + (~v & 1) * BUF, wave, lane);
+          if (v + 2 < it.n_tiles)
+            rid = row_of(a, it, base, first_key(it, v + 2, kWideTile) + lane);
+        }
+        const int key0 = first_key(it, v, kWideTile);
+        const bool whole = whole_tile(a, it, key0, kWideTile);
+        if (!whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256))) {
+          left = true;
+          continue;
+        }
+        keys<2>(a, it, q, now, w, key0, whole, pos, st, lane);
+      }
+    }
+    const float l = st.l + other_half(st.l, half);
+    if (__syncthreads_or(left)) careful(a, it, lds, row, half, st, l, 0, true);
+    else store(a, it, row, half, st, l, 0);
+  }
+
+  // Latent rows: 64 query rows, two waves to each 32 of them.  The sums of a
+  // row are 512 values, too many registers beside its 576 of query for one
+  // wave, so of a tile's 64 keys each wave of a pair scores 32, hands its
+  // weights to the other through LDS, and both add all 64 keys to their half
+  // of the values.  A wave weighs by the larger of the pair's last common
+  // maximum and its own keys' maximum; where the two differ (a new maximum)
+  // the weights are brought to the larger one before they are used.
+  static __device__ __forceinline__ void latent(const AttendArgs &a, const AttendItem &it,
+                                              lds_u8 *lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int part = wave & 1, half = lane >> 5;
+    const int row = (wave >> 1) * 32 + (lane & 31);
+    const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
+    constexpr int BUF = kWideTile * ROW;
+    lds_u8 *mine = lds + TILES_LDS + wave * WAVE_XCHG;
+    const lds_u8 *theirs = lds + TILES_LDS + (wave ^ 1) * WAVE_XCHG;
+    typedef __attribute__((address_space(3))) x8 lds8;
+    typedef __attribute__((address_space(3))) float lds_float;
+    x8 q[DK / 16];
+    int pos;
+    load_queries(a, it, row, half, q, &pos);
+    Places w;
+    find_places(w, lane);
+    State st;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) st.o[t] = f32x16{};
+    st.m = -INFINITY;
+    st.l = 0.0f;
+    bool left = false;  // a tile is left to `careful`
+    if (it.n_tiles > 0) {
+      const int64_t base = request_base(a, it.req);
+      uint32_t rid = row_of(a, it, base, first_key(it, 0, kWideTile) + lane);
+      load_tile<kWideTile, 4>(a, it, rid, lds, wave, lane);
+      rid = row_of(a, it, base, first_key(it, min(1, it.n_tiles - 1), kWideTile) + lane);
+      for (int v = 0; v < it.n_tiles; ++v) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        lds_u8 *now = lds + (v & 1) * BUF;
+        if (v + 1 < it.n_tiles) {
+          load_tile<kWideTile, 4>(a, it, rid, lds + (~v & 1) * BUF, wave, lane);
+          if (v + 2 < it.n_tiles)
+            rid = row_of(a, it, base, first_key(it, v + 2, kWideTile) + lane);
+        }
+        const int key0 = first_key(it, v, kWideTile);
+        const bool whole = whole_tile(a, it, key0, kWideTile);
+        if (!whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256))) {
+          left = true;
+          continue;
+        }
+        x8 p[2], p2[2];
+        float m = -INFINITY;
+        if (!idle) {
+          const f32x16 s = scores<kWideTile>(a, it, q, now, 32 * part, w, key0 + 32 * part, whole,
+                                             pos, half);
+          const float top = largest(s);
+          m = fmaxf(st.m, fmaxf(top, other_half(top, half)));
+          const float sum = weights(s, m == -INFINITY ? 0.0f : m, p);
+          if (__any(m > st.m)) st.l *= __builtin_amdgcn_exp2f(st.m - (m == -INFINITY ? 0.0f : m));
+          st.l += sum;
+          ((lds8 *)mine)[lane] = p[0];
+          ((lds8 *)mine)[64 + lane] = p[1];
+          if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
+        }
+        __syncthreads();
+        if (!idle) {
+          p2[0] = ((const lds8 *)theirs)[lane];
+          p2[1] = ((const lds8 *)theirs)[64 + lane];
+          const float m2 = ((const lds_float *)(theirs + 2048))[lane & 31];
+          const float both = fmaxf(m, m2), ref = both == -INFINITY ? 0.0f : both;
+          if (__any(m != m2)) {
+            const float f = __builtin_amdgcn_exp2f(m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
+            st.l *= f;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                p[b][j] = static_cast<T>(static_cast<float>(p[b][j]) * f);
+                p2[b][j] = static_cast<T>(static_cast<float>(p2[b][j]) * f2);
+              }
+          }
+          if (__any(both > st.m)) {
+            float unused = 0.0f;
+            rescale<NT>(st.o, &unused, __builtin_amdgcn_exp2f(st.m - ref));
+            st.m = both;
+          }
+          add_values<2, NT>(p, now + 32 * part * VS, w, part * NT, st.o);
+          add_values<2, NT>(p2, now + 32 * (1 - part) * VS, w, part * NT, st.o);
+        }
+      }
+    }
+    // each wave has summed the weights of its own keys
+    float l = st.l + other_half(st.l, half);
+    __syncthreads();
+    ((lds_float *)mine)[lane] = l;
+    __syncthreads();
+    l += ((const lds_float *)theirs)[lane];
+    if (__syncthreads_or(left)) careful(a, it, lds, row, half, st, l, part * NT, true);
+    else store(a, it, row, half, st, l, part * NT);
+  }
+
+  // Four waves over the same rows, each with tiles of 32 keys of its own;
+  // their sums meet in LDS at the end, the waves in order.
+  static __device__ __forceinline__ void narrow(const AttendArgs &a, const AttendItem &it,
+                                              lds_u8 *lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = lane & 31, half = lane >> 5;
+    x8 q[DK / 16];
+    int pos;
+    load_queries(a, it, row, half, q, &pos);
+    Places w;
+    find_places(w, lane);
+    State st;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) st.o[t] = f32x16{};
+    st.m = -INFINITY;
+    st.l = 0.0f;
+    bool left = false;  // a tile is left to `careful`
+    lds_u8 *own = lds + wave * kNarrowTile * ROW;
+    if (wave < it.n_tiles) {
+      const int64_t base = request_base(a, it.req);
+      uint32_t rid = row_of(a, it, base, first_key(it, wave, kNarrowTile) + (lane & 31));
+      for (int v = wave; v < it.n_tiles; v += 4) {
+        load_tile<kNarrowTile, 1>(a, it, rid, own, 0, lane);
+        if (v + 4 < it.n_tiles)
+          rid = row_of(a, it, base, first_key(it, v + 4, kNarrowTile) + (lane & 31));
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const int key0 = first_key(it, v, kNarrowTile);
+        const bool whole = whole_tile(a, it, key0, kNarrowTile);
+        if (!whole && __any(odd_values<kNarrowTile>(own, lane, 64))) left = true;
+        else keys<1>(a, it, q, own, w, key0, whole, pos, st, lane);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+    }
+    float l = st.l + other_half(st.l, half);
+
+    // waves 2 and 3 hand over to 0 and 1, then 1 to 0
+    typedef __attribute__((address_space(3))) float lds_float;
+    lds_float *slot = (lds_float *)lds;
+    constexpr int SLOT = (NT * 16 + 2) * 64;
+#pragma unroll
+    for (int step = 2; step >= 1; step >>= 1) {
+      __syncthreads();
+      if (wave >= step && wave < 2 * step) {
+        lds_float *to = slot + (wave - step) * SLOT + lane;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) to[(t * 16 + i) * 64] = st.o[t][i];
+        to[NT * 16 * 64] = st.m;
+        to[NT * 16 * 64 + 64] = l;
+      }
+      __syncthreads();
+      if (wave < step) {
+        const lds_float *from = slot + wave * SLOT + lane;
+        const float m2 = from[NT * 16 * 64], l2 = from[NT * 16 * 64 + 64];
+        const float m = fmaxf(st.m, m2), ref = m == -INFINITY ? 0.0f : m;
+        const float f1 = __builtin_amdgcn_exp2f(st.m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
+        l = l * f1 + l2 * f2;
+        st.m = m;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            st.o[t][i] = st.o[t][i] * f1 + from[(t * 16 + i) * 64] * f2;
+      }
+    }
+    if (__syncthreads_or(left)) careful(a, it, lds, row, half, st, l, 0, wave == 0);
+    else if (wave == 0) store(a, it, row, half, st, l, 0);
+  }
+};
+
+template <typename T, int DK, int DV, bool IN_KEY>
+__global__ __launch_bounds__(256, IN_KEY ? 1 : 2) void k_attend(AttendArgs a) {
+  typedef Attend<T, DK, DV, IN_KEY> A;
+  __shared__ __attribute__((aligned(1024))) uint8_t memory[A::LDS];
+  lds_u8 *lds = (lds_u8 *)memory;
+  const AttendItem it = reinterpret_cast<const AttendItem *>(a.list)[blockIdx.x];
+  // the list is the caller's device memory: an item outside the batch is left
+  // out, whatever it holds
+  const int64_t all = static_cast<int64_t>(a.n_tokens) * a.G;
+  const bool ok = it.req >= 0 && it.req < a.bs && it.row0 >= 0 && it.n_rows >= 1 &&
+                  it.n_rows <= (IN_KEY ? kLatentRows : it.wide ? kWideRows : kNarrowRows) &&
+                  it.row0 + it.n_rows <= all &&
+                  it.kv_head >= 0 && it.kv_head < a.hkv && it.key_lo >= 0 &&
+                  it.key_lo <= it.key_hi && it.key_hi <= a.max_keys &&
+                  (it.n_tiles == 0 || it.key_lo < it.key_hi) && it.n_tiles >= 0 &&
+                  it.n_tiles <= a.max_keys / kNarrowTile + 1 && it.n_first >= 0 &&
+                  it.tile0 >= 0 && it.tile1 >= 0 && it.tile0 <= a.max_keys / kNarrowTile &&
+                  it.tile1 <= a.max_keys / kNarrowTile && it.partial >= -1 &&
+                  it.partial <= a.n_partial_rows - (it.partial < 0 ? 0 : it.n_rows);
+  if (!ok) {
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, GPB_STATUS_BAD_PLAN_INPUT);
+    return;
+  }
+  if constexpr (IN_KEY) {
+    A::latent(a, it, lds);
+  } else {
+    if (it.wide) A::wide(a, it, lds);
+    else A::narrow(a, it, lds);
+  }
+}
+
+// The rows of one token and KV head: parts weighted by 2^(m - max m), in the
+// order of the list.  A wave a row, a lane DV / 64 values.
+template <typename T, int DV>
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+  const AttendJoin j = reinterpret_cast<const AttendJoin *>(a.list + a.joins_at)[blockIdx.x];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int PER = DV / 64;
+  bool ok = j.row0 >= 0 && j.n_rows >= 1 && j.n_rows <= kNarrowRows &&
+            static_cast<int64_t>(j.row0) + j.n_rows <= static_cast<int64_t>(a.n_tokens) * a.G &&
+            j.kv_head >= 0 && j.kv_head < a.hkv && j.ref0 >= 0 && j.n_refs >= 1 &&
+            j.ref0 <= a.n_refs - j.n_refs;
+  const int32_t *refs = a.list + a.refs_at + (ok ? j.ref0 : 0);
+  for (int i = lane; ok && i < j.n_refs; i += 64)
+    if (refs[i] < 0 || refs[i] > a.n_partial_rows - j.n_rows) ok = false;
+  if (__any(!ok)) {
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, GPB_STATUS_BAD_PLAN_INPUT);
+    return;
+  }
+  typedef Attend<T, 64, 64, false> A;  // for what depends on T alone
+  for (int r = wave; r < j.n_rows; r += 4) {
+    float top = -INFINITY;
+    for (int i = 0; i < j.n_refs; ++i)
+      top = fmaxf(top, a.ml[2 * (static_cast<int64_t>(refs[i]) + r)]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f, o[PER] = {};
+    for (int i = 0; i < j.n_refs; ++i) {
+      const int64_t at = static_cast<int64_t>(refs[i]) + r;
+      const f32x2 ml = *reinterpret_cast<const f32x2 *>(a.ml + 2 * at);
+      const float f = __builtin_amdgcn_exp2f(ml[0] - ref);
+      l += ml[1] * f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] += a.sums[at * DV + lane * PER + e] * f;
+    }
+    const int g = j.row0 + r;
+    const int t = g / a.G, h = g - t * a.G + j.kv_head * a.G;
+    const float inv = A::inverse(l);
+    T *dst = reinterpret_cast<T *>(a.out + t * a.o_ts + h * a.o_hs) + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(o[e] * inv);
+    if (lane == 0 && a.lse)
+      a.lse[static_cast<int64_t>(t) * a.n_heads + h] = A::log_sum(top, l);
+  }
+}
+
+template <typename T, int DK, int DV, bool IN_KEY>
+int launch_attend(const AttendArgs &a, hipStream_t st) {
+  int rc = launch(k_attend<T, DK, DV, IN_KEY>, dim3(a.n_items), dim3(256), st, a);
+  if (rc == GPB_OK && a.n_joins > 0)
+    rc = launch(k_attend_join<T, DV>, dim3(a.n_joins), dim3(256), st, a);
+  return rc;
+}
+
+template <typename T>
+int launch_format(int which, const AttendArgs &a, hipStream_t st) {
+  if (which == 0) return launch_attend<T, 64, 64, false>(a, st);
+  if (which == 1) return launch_attend<T, 128, 128, false>(a, st);
+  return launch_attend<T, 576, 512, true>(a, st);
+}
+
+int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io *io,
+           const void *d_rows, int64_t n_rows, const int32_t *d_pages, int64_t n_listed,
+           const int32_t *d_base, int64_t pages_stride, bool paged, void *d_workspace,
+           int64_t workspace_bytes, int32_t *d_status, void *stream) {
+  if (!p || !io) return GPB_EINVAL;
+  int rc = check_format(&p->format);
+  if (rc != GPB_OK) return rc;
+  const int which = attend_kernel(p->format);
+  if (which < 0 || p->bs < 0 || p->n_heads < 1 || p->n_heads % p->format.n_kv_heads ||
+      p->n_tokens < 0 || p->max_keys < 0 || p->n_items < 0 || p->n_joins < 0 || p->n_refs < 0 ||
+      p->n_partial_rows < 0 || p->window < 0 || p->sinks < 0 || p->page_rows < 1 ||
+      p->list_ints < 0)
+    return GPB_EINVAL;
+  const int64_t items = static_cast<int64_t>(p->n_items) * kItemInts;
+  if (p->joins_at != items ||
+      p->refs_at != items + static_cast<int64_t>(p->n_joins) * kJoinInts ||
+      p->positions_at != static_cast<int64_t>(p->refs_at) + p->n_refs ||
+      p->list_ints != static_cast<int64_t>(p->positions_at) + p->n_tokens ||
+      p->workspace_bytes !=
+          static_cast<int64_t>(p->n_partial_rows) * (p->format.v_dim + 2) * 4)
+    return GPB_EINVAL;
+  if (!(io->scale > 0.0f) || std::isinf(io->scale)) return GPB_EINVAL;
+  if (!paged && p->n_groups > 0) return GPB_EINVAL;
+  if (n_rows < 0 || n_listed < 0 || pages_stride < 0 || workspace_bytes < 0) return GPB_EINVAL;
+  if (n_rows > INT32_MAX) return GPB_ERANGE;
+  if (p->n_tokens == 0) return GPB_OK;
+  if (!d_list || !io->d_q || !io->d_out) return GPB_EINVAL;
+  if (workspace_bytes < p->workspace_bytes || (p->workspace_bytes > 0 && !d_workspace))
+    return GPB_EINVAL;
+  int64_t usable = n_rows;
+  if (paged) usable = n_rows / p->page_rows * p->page_rows;
+  if (p->max_keys > 0) {
+    if (!d_rows || usable < 1) return GPB_EINVAL;
+    if (!paged && !d_base) return GPB_EINVAL;
+    if (paged) {
+      if (!d_pages || n_listed < 1) return GPB_EINVAL;
+      if (!d_base && (pages_stride < ceil_div64(p->max_keys, p->page_rows) ||
+                      pages_stride > n_listed / p->bs))
+        return GPB_EINVAL;
+    }
+  }
+  if (!aligned(d_list, 16) || !aligned(io->d_q, 16) || !aligned(io->d_out, 8) ||
+      !aligned(io->d_lse, 4) || !aligned(d_rows, 16) || !aligned(d_pages, 4) ||
+      !aligned(d_base, 4) || !aligned(d_workspace, 16) || !aligned(d_status, 4) ||
+      io->q_token_stride % 8 || io->q_head_stride % 8 || io->out_token_stride % 4 ||
+      io->out_head_stride % 4)
+    return GPB_EALIGN;
+
+  AttendArgs a = {};
+  a.list = d_list;
+  a.q = static_cast<const uint16_t *>(io->d_q);
+  a.q_ts = io->q_token_stride; a.q_hs = io->q_head_stride;
+  a.rows = static_cast<const uint8_t *>(d_rows);
+  a.n_rows = usable;
+  a.pages = paged ? d_pages : nullptr;
+  a.base = d_base; a.n_listed = n_listed; a.pages_stride = pages_stride;
+  a.out = static_cast<uint16_t *>(io->d_out);
+  a.o_ts = io->out_token_stride; a.o_hs = io->out_head_stride;
+  a.lse = io->d_lse;
+  a.sums = static_cast<float *>(d_workspace);
+  a.ml = a.sums + static_cast<int64_t>(p->n_partial_rows) * p->format.v_dim;
+  a.status = d_status;
+  a.c = io->scale * 1.44269504088896341f;
+  a.row_bytes = p->format.row_bytes; a.page_rows = p->page_rows;
+  a.window = p->window; a.sinks = p->sinks;
+  a.hkv = p->format.n_kv_heads; a.n_heads = p->n_heads; a.G = p->n_heads / a.hkv;
+  a.n_tokens = p->n_tokens; a.bs = p->bs; a.max_keys = p->max_keys;
+  a.n_items = p->n_items; a.n_joins = p->n_joins; a.n_refs = p->n_refs;
+  a.n_partial_rows = p->n_partial_rows;
+  a.joins_at = p->joins_at; a.refs_at = p->refs_at; a.positions_at = p->positions_at;
+  return p->format.dtype == GPB_BF16 ? launch_format<__bf16>(which, a, as_stream(stream))
+                                     : launch_format<_Float16>(which, a, as_stream(stream));
+}
+
+}  // namespace
+}  // namespace gpb
+
+extern "C" int gpb_attend_dense(const gpb_attend_plan *plan, const int32_t *d_list,
+                                const gpb_attend_io *io, const void *d_dense,
+                                int64_t n_dense_rows, const int32_t *d_k_bases,
+                                void *d_workspace, int64_t workspace_bytes, int32_t *d_status,
+                                void *stream) {
+  return gpb::attend(plan, d_list, io, d_dense, n_dense_rows, nullptr, 0, d_k_bases, 0, false,
+                     d_workspace, workspace_bytes, d_status, stream);
+}
+
+extern "C" int gpb_attend_paged(const gpb_attend_plan *plan, const int32_t *d_list,
+                                const gpb_attend_io *io, const void *d_pool,
+                                int64_t n_pool_rows, const int32_t *d_pages,
+                                int64_t n_pages_listed, const int32_t *d_page_base,
+                                int64_t pages_stride, void *d_workspace,
+                                int64_t workspace_bytes, int32_t *d_status, void *stream) {
+  return gpb::attend(plan, d_list, io, d_pool, n_pool_rows, d_pages, n_pages_listed,
+                     d_page_base, pages_stride, true, d_workspace, workspace_bytes, d_status,
+                     stream);
+}

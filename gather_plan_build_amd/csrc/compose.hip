@@ -556,6 +556,7 @@ extern "C" const char *gpb_strerror(int status) {
     case GPB_ERANGE: return "index or size does not fit in int32";
     case GPB_EHIP: return gpb::hip_error_text;
     case GPB_ESCRATCH: return "staging would exceed the library's static scratch array";
+    case GPB_ENOMEM: return "out of host memory";
     default: return "unknown gpb status";
   }
 }

@@ -268,6 +268,48 @@ class ComposeRunner:
                            self.n_pool_pages * self.ps, self.plan.t["pool_locs"],
                            self.curs[k], self.T, self.rb, self.status, stream)
 
+    # Around the compose: the rows it moves are made by ``append`` and read by
+    # ``attend`` (or, straight from the pool, by ``attend_pool``).
+
+    def append(self, layer, fmt, k, v, rotation=None, positions=None, q=None, q_out=None,
+               stream=None):
+        """The layer's current rows made from keys and values (rotated at
+        ``positions``): token-packed into the layer's current rows, which the
+        compose takes, and at their pool rows in the layer's pool arena."""
+        self._check_format(fmt)
+        B.row_append(fmt, k, v, self.pools[layer % len(self.pools)], self.plan.t["pool_locs"],
+                     rotation, positions, rows=self.curs[layer % len(self.curs)], q=q,
+                     q_out=q_out, status=self.status, stream=stream)
+
+    def attend_plan(self, fmt, n_heads, window=0, sinks=0):
+        """The attention work list of the batch: every current token a query
+        over its request's prefix and the current tokens up to itself."""
+        self._check_format(fmt)
+        kv = self.meta.h_prefix.astype("int64") * self.ps + self.meta.h_cur
+        return B.AttendPlan(fmt, n_heads, self.meta.h_cur, kv, window=window, sinks=sinks,
+                            page_size=self.ps, device=self.plan.device)
+
+    def attend(self, layer, plan, q, scale, out=None, lse=True, workspace=None, stream=None):
+        """Attention of the layer's queries (token-packed) over its dense half."""
+        return B.attend_dense(plan, q, self.dense_of(layer), self.plan.t["k_bases"], scale,
+                              out=out, lse=lse, workspace=workspace, status=self.status,
+                              stream=stream)
+
+    def attend_pool(self, layer, plan, q, scale, out=None, lse=True, workspace=None,
+                    stream=None):
+        """The same attention read from the layer's pool arena through the
+        plan's slot pages; the pool must hold the current rows (``append``, or
+        one of the fused fills)."""
+        return B.attend_paged(plan, q, self.pools[layer % len(self.pools)],
+                              self.plan.t["slot_pages"], scale,
+                              page_base=self.plan.t["slot_base"], out=out, lse=lse,
+                              workspace=workspace, status=self.status, stream=stream)
+
+    def _check_format(self, fmt):
+        if fmt.row_bytes != self.rb:
+            raise ValueError("rows of %d bytes in a runner of %d-byte rows"
+                             % (fmt.row_bytes, self.rb))
+
     def run(self, n_layers, stream=None):
         self.begin_batch(stream)
         for l in range(n_layers):

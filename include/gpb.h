@@ -101,8 +101,10 @@ typedef enum gpb_status {
   GPB_ECAPACITY = -4,  /* 1 + current pages > staging_cap_pages              */
   GPB_ERANGE = -5,     /* a row or element index would not fit in int32     */
   GPB_EHIP = -6,       /* the HIP runtime refused a launch                   */
-  GPB_ESCRATCH = -7    /* gpb_compose_layer_noalloc: the staging region would
+  GPB_ESCRATCH = -7,   /* gpb_compose_layer_noalloc: the staging region would
                           exceed GPB_SCRATCH_BYTES                           */
+  GPB_ENOMEM = -8      /* the host ran out of memory while a work list was
+                          made                                               */
 } gpb_status;
 
 /* Bits the kernels OR into the optional device status word (int32). */
@@ -553,6 +555,175 @@ int gpb_compose_layer_noalloc(void *d_dense, const gpb_sources *pools, int32_t n
                               int32_t n_slots, int32_t n_cur_pages, const void *d_cur_rows,
                               int32_t n_rows, int32_t page_rows, int32_t row_bytes,
                               int32_t *d_status, void *stream);
+
+/* ---- Making the rows, and reading them -------------------------------------
+ *
+ * The calls above move rows as opaque bytes.  The calls below know what is in
+ * them: gpb_row_append makes rows out of keys and values, rotates the keys by
+ * their positions and stores the rows in the paged pool (and token-packed, as
+ * the compose takes its current rows); gpb_attend_dense is the attention over
+ * the dense buffer the compose fills; gpb_attend_paged reads the pool itself
+ * through page tables, as a decode step does. */
+#define GPB_BF16 1
+#define GPB_FP16 2
+
+/* What a token row holds: n_kv_heads key heads of k_dim values one after
+ * another from the row's first byte, then n_kv_heads value heads of v_dim
+ * values.  With values_in_key = 1 the row is one key head (n_kv_heads = 1)
+ * whose first v_dim values are the value (a latent row).  row_bytes is the
+ * distance between rows, a multiple of 16, at least the payload; bytes past
+ * the payload belong to the caller and are neither read nor written.  k_dim
+ * and v_dim are multiples of 8, at most 1024. */
+typedef struct gpb_row_format {
+  int32_t dtype;                /* GPB_BF16 or GPB_FP16                        */
+  int32_t n_kv_heads;           /* 1 .. 1024                                   */
+  int32_t k_dim, v_dim;
+  int32_t values_in_key;        /* 0 or 1                                      */
+  int32_t row_bytes;
+} gpb_row_format;
+
+#define GPB_MAX_AXES 4
+
+/* One append.  Token t < n_rows: its key heads (d_k, element strides
+ * k_token_stride and k_head_stride, the values of a head contiguous) are
+ * rotated, rounded once to the row's type and stored with its value heads
+ * (d_v, the same way; unused with values_in_key) as one row, at pool row
+ * d_pool_locs[t] of d_pool and, when d_rows is not NULL, as row t of d_rows
+ * (n_rows contiguous rows of row_bytes, what the compose takes as d_cur_rows).
+ * d_pool_locs[t] = -1 stores no pool row (a padded entry of a batch); any
+ * other value outside [0, n_pool_rows) is skipped and
+ * GPB_STATUS_BAD_STAGING_ROW is ORed into *d_status.  Pool rows must not
+ * repeat.  d_pool may be NULL (n_pool_rows = 0): then only d_rows is written.
+ *
+ * When d_q is not NULL the n_q_heads query heads of k_dim values of every
+ * token are rotated the same way into d_q_out; d_q_out may be d_q with equal
+ * strides (in place), and must not overlap it otherwise.
+ *
+ * The rotation acts on values [rot_start, rot_start + rot_dim) of each key
+ * and query head: pair i < rot_dim / 2 is (2i, 2i + 1) with interleaved = 1,
+ * (i, i + rot_dim / 2) with interleaved = 0, and (x, y) becomes
+ * (x cos a - y sin a, y cos a + x sin a) with a = position * d_inv_freq[i].
+ * The position is that of the pair's axis: the first section[0] pairs take
+ * axis 0, the next section[1] pairs axis 1, and so on over n_axes axes, whose
+ * sections sum to rot_dim / 2; axis x of token t is
+ * d_positions[x * positions_stride + t] (any int32).  The angle is reduced in
+ * 64 bits, so far positions keep their fraction.  rot_dim = 0 rotates
+ * nothing.  rot_start is a multiple of 8, rot_dim a multiple of 16, at most
+ * 512.  Strides are in elements and multiples of 8, pointers to row data
+ * 16-byte aligned. */
+typedef struct gpb_append {
+  int32_t n_rows, n_q_heads;
+  const void *d_k, *d_v;
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  void *d_pool;
+  int64_t n_pool_rows;
+  const int32_t *d_pool_locs;   /* [n_rows]                                    */
+  void *d_rows;
+  const void *d_q;
+  void *d_q_out;
+  int64_t q_token_stride, q_head_stride, qo_token_stride, qo_head_stride;
+  int32_t rot_start, rot_dim, interleaved;
+  int32_t n_axes, section[GPB_MAX_AXES];
+  const float *d_inv_freq;      /* [rot_dim / 2]                               */
+  const int32_t *d_positions;   /* [n_axes] rows of n_rows                     */
+  int64_t positions_stride;
+} gpb_append;
+
+/* Append the rows in one launch.  Errors: GPB_EINVAL, GPB_EALIGN, GPB_ERANGE
+ * (n_pool_rows beyond INT32_MAX), GPB_EHIP. */
+int gpb_row_append(const gpb_row_format *format, const gpb_append *append,
+                   int32_t *d_status, void *stream);
+
+/* A batch to attend.  Request r has q_lens[r] queries, the last ones of its
+ * kv_lens[r] keys: query j of r is at position kv_lens[r] - q_lens[r] + j and
+ * sees key x if x <= its position and (window == 0, or position - x < window,
+ * or x < sinks).  A query with a negative position (more queries than keys)
+ * sees nothing: its output is 0 and its log-sum -infinity.  Queries are packed
+ * request after request.
+ *
+ * A group (first request, number of requests, shared keys) says that these
+ * consecutive requests begin with the same keys, held once, in the pages of
+ * the group's first request: the queries of the whole group read them
+ * together.  Groups are in ascending order and do not overlap; shared is at
+ * least 1, a multiple of page_rows, and no more than kv_lens - q_lens of any
+ * member (a query is never among the shared keys). */
+typedef struct gpb_attend_shape {
+  int32_t bs, n_heads;          /* n_heads a multiple of n_kv_heads            */
+  int32_t window, sinks;        /* window 0: every earlier key                 */
+  int32_t page_rows;            /* keys per page; any >= 1 for the dense call  */
+  const int32_t *h_q_lens, *h_kv_lens;  /* host [bs]                           */
+  int32_t n_groups;
+  const int32_t *h_groups;      /* host [3 * n_groups]                         */
+} gpb_attend_shape;
+
+/* What gpb_attend_plan_build found: sizes and places in the work list. */
+typedef struct gpb_attend_plan {
+  gpb_row_format format;
+  int32_t bs, n_heads, window, sinks, page_rows, n_groups;
+  int32_t n_tokens;             /* queries of the batch                        */
+  int32_t max_keys;             /* longest kv_lens                             */
+  int32_t n_items, n_joins, n_refs, n_partial_rows;
+  int32_t joins_at, refs_at, positions_at;  /* int32 offsets in the list       */
+  int32_t list_ints;            /* int32 values of the whole list              */
+  int64_t workspace_bytes;
+} gpb_attend_plan;
+
+/* Host only: cut the batch into work items (blocks of query rows over ranges
+ * of keys, long ranges cut further so that they fill the GPU, their parts
+ * joined by their log-sums in a second launch) and write the list to h_list,
+ * list_ints int32 values; with h_list NULL only *plan is filled.  The caller
+ * copies the list to the device.  The list depends on nothing but the
+ * format's heads, dimensions and the shape: one list serves every layer of a
+ * batch.  Formats attended: k_dim = v_dim = 64 or 128, or k_dim 576 with
+ * v_dim 512 in the key.  Errors: GPB_EINVAL, GPB_EALIGN, GPB_ERANGE (sizes
+ * past int32, or a list_ints smaller than the list), GPB_ENOMEM. */
+int gpb_attend_plan_build(const gpb_row_format *format, const gpb_attend_shape *shape,
+                          gpb_attend_plan *plan, int32_t *h_list, int64_t list_ints);
+
+/* Queries and results of one layer.  q: n_tokens tokens of n_heads heads of
+ * k_dim values of the format's type; out: the same of v_dim; element strides,
+ * multiples of 8 (out: of 4), pointers 16-byte aligned (out: 8).  Rows behind
+ * the last query are neither read nor written.  lse (optional): float,
+ * natural log of the sum of exp(score), [n_tokens][n_heads] contiguous.
+ * scale > 0 multiplies q.k.  out must not overlap any input. */
+typedef struct gpb_attend_io {
+  const void *d_q;
+  int64_t q_token_stride, q_head_stride;
+  void *d_out;
+  int64_t out_token_stride, out_head_stride;
+  float *d_lse;
+  float scale;
+} gpb_attend_io;
+
+/* Attention over the dense buffer of a compose: key x of request r is row
+ * d_k_bases[r] + x of d_dense (n_dense_rows rows of row_bytes; the plan's
+ * k_bases).  d_list is the device copy of the plan's list; d_workspace holds
+ * plan->workspace_bytes bytes, 16-byte aligned, and may be NULL when that is
+ * 0; calls that may overlap need a workspace each.  A plan with groups is
+ * refused (the dense buffer holds each request's keys apart).  A base that
+ * leads outside the buffer reads row 0 instead and ORs
+ * GPB_STATUS_BAD_DESCRIPTOR into *d_status; a list that is not the plan's
+ * ORs GPB_STATUS_BAD_PLAN_INPUT and its item is left out.  Errors: GPB_EINVAL,
+ * GPB_EALIGN, GPB_ERANGE, GPB_EHIP. */
+int gpb_attend_dense(const gpb_attend_plan *plan, const int32_t *d_list,
+                     const gpb_attend_io *io, const void *d_dense, int64_t n_dense_rows,
+                     const int32_t *d_k_bases, void *d_workspace, int64_t workspace_bytes,
+                     int32_t *d_status, void *stream);
+
+/* The same over the paged pool: key x of request r is row
+ * page * page_rows + x mod page_rows of d_pool with page the entry
+ * x div page_rows of the request's page list.  The list of request r starts at
+ * d_pages[d_page_base[r]], or at d_pages[r * pages_stride] when d_page_base is
+ * NULL; d_pages holds n_pages_listed entries (with d_page_base NULL, at least
+ * bs * pages_stride, and pages_stride covers the longest request).  The plan's
+ * slot_pages with slot_base are such a list.  A page outside the pool's whole
+ * pages, or an entry outside d_pages, reads page 0 instead and ORs
+ * GPB_STATUS_BAD_DESCRIPTOR into *d_status.  Errors as gpb_attend_dense. */
+int gpb_attend_paged(const gpb_attend_plan *plan, const int32_t *d_list,
+                     const gpb_attend_io *io, const void *d_pool, int64_t n_pool_rows,
+                     const int32_t *d_pages, int64_t n_pages_listed,
+                     const int32_t *d_page_base, int64_t pages_stride, void *d_workspace,
+                     int64_t workspace_bytes, int32_t *d_status, void *stream);
 
 /* Static, human-readable name of a gpb_status value. */
 const char *gpb_strerror(int status);

@@ -1,0 +1,580 @@
+"""The row append and the attentions on the GPU, against 64-bit references."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gather_plan_build_amd as gpb
+from rows_reference import attention, check, rotated, rotation_bound
+import workloads
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def fmt(which, dtype="bf16", hkv=2, **kw):
+    if which == "latent":
+        return gpb.RowFormat(dtype, 1, 576, 512, values_in_key=True, **kw)
+    return gpb.RowFormat(dtype, hkv, int(which), int(which), **kw)
+
+
+def normal(seed, *shape, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def ints(a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ append
+
+def row_values(f, k, v):
+    return torch.cat([k.flatten(1)] + ([] if v is None else [v.flatten(1)]), 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("which,hkv,hq,start,pairs,interleaved,sections", [
+    ("128", 2, 6, 0, 64, False, None),
+    ("128", 3, 3, 0, 64, False, [16, 24, 24]),
+    ("128", 1, 5, 32, 16, True, [1, 15]),
+    ("64", 4, 8, 0, 32, True, None),
+    ("64", 1, 2, 8, 8, False, [0, 3, 5, 0]),
+    ("latent", 1, 16, 512, 32, True, None),
+    ("latent", 1, 1, 0, 256, False, [100, 156]),
+    ("128", 2, 4, 0, 0, False, None),
+])
+@pytest.mark.parametrize("tokens", [1, 67])
+def test_append(dtype, which, hkv, hq, start, pairs, interleaved, sections, tokens):
+    f = fmt(which, dtype, hkv)
+    dt = f.dtype
+    # keys, values and queries are parts of one packed tensor, as a projection
+    # leaves them
+    parts = [hq, f.n_kv_heads] + ([] if f.values_in_key else [f.n_kv_heads])
+    packed = normal(1, tokens, sum(parts) * f.k_dim, dtype=dt)
+    q = packed[:, :hq * f.k_dim].unflatten(1, (hq, f.k_dim))
+    k = packed[:, hq * f.k_dim:(hq + hkv) * f.k_dim].unflatten(1, (hkv, f.k_dim))
+    v = None if f.values_in_key else packed[:, (hq + hkv) * f.k_dim:].unflatten(
+        1, (hkv, f.v_dim))
+    sec = sections or [pairs]
+    rng = np.random.default_rng(tokens)
+    pos = ints(rng.integers(-5, 2 ** 31 - 1, (len(sec), tokens)) // rng.integers(
+        1, 2 ** 20, (len(sec), tokens)))
+    freq = (10000.0 ** (-torch.arange(pairs, dtype=torch.float64) / max(pairs, 1))).float().cuda()
+    rot = gpb.Rotation(freq, start, interleaved, sec) if pairs else None
+    n = f.row_bytes // 2
+    pool = normal(2, 200, n, dtype=dt)
+    before = pool.clone()
+    locs = rng.permutation(200)[:tokens]
+    locs[tokens // 2] = -1                       # a padded entry
+    rows = torch.empty(tokens, n, dtype=dt, device="cuda")
+    q_out = torch.empty(tokens, hq, f.k_dim, dtype=dt, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gpb.row_append(f, k, v, pool, ints(locs), rot, pos, rows=rows, q=q, q_out=q_out,
+                   status=status)
+    assert int(status) == 0
+    kd, qd = (k.double(), q.double())
+    if pairs:
+        kd = rotated(k, pos, freq, start, interleaved, sec)
+        qd = rotated(q, pos, freq, start, interleaved, sec)
+    assert ((q_out.double() - qd).abs() <= rotation_bound(qd, q, dt)).all()
+    got_k = rows[:, :f.n_kv_heads * f.k_dim].view(tokens, -1, f.k_dim)
+    assert ((got_k.double() - kd).abs() <= rotation_bound(kd, k, dt)).all()
+    if v is not None:
+        assert torch.equal(rows[:, f.n_kv_heads * f.k_dim:], v.flatten(1))
+    # what is not rotated is copied
+    out = torch.ones(f.k_dim, dtype=torch.bool)
+    out[start:start + 2 * pairs] = False
+    assert torch.equal(got_k[..., out], k[..., out])
+    want = before.clone()
+    for t, at in enumerate(locs):
+        if at >= 0:
+            want[at] = rows[t]
+    assert torch.equal(pool, want)
+    # in place, and without a pool
+    q2 = q.clone()
+    rows2 = torch.zeros_like(rows)
+    gpb.row_append(f, k, v, None, None, rot, pos, rows=rows2, q=q2)
+    assert torch.equal(q2, q_out) and torch.equal(rows2, rows)
+    q3 = packed.clone()
+    part = q3[:, :hq * f.k_dim].unflatten(1, (hq, f.k_dim))
+    gpb.row_append(f, k, v, pool, ints(locs), rot, pos, q=part)
+    assert torch.equal(part, q_out)
+    assert torch.equal(q3[:, hq * f.k_dim:], packed[:, hq * f.k_dim:])
+
+
+def test_append_flags_rows_outside_the_pool_and_keeps_the_padding():
+    f = fmt("64", hkv=1, row_bytes=64 * 4 + 32)
+    k, v = normal(1, 4, 1, 64), normal(2, 4, 1, 64)
+    pool = normal(3, 8, f.row_bytes // 2)
+    before = pool.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gpb.row_append(f, k, v, pool, ints([7, 8, -1, 2]), status=status)
+    assert int(status) == gpb.STATUS_BAD_STAGING_ROW
+    want = before.clone()
+    for t, at in ((0, 7), (3, 2)):
+        want[at, :64], want[at, 64:128] = k[t, 0], v[t, 0]
+    assert torch.equal(pool, want)
+    status.zero_()
+    gpb.row_append(f, k, v, pool, ints([-2, 0, 1, 3]), status=status)
+    assert int(status) == gpb.STATUS_BAD_STAGING_ROW
+
+
+def test_append_past_4_gib_of_pool():
+    f = fmt("128", hkv=8)
+    n = (5 << 30) // f.row_bytes
+    pool = torch.zeros(n, f.row_bytes // 2, dtype=torch.bfloat16, device="cuda")
+    k, v = normal(1, 2, 8, 128), normal(2, 2, 8, 128)
+    gpb.row_append(f, k, v, pool, ints([n - 1, 0]))
+    assert torch.equal(pool[n - 1], row_values(f, k, v)[0])
+    assert torch.equal(pool[0], row_values(f, k, v)[1])
+    assert not pool[n - 2].any()
+
+
+# ------------------------------------------------------------------ attention
+
+def split(f, rows):
+    """[n, row values] -> keys, values."""
+    k = rows[:, :f.n_kv_heads * f.k_dim].reshape(-1, f.n_kv_heads, f.k_dim)
+    v = rows[:, :f.v_dim].reshape(-1, 1, f.v_dim) if f.values_in_key else \
+        rows[:, f.n_kv_heads * f.k_dim:f.n_kv_heads * (f.k_dim + f.v_dim)].reshape(
+            -1, f.n_kv_heads, f.v_dim)
+    return k, v
+
+
+class Batch:
+    """Rows of a batch, dense and paged, with stale rows all around them."""
+
+    def __init__(self, f, hq, q_lens, kv_lens, page=64, groups=(), seed=0, stale=float("nan")):
+        self.f, self.hq, self.q_lens, self.kv_lens, self.page = f, hq, q_lens, kv_lens, page
+        self.groups = list(groups)
+        dt, n = f.dtype, f.row_bytes // 2
+        rng = np.random.default_rng(seed)
+        self.q = normal(seed + 1, sum(q_lens) + 3, hq, f.k_dim, dtype=dt)
+        self.rows = [normal(seed + 10 + r, m, n, dtype=dt) for r, m in enumerate(kv_lens)]
+        for first, count, shared in self.groups:
+            for r in range(first + 1, first + count):
+                self.rows[r][:shared] = self.rows[first][:shared]
+        need = [-(-m // page) for m in kv_lens]
+        base = np.concatenate([[0], np.cumsum([p * page for p in need])])
+        self.dense = torch.full((int(base[-1]) + 5, n), stale, dtype=dt, device="cuda")
+        for b, x in zip(base, self.rows):
+            self.dense[b:b + len(x)] = x
+        self.k_bases = ints(base[:-1])
+        total = sum(need) + 4
+        ids = iter(rng.permutation(total))
+        self.pool = torch.full((total * page, n), stale, dtype=dt, device="cuda")
+        own = {r: (first, shared // page) for first, count, shared in self.groups
+               for r in range(first + 1, first + count)}
+        self.lists = []
+        for r, m in enumerate(kv_lens):
+            first, s = own.get(r, (None, 0))
+            pages = (self.lists[first][:s] if s else []) + [int(next(ids)) for _ in range(need[r] - s)]
+            self.lists.append(pages)
+            for i in range(s, need[r]):
+                part = self.rows[r][i * page:(i + 1) * page]
+                self.pool[pages[i] * page:pages[i] * page + len(part)] = part
+        width = max(need + [1]) + 2
+        self.table = ints([p + [-1] * (width - len(p)) for p in self.lists])
+
+    def want(self, window, sinks, scale):
+        parts, at = [], 0
+        for r, (n, m) in enumerate(zip(self.q_lens, self.kv_lens)):
+            pos = torch.arange(m - n, m, device="cuda")
+            k, v = split(self.f, self.rows[r])
+            parts.append(attention(self.q[at:at + n], k, v, pos, window, sinks, scale))
+            at += n
+        return [torch.cat([p[i] for p in parts]) for i in range(4)]
+
+    def plan(self, window=0, sinks=0, groups=True):
+        return gpb.AttendPlan(self.f, self.hq, self.q_lens, self.kv_lens, window=window,
+                              sinks=sinks, page_size=self.page,
+                              groups=self.groups if groups else ())
+
+    def check(self, window=0, sinks=0, dense=True):
+        T = sum(self.q_lens)
+        scale = 1.0 / math.sqrt(self.f.k_dim)
+        want = self.want(window, sinks, scale)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        plan = self.plan(window, sinks)
+        out, lse = gpb.attend_paged(plan, self.q, self.pool, self.table, scale, status=status)
+        assert out.shape == (T, self.hq, self.f.v_dim) and lse.shape == (T, self.hq)
+        check(out, lse, want)
+        assert int(status) == 0
+        if dense:
+            flat = self.plan(window, sinks, groups=False) if self.groups else plan
+            o2, l2 = gpb.attend_dense(flat, self.q, self.dense, self.k_bases, scale,
+                                      status=status)
+            check(o2, l2, want)
+            assert int(status) == 0
+            if not self.groups:      # the same work list: the same sums
+                assert torch.equal(out.view(torch.int16), o2.view(torch.int16))
+                assert torch.equal(lse, l2)
+        return out, lse
+
+
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 14), ("64", 1, 1), ("128", 2, 8),
+                                          ("128", 1, 7), ("latent", 1, 16), ("latent", 1, 3)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("q,kv", [
+    ([1], [1]),
+    ([1, 1, 1], [31, 32, 33]),
+    ([1, 1], [63, 65]),
+    ([3, 0, 5], [3, 17, 2]),                 # the last: three queries before any key
+    ([2, 1], [0, 5]),
+    ([129, 40], [129, 300]),
+    ([1, 2, 1], [777, 1300, 4]),
+])
+def test_lengths(which, hkv, hq, dtype, q, kv):
+    Batch(fmt(which, dtype, hkv), hq, q, kv).check()
+
+
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 14), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 3), (64, 64), (100, 0),
+                                          (300, 70), (5000, 4), (2, 5000)])
+def test_windows_and_first_tokens(which, hkv, hq, window, sinks):
+    Batch(fmt(which, "bf16", hkv), hq, [1, 90, 2, 200], [640, 500, 1000, 200]).check(window, sinks)
+
+
+@pytest.mark.parametrize("hq,hkv,which", [(128, 1, "latent"), (130, 1, "128"), (48, 1, "64"),
+                                          (200, 1, "latent"), (33, 3, "128"), (1, 1, "latent")])
+def test_heads(hq, hkv, which):
+    Batch(fmt(which, "bf16", hkv), hq, [2, 5, 1], [700, 5, 90]).check()
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 48, 100, 256])
+@pytest.mark.parametrize("which", ["64", "128", "latent"])
+def test_page_sizes(page, which):
+    Batch(fmt(which, "fp16", 1), 4, [1, 4, 70], [333, 65, 70], page=page).check(window=0)
+
+
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 16), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("q,kv,page,groups,window,sinks", [
+    ([1, 1, 1], [700, 650, 641], 64, [(0, 3, 640)], 0, 0),
+    ([2, 1, 3, 1], [330, 301, 420, 55], 10, [(0, 3, 300)], 0, 0),     # ends inside a tile
+    ([1] * 20, [1030 + 3 * r for r in range(20)], 64, [(0, 9, 1024), (9, 11, 512)], 0, 0),
+    ([1, 2, 1, 1], [1100, 1200, 1300, 2000], 50, [(0, 3, 1000)], 150, 5),
+    ([1, 0, 1], [200, 128, 129], 64, [(0, 3, 128)], 0, 0),
+    ([40, 30, 20], [168, 158, 148], 64, [(0, 3, 128)], 0, 0),
+    ([1, 1], [640, 640], 64, [(0, 1, 64), (1, 1, 64)], 0, 0),
+])
+def test_shared_prefixes(which, hkv, hq, q, kv, page, groups, window, sinks):
+    Batch(fmt(which, "bf16", hkv), hq, q, kv, page=page, groups=groups).check(window, sinks)
+
+
+@pytest.mark.parametrize("which", ["64", "128"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("q,kv,window,sinks", [
+    ([100], [230], 0, 0),            # a later token's values: seen by later queries alone
+    ([20], [500], 40, 2),            # values that left the window of some queries
+    ([1, 3], [70, 40], 0, 0),
+])
+def test_values_that_are_not_finite_reach_those_that_see_them_only(which, bad, q, kv, window,
+                                                                   sinks):
+    f = fmt(which, "bf16", 1)
+    b = Batch(f, 4, q, kv)
+    for r in range(len(kv)):
+        n = kv[r]
+        rows = [n - 1, max(0, n - q[r] // 2 - 1)]
+        if window:
+            rows.append(n - q[r] - window + 3)
+        for x in rows:
+            b.rows[r][x, f.k_dim + 5] = bad
+    base = b.k_bases.tolist()
+    for r, x in enumerate(b.rows):
+        b.dense[base[r]:base[r] + len(x)] = x
+        for i, p in enumerate(b.lists[r]):
+            part = x[i * 64:(i + 1) * 64]
+            b.pool[p * 64:p * 64 + len(part)] = part
+    b.check(window, sinks)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_latent_rows_that_are_not_finite(bad):
+    """A latent is key and value: a query that sees the row has no finite score,
+    the others must not notice."""
+    f = fmt("latent", "bf16")
+    b = Batch(f, 4, [60], [200])
+    b.rows[0][170, 7] = bad
+    b.dense[170] = b.rows[0][170]
+    scale = 0.05
+    plan = b.plan()
+    out, lse = gpb.attend_dense(plan, b.q, b.dense, b.k_bases, scale)
+    clean = b.rows[0].clone()
+    clean[170] = 0
+    k, v = split(f, clean)
+    pos = torch.arange(140, 200, device="cuda")
+    want = attention(b.q[:60], k, v, pos, 0, 0, scale)
+    check(out[:30], lse[:30], [w[:30] for w in want])
+    assert not torch.isfinite(out[30:, :, 7]).any()
+
+
+def test_large_scores_and_a_growing_maximum():
+    """Keys that grow along the sequence move the running maximum in every
+    tile; scores of some hundreds stay in range."""
+    for which in ("64", "128", "latent"):
+        f = fmt(which, "fp16", 1)
+        b = Batch(f, 4, [1, 70], [900, 300], stale=0.0)
+        for r, x in enumerate(b.rows):
+            grow = torch.linspace(0.1, 8.0, len(x), device="cuda")[:, None]
+            x[:, :f.k_dim] = (x[:, :f.k_dim] * grow).to(f.dtype)
+            base = int(b.k_bases[r])
+            b.dense[base:base + len(x)] = x
+            for i, p in enumerate(b.lists[r]):
+                part = x[i * 64:(i + 1) * 64]
+                b.pool[p * 64:p * 64 + len(part)] = part
+        b.check()
+
+
+def test_small_weights_in_half_precision():
+    """One key far above many others whose weights are below what fp16 holds of
+    a weight of 1: together they are a third of the sum."""
+    f = fmt("64", "fp16", 1)
+    n = 60000
+    b = Batch(f, 2, [1], [n], stale=0.0)
+    b.rows[0][:, :64] = 0
+    b.rows[0][100, :64] = 1
+    b.q[:] = 0
+    b.q[..., :64] = 11.7 / 8.0          # score 11.7 against 0: weights of 2^-17
+    b.rows[0][:, 64:] = 1.0
+    b.rows[0][100, 64:] = -1.0
+    for i, p in enumerate(b.lists[0]):
+        part = b.rows[0][i * 64:(i + 1) * 64]
+        b.pool[p * 64:p * 64 + len(part)] = part
+    b.dense[:n] = b.rows[0]
+    b.check()
+
+
+@pytest.mark.parametrize("which", ["128", "latent"])
+def test_strided_queries_and_results_and_rows_behind(which):
+    f = fmt(which, "bf16", 1)
+    hq, T = 4, 75
+    b = Batch(f, hq, [1, 74], [400, 90])
+    want = b.want(0, 0, 0.1)
+    plan = b.plan()
+    wide = normal(5, hq + 1, T + 9, f.k_dim + 8).transpose(0, 1)[:, :hq, :f.k_dim]
+    wide[:T] = b.q[:T]
+    assert not wide.is_contiguous()
+    full = torch.full((T + 9, hq, f.v_dim + 4), 7.0, dtype=f.dtype, device="cuda")
+    lse = torch.full((T + 9, hq), 7.0, device="cuda")
+    out, l2 = gpb.attend_paged(plan, wide, b.pool, b.table, 0.1, out=full[..., :f.v_dim], lse=lse)
+    assert l2 is lse
+    check(out[:T], lse[:T], want)
+    assert (full[T:] == 7).all() and (full[..., f.v_dim:] == 7).all() and (lse[T:] == 7).all()
+    only, none = gpb.attend_paged(plan, wide, b.pool, b.table, 0.1, lse=None)
+    assert none is None and torch.equal(only, out[:T])
+
+
+def test_page_lists_of_a_compose_plan_form():
+    f = fmt("128", "bf16", 2)
+    b = Batch(f, 4, [1, 2, 0, 9], [300, 70, 128, 9])
+    flat = ints([x for p in b.lists for x in p])
+    starts = ints(np.concatenate([[0], np.cumsum([len(p) for p in b.lists])[:-1]]))
+    plan = b.plan()
+    out, lse = gpb.attend_paged(plan, b.q, b.pool, flat, 0.1, page_base=starts)
+    check(out, lse, b.want(0, 0, 0.1))
+
+
+def test_pages_outside_the_pool_are_reported_and_touch_one_request():
+    f = fmt("64", "bf16", 1)
+    b = Batch(f, 2, [1, 1, 1], [200, 200, 200], stale=0.0)
+    plan = b.plan()
+    good, _ = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1)
+    for wrong in (-1, 10 ** 9, b.pool.shape[0] // 64, -2 ** 31):
+        t = b.table.clone()
+        t[1, 2] = wrong
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, _ = gpb.attend_paged(plan, b.q, b.pool, t, 0.1, status=status)
+        assert int(status) == gpb.STATUS_BAD_DESCRIPTOR
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+        assert torch.isfinite(out).all()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bases = ints([0, 2 ** 31 - 5, -9])
+    gpb.attend_dense(plan, b.q, b.dense, bases, 0.1, status=status)
+    assert int(status) == gpb.STATUS_BAD_DESCRIPTOR
+    status.zero_()
+    starts = ints([0, 2 ** 31 - 5, -9])
+    gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1, page_base=starts, status=status)
+    assert int(status) == gpb.STATUS_BAD_DESCRIPTOR
+
+
+def test_a_list_that_is_not_the_plans_is_reported():
+    f = fmt("64", "bf16", 1)
+    b = Batch(f, 2, [1, 1], [900, 2000], stale=0.0)
+    plan = b.plan()
+    assert plan.c.n_joins > 0
+    for fill in (-1, 2 ** 30, -2 ** 31):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        plan.list.fill_(fill)
+        gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1, status=status)
+        assert int(status) == 4          # GPB_STATUS_BAD_PLAN_INPUT
+
+
+def test_rows_past_4_gib():
+    """Pages at both ends of a pool of more than 4 GiB, and a dense buffer whose
+    last request starts past it."""
+    f = fmt("128", "bf16", 8)
+    pages = (5 << 30) // (64 * f.row_bytes)
+    pool = torch.zeros(pages * 64, f.row_bytes // 2, dtype=torch.bfloat16, device="cuda")
+    rows = normal(4, 150, f.row_bytes // 2)
+    ids = [pages - 1, 0, pages - 2]
+    for i, p in enumerate(ids):
+        part = rows[i * 64:(i + 1) * 64]
+        pool[p * 64:p * 64 + len(part)] = part
+    q = normal(5, 3, 16, 128)
+    plan = gpb.AttendPlan(f, 16, [3], [150])
+    k, v = split(f, rows)
+    want = attention(q, k, v, torch.arange(147, 150, device="cuda"), 0, 0, 0.1)
+    check(*gpb.attend_paged(plan, q, pool, ints([ids]), 0.1), want)
+    at = pages * 64 - 150
+    pool[at:] = rows
+    check(*gpb.attend_dense(plan, q, pool, ints([at]), 0.1), want)
+
+
+@pytest.mark.parametrize("which,hkv,hq", [("64", 8, 64), ("128", 2, 8), ("latent", 1, 16)])
+def test_results_do_not_change_from_run_to_run(which, hkv, hq):
+    b = Batch(fmt(which, "bf16", hkv), hq, [1] * 12, [2000 + 77 * r for r in range(12)],
+              groups=[(0, 7, 1920)])
+    plan = b.plan()
+    first = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1)
+    for _ in range(3):
+        again = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_other_streams_and_workspaces():
+    b = Batch(fmt("128", "bf16", 2), 8, [1, 1], [1500, 1800])
+    plan = b.plan()
+    want = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1, stream=s) for s in streams]
+    got.append(gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1, stream=streams[0].cuda_stream,
+                                workspace=plan.workspace()))
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    with pytest.raises(gpb.GpbError):
+        gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1,
+                         workspace=plan.workspace()[:-16])
+    with pytest.raises(ValueError):
+        gpb.attend_paged(plan, b.q.cpu(), b.pool, b.table, 0.1)
+    with pytest.raises(ValueError):
+        gpb.attend_paged(plan, b.q.half(), b.pool, b.table, 0.1)
+    with pytest.raises(ValueError):
+        gpb.attend_paged(plan, b.q[:1], b.pool, b.table, 0.1)
+
+
+def test_two_captured_graphs_of_a_decode_step():
+    """Append and attention captured twice, replayed in turn with eager work in
+    between; every replay equals the eager result."""
+    f = fmt("128", "bf16", 2)
+    b = Batch(f, 8, [1, 1], [1400, 900])
+    plan = b.plan()
+    freq = torch.full((64,), 0.01, device="cuda")
+    rot = gpb.Rotation(freq)
+    pos = ints([1399, 899])
+    locs = ints([b.lists[0][1399 // 64] * 64 + 1399 % 64, b.lists[1][899 // 64] * 64 + 899 % 64])
+    k, v, q = normal(1, 2, 2, 128), normal(2, 2, 2, 128), normal(3, 2, 8, 128)
+    turned = torch.empty_like(q)
+
+    def step(out, lse):
+        gpb.row_append(f, k, v, b.pool, locs, rot, pos, q=q, q_out=turned)
+        gpb.attend_paged(plan, turned, b.pool, b.table, 0.1, out=out, lse=lse)
+
+    def buffers():
+        return (torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(2, 8, device="cuda"))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*buffers())
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        bufs = buffers()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(*bufs)
+        graphs.append((g, bufs))
+    for turn in range(4):
+        k.copy_(normal(20 + turn, 2, 2, 128))
+        q.copy_(normal(30 + turn, 2, 8, 128))
+        eager = buffers()
+        step(*eager)
+        torch.cuda.synchronize()
+        for g, bufs in graphs:
+            bufs[0].zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(bufs[0], eager[0]) and torch.equal(bufs[1], eager[1])
+
+
+# ------------------------------------------------------------------ together
+
+def test_append_compose_attend_and_decode():
+    """A prefill through the runner (rows made, composed, attended densely and
+    from the pool) and a decode step after it, against the reference on the
+    rows read back."""
+    batch = workloads.make_batch("tiny")
+    f = fmt("latent")
+    pools, curs = workloads.make_values(batch, device="cuda")
+    r = gpb.ComposeRunner(gpb.BatchMeta.of(batch), pools, curs)
+    r.begin_batch()
+    T, hq, scale = r.T, 16, 0.07
+    k, q = normal(1, T, 1, 576), normal(2, T, hq, 576)
+    freq = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).float().cuda()
+    rot = gpb.Rotation(freq, start=512, interleaved=True)
+    c, P = batch.cur_tokens, batch.prefix_pages
+    pos = ints(np.concatenate([P[i] * 64 + np.arange(c[i]) for i in range(batch.bs)]))
+    turned = torch.empty_like(q)
+    r.append(0, f, k, None, rot, pos, q=q, q_out=turned)
+    kd = rotated(k, pos[None], freq, 512, True, [32])
+    rows = curs[0].view(torch.bfloat16)
+    assert ((rows.double()[:, None] - kd).abs() <= rotation_bound(kd, k, torch.bfloat16)).all()
+    r.layer(0)
+    plan = r.attend_plan(f, hq)
+    out, lse = r.attend(0, plan, turned, scale)
+    from_pool = r.attend_pool(0, plan, turned, scale)
+    assert int(r.status) == 0
+    assert torch.equal(out, from_pool[0]) and torch.equal(lse, from_pool[1])
+    dense = r.dense_of(0).view(torch.bfloat16)
+    at, want = 0, []
+    for i in range(batch.bs):
+        base, n = int(r.plan.t["k_bases"][i]), int(P[i]) * 64 + int(c[i])
+        keys, vals = split(f, dense[base:base + n])
+        want.append(attention(turned[at:at + int(c[i])], keys, vals,
+                              torch.arange(n - int(c[i]), n, device="cuda"), 0, 0, scale))
+        at += int(c[i])
+    check(out, lse, [torch.cat([w[j] for w in want]) for j in range(4)])
+
+    # one more token per request: the next row of its last page, or a new page
+    n = [int(P[i]) * 64 + int(c[i]) for i in range(batch.bs)]
+    used = set(r.plan.t["slot_pages"].tolist())
+    free = iter(x for x in range(1, batch.n_pool_pages) if x not in used)
+    base = r.plan.t["slot_base"].tolist()
+    pages = r.plan.t["slot_pages"].tolist()
+    lists = [pages[base[i]:base[i] + -(-n[i] // 64)] for i in range(batch.bs)]
+    for i in range(batch.bs):
+        if n[i] % 64 == 0:
+            lists[i].append(next(free))
+    width = max(len(x) for x in lists)
+    table = ints([x + [0] * (width - len(x)) for x in lists])
+    locs = ints([lists[i][n[i] // 64] * 64 + n[i] % 64 for i in range(batch.bs)])
+    k1, q1 = normal(8, batch.bs, 1, 576), normal(9, batch.bs, hq, 576)
+    gpb.row_append(f, k1, None, pools[0], locs, rot, ints(n), q=q1)
+    step = gpb.AttendPlan(f, hq, [1] * batch.bs, [x + 1 for x in n])
+    o1, l1 = gpb.attend_paged(step, q1, pools[0], table, scale)
+    pool = pools[0].view(torch.bfloat16)
+    want = []
+    for i in range(batch.bs):
+        idx = torch.tensor([p * 64 + j for p in lists[i] for j in range(64)], device="cuda")
+        keys, vals = split(f, pool[idx[:n[i] + 1]])
+        want.append(attention(q1[i:i + 1], keys, vals, ints([n[i]]), 0, 0, scale))
+    check(o1, l1, [torch.cat([w[j] for w in want]) for j in range(4)])
+    with pytest.raises(ValueError):
+        r.attend_plan(fmt("128"), 8)
