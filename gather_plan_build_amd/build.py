@@ -32,6 +32,10 @@ def command(out, defines=()):
            # the leading kernel arguments arrive in scalar registers at wave
            # launch instead of being read from the argument segment
            "-mllvm", "-amdgpu-kernarg-preload-count=16",
+           # matrix instructions keep their sums in vector registers: the
+           # attention kernels rescale them there, and the default carries
+           # them from accumulation registers and back for it
+           "-mllvm", "-amdgpu-mfma-vgpr-form",
            "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc")]
     cmd += ["-D" + d for d in defines]
     return cmd + ["-o", out] + sources()

@@ -72,6 +72,45 @@ __device__ __forceinline__ float other_half(float x, int half) {
   return __builtin_bit_cast(float, half ? r[0] : r[1]);
 }
 
+__device__ __forceinline__ int wave_id() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the same in every lane
+}
+
+// Direct loads of 16 bytes a lane into 1 KiB of LDS.  Written out because the
+// compiler, which cannot tell the two buffers of a tile apart, lets every LDS
+// read wait for all such loads; `loads_done` waits for them where the tile is
+// needed, and it and the barriers keep the LDS reads on their side.  The loads
+// have no register to write, so nothing of the compiler's can be overtaken.
+__device__ __forceinline__ uint32_t lds_at(lds_u8 *p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+}
+__device__ __forceinline__ void load_to_lds(const uint8_t *from, lds_u8 *to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds_at(to)), "v"(from));
+}
+// The lane's place is `lane16` ^ X bytes from base + off, which all lanes
+// share; the LDS place is `to` + TO.
+template <int X, int TO>
+__device__ __forceinline__ void load_to_lds(const uint8_t *base, uint64_t off, uint32_t lane16,
+                                            lds_u8 *to) {
+  uint32_t at;
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  asm volatile("s_add_u32 m0, %1, %7\n\ts_add_u32 s96, %2, %3\n\ts_addc_u32 s97, %4, %5\n\t"
+               "v_xor_b32 %0, %8, %6\n\tglobal_load_lds_dwordx4 %0, s[96:97]"
+               : "=&v"(at)
+               : "s"(lds_at(to)), "s"(static_cast<uint32_t>(b)), "s"(static_cast<uint32_t>(off)),
+                 "s"(static_cast<uint32_t>(b >> 32)), "s"(static_cast<uint32_t>(off >> 32)),
+                 "v"(lane16), "n"(TO), "n"(X)
+               : "s96", "s97", "scc");
+}
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Keeps instructions on their side.  The products below read their operands
+// some steps ahead, and with this after every step the compiler, which would
+// put each read next to its use to save registers, leaves them there.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // Place of chunk c of row r.  Rows of 128 bytes start half way through the
 // banks in turn: the row's bits 1 .. 3 move the chunk among eight.  Rows of
 // whole 256 bytes all start at bank 0: its bits 0 .. 3 move it among sixteen.
@@ -102,66 +141,95 @@ struct Attend {
   // 2^-31 of the largest keep a value, where fp16 alone ends at 2^-25
   static constexpr float SHIFT = sizeof(T) == 2 && __is_same(T, _Float16) ? 6.0f : 0.0f;
 
-  // Row of the rows array that holds key `key` of the item's request.
+  // The row that holds key `key` of the item's request, in two steps, so that
+  // a page number is asked for a tile earlier than it is needed: its load would
+  // otherwise be waited for behind the loads of a whole tile.
+  static __device__ __forceinline__ int in_range(const AttendItem &it, int key) {
+    return min(max(key, it.key_lo), it.key_hi - 1);
+  }
+  static __device__ __forceinline__ int page_of(const AttendArgs &a, const AttendItem &it,
+                                                int64_t base, int key) {
+    if (!a.pages) return 0;
+    const int64_t at = base + static_cast<unsigned>(in_range(it, key)) /
+                                  static_cast<unsigned>(a.page_rows);
+    return at >= 0 && at < a.n_listed ? a.pages[at] : -1;
+  }
   static __device__ __forceinline__ uint32_t row_of(const AttendArgs &a, const AttendItem &it,
-                                                    int64_t base, int key) {
-    key = min(max(key, it.key_lo), it.key_hi - 1);
-    int64_t row;
-    bool ok;
+                                                    int64_t base, int key, int page) {
+    key = in_range(it, key);
+    int64_t row = base + key, instead = 0;
     if (a.pages) {
-      const int idx = static_cast<unsigned>(key) / static_cast<unsigned>(a.page_rows);
-      const int64_t at = base + idx;
-      ok = at >= 0 && at < a.n_listed;
-      const int page = ok ? a.pages[at] : 0;
-      row = static_cast<int64_t>(page) * a.page_rows + (key - idx * a.page_rows);
-      ok = ok && row >= 0 && row < a.n_rows && page >= 0;
-      if (!ok) row = key - idx * a.page_rows;
-    } else {
-      row = base + key;
-      ok = row >= 0 && row < a.n_rows;
-      if (!ok) row = 0;
+      instead = static_cast<unsigned>(key) % static_cast<unsigned>(a.page_rows);
+      row = page < 0 ? -1 : static_cast<int64_t>(page) * a.page_rows + instead;
     }
-    if (!ok && a.status) atomicOr(a.status, GPB_STATUS_BAD_DESCRIPTOR);
+    if (row < 0 || row >= a.n_rows) {
+      row = instead;
+      if (a.status) atomicOr(a.status, GPB_STATUS_BAD_DESCRIPTOR);
+    }
     return static_cast<uint32_t>(row);
   }
 
-  // Direct loads of wave `wave` of WAVES into TILE LDS rows of B bytes from
-  // src: an instruction fills 64 chunks, a whole row or several.  Lane r of
-  // rid holds the source row of key r.
-  template <int B, int TILE, int WAVES>
-  static __device__ __forceinline__ void load_rows(const uint8_t *src, int row_bytes, uint32_t rid,
-                                                   lds_u8 *to, int wave, int lane) {
-    constexpr int C = B / 16, N = TILE * C / 64 / WAVES;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint8_t *from;
-      const int at = wave * N + i;  // instruction of the tile
-      if constexpr (C == 64) {
-        const uint32_t row = __builtin_amdgcn_readlane(rid, at);
-        from = src + static_cast<uint64_t>(row) * row_bytes;
-        from += static_cast<uint32_t>((lane ^ swizzle<B>(at)) * 16);
-      } else {
-        const int r = at * (64 / C) + lane / C;
-        const uint32_t row = __shfl(rid, r, 64);
-        from = src + static_cast<uint64_t>(row) * row_bytes + ((lane % C) ^ swizzle<B>(r)) * 16;
-      }
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void *)(from),
-          (__attribute__((address_space(3))) void *)(to + at * 1024), 16, 0, 0);
-    }
+  static __device__ __forceinline__ uint32_t whole_row(const AttendArgs &a, const AttendItem &it,
+                                                       int64_t base, int key) {
+    return row_of(a, it, base, key, page_of(a, it, base, key));
   }
 
-  // One tile of TILE keys: WAVES waves share the load.
+  // The loads of one tile of TILE keys, WAVES waves sharing them, each TILE /
+  // WAVES keys.  Lane r of `row` holds the source row of the wave's key r.
+  // Instruction i of the wave, of N, goes out by issue<i>: the products of one
+  // tile are under way meanwhile.
   template <int TILE, int WAVES>
-  static __device__ __forceinline__ void load_tile(const AttendArgs &a, const AttendItem &it,
-                                                   uint32_t rid, lds_u8 *to, int wave, int lane) {
-    const uint8_t *k = a.rows + static_cast<int64_t>(it.kv_head) * KB;
-    const uint8_t *v = IN_KEY ? k + VB
-                              : a.rows + static_cast<int64_t>(a.hkv) * KB +
-                                    static_cast<int64_t>(it.kv_head) * VB;
-    load_rows<R0, TILE, WAVES>(k, a.row_bytes, rid, to, wave, lane);
-    load_rows<R1, TILE, WAVES>(v, a.row_bytes, rid, to + TILE * R0, wave, lane);
-  }
+  struct Loader {
+    static constexpr int N0 = TILE * R0 / 1024 / WAVES, N1 = TILE * R1 / 1024 / WAVES;
+    static constexpr int N = N0 + N1;
+    const uint8_t *src[2];  // of the rows of R0 and of R1 bytes
+    lds_u8 *to;             // of the wave's first load
+    uint64_t off;           // of the lane's row
+    int wave, lane;
+
+    __device__ __forceinline__ Loader(const AttendArgs &a, const AttendItem &it, uint32_t row,
+                                      lds_u8 *tile, int wave, int lane)
+        : to(tile), off(static_cast<uint64_t>(row) * static_cast<uint32_t>(a.row_bytes)),
+          wave(wave), lane(lane) {
+      src[0] = a.rows + static_cast<int64_t>(it.kv_head) * KB;
+      src[1] = IN_KEY ? src[0] + VB
+                      : a.rows + static_cast<int64_t>(a.hkv) * KB +
+                            static_cast<int64_t>(it.kv_head) * VB;
+    }
+    template <int I>
+    __device__ __forceinline__ void issue() const {
+      if constexpr (I < N) {
+        constexpr int B = I < N0 ? R0 : R1, C = B / 16, J = I < N0 ? I : I - N0;
+        const int first = wave * (I < N0 ? N0 : N1);  // instruction of the tile
+        lds_u8 *at = to + (I < N0 ? 0 : TILE * R0) + first * 1024;
+        if constexpr (C == 64) {  // a row each, 16 a wave: its swizzle is that of J
+          const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(off), J);
+          const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(off >> 32), J);
+          load_to_lds<swizzle<B>(J) * 16, J * 1024>(
+              src[0], lo | static_cast<uint64_t>(hi) << 32, lane * 16, at);
+        } else {
+          const int r = J * (64 / C) + lane / C;  // and so is the swizzle of key r
+          const uint32_t lo = __shfl(static_cast<uint32_t>(off), r, 64);
+          const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), r, 64);
+          load_to_lds(src[I < N0 ? 0 : 1] + (lo | static_cast<uint64_t>(hi) << 32) +
+                          ((lane % C) ^ swizzle<B>(r)) * 16,
+                      at + J * 1024);
+        }
+      }
+    }
+    template <int I = 0>
+    __device__ __forceinline__ void all() const {
+      if constexpr (I < N) {
+        issue<I>();
+        all<I + 1>();
+      }
+    }
+  };
+  // In place of a Loader where no tile follows.
+  struct NoLoader {
+    template <int I>
+    __device__ __forceinline__ void issue() const {}
+  };
 
   struct State {
     f32x16 o[NT];
@@ -212,51 +280,81 @@ struct Attend {
            (a.window == 0 || pos - key < a.window || key < a.sinks);
   }
 
-  // Scores of the 32 keys in LDS rows row0 .. of a tile of TILE and the lane's
-  // query row, in units of log2, keys that it does not see at -infinity.
+  // 16 values of the 32 keys in LDS rows row0 .. of a tile of TILE.
   template <int TILE>
-  static __device__ __forceinline__ f32x16 scores(const AttendArgs &a, const AttendItem &it,
-                                                  const x8 *q, const lds_u8 *tile, int row0,
-                                                  const Places &w, int key0, bool whole, int pos,
-                                                  int half) {
+  static __device__ __forceinline__ x8 key_operand(const lds_u8 *tile, int row0, const Places &w,
+                                                   int d) {
     typedef __attribute__((address_space(3))) x8 lds8;
-    f32x16 s = {};
-#pragma unroll
-    for (int d = 0; d < DK / 16; ++d) {
-      constexpr int D0 = R0 / 32;  // steps in the rows of R0 bytes
-      const lds_u8 *at;
-      if (d < D0)
-        at = tile + row0 * R0 + w.k0[d % (G0 / 2)] + d / (G0 / 2) * G0 * 16;
-      else
-        at = tile + TILE * R0 + row0 * R1 + w.k1[IN_KEY ? (d - D0) % (G1 / 2) : 0] +
-             (d - D0) / (G1 / 2) * G1 * 16;
-      s = mma<T>(*(const lds8 *)at, q[d], s);
-    }
-    s *= a.c;
-    if (!whole) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = key0 + 8 * (i / 4) + 4 * half + i % 4;
-        s[i] = sees(a, it, pos, key) ? s[i] : -INFINITY;
-      }
-    }
-    return s;
+    constexpr int D0 = R0 / 32;  // steps in the rows of R0 bytes
+    if (d < D0)
+      return *(const lds8 *)(tile + row0 * R0 + w.k0[d % (G0 / 2)] + d / (G0 / 2) * G0 * 16);
+    return *(const lds8 *)(tile + TILE * R0 + row0 * R1 +
+                           w.k1[IN_KEY ? (d - D0) % (G1 / 2) : 0] +
+                           (d - D0) / (G1 / 2) * G1 * 16);
   }
 
-  static __device__ __forceinline__ float largest(f32x16 s) {
+  // q.k of the 32 keys in LDS rows row0 .. of a tile of TILE and the lane's
+  // query row; the next tile's loads FIRST .. go out between the steps.
+  template <int TILE, int FIRST, typename L>
+  static __device__ __forceinline__ f32x16 products(const x8 *q, const lds_u8 *tile, int row0,
+                                                    const Places &w, const L &next) {
+    constexpr int AHEAD = DK / 16 < 6 ? DK / 16 : 6;
+    x8 k[AHEAD];
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) k[d] = key_operand<TILE>(tile, row0, w, d);
+    f32x16 s = {};
+    product_steps<TILE, FIRST, 0, AHEAD>(q, tile, row0, w, next, k, s);
+    return s;
+  }
+  template <int TILE, int FIRST, int D, int AHEAD, typename L>
+  static __device__ __forceinline__ void product_steps(const x8 *q, const lds_u8 *tile, int row0,
+                                                       const Places &w, const L &next, x8 *k,
+                                                       f32x16 &s) {
+    if constexpr (D < DK / 16) {
+      s = mma<T>(k[D % AHEAD], q[D], s);
+      if constexpr (D + AHEAD < DK / 16)
+        k[D % AHEAD] = key_operand<TILE>(tile, row0, w, D + AHEAD);
+      next.template issue<FIRST + D>();
+      in_order();
+      product_steps<TILE, FIRST, D + 1, AHEAD>(q, tile, row0, w, next, k, s);
+    }
+  }
+
+  // The keys that the row does not see go to -infinity.
+  static __device__ __forceinline__ void mask(const AttendArgs &a, const AttendItem &it, int key0,
+                                              int pos, int half, f32x16 &s) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int key = key0 + 8 * (i / 4) + 4 * half + i % 4;
+      s[i] = sees(a, it, pos, key) ? s[i] : -INFINITY;
+    }
+  }
+
+  static __device__ __forceinline__ float largest(const f32x16 &s) {
     float top = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
     return top;
   }
 
-  // Weights 2^(s - ref) of 32 keys, as two right operands of the second
+  // The m to weigh by, given the largest score of new keys: m stays until it is
+  // passed by more than 8, so that the sums are rescaled now and then and not
+  // with every new maximum.  Weights then reach 2^8 (fp16: 2^14).
+  static __device__ __forceinline__ float next_m(float m, float top) {
+    return top > m + 8.0f ? top : m;
+  }
+  static __device__ __forceinline__ float finite_m(float m) {
+    return m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 0
+  }
+
+  // Weights 2^(c s - m) of 32 keys, as two right operands of the second
   // product; returns their sum.
-  static __device__ __forceinline__ float weights(f32x16 s, float ref, x8 *p) {
+  static __device__ __forceinline__ float weights(const f32x16 &s, float c, float m, x8 *p) {
     float sum = 0.0f;
+    const float ref = finite_m(m) - SHIFT;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float x = __builtin_amdgcn_exp2f(s[i] - (ref - SHIFT));
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ref));
       sum += x;
       p[i / 8][i % 8] = static_cast<T>(x);
     }
@@ -268,11 +366,18 @@ struct Attend {
   template <int NP, int N>
   static __device__ __forceinline__ void add_values(const x8 *p, const lds_u8 *v, const Places &w,
                                                     int t0, f32x16 *o) {
+    constexpr int ALL = NP * N, AHEAD = 4;
+    const lds_u8 *at = v + t0 / (VG / 4) * VG * 16;
+    x8 x[AHEAD];
 #pragma unroll
-    for (int b = 0; b < NP; ++b)
+    for (int i = 0; i < AHEAD && i < ALL; ++i) x[i] = value_operand(at, w, i / N * 16, i % N);
 #pragma unroll
-      for (int t = 0; t < N; ++t)
-        o[t] = mma<T>(value_operand(v + t0 / (VG / 4) * VG * 16, w, 16 * b, t), p[b], o[t]);
+    for (int i = 0; i < ALL; ++i) {
+      o[i % N] = mma<T>(x[i % AHEAD], p[i / N], o[i % N]);
+      if (i + AHEAD < ALL)
+        x[i % AHEAD] = value_operand(at, w, (i + AHEAD) / N * 16, (i + AHEAD) % N);
+      in_order();
+    }
   }
 
   // A key that one row sees and another does not has weight 0 in the other's
@@ -301,30 +406,35 @@ struct Attend {
   static __device__ __forceinline__ void rescale(f32x16 *o, float *l, float f) {
     *l *= f;
 #pragma unroll
-    for (int t = 0; t < N; ++t) o[t] *= f;
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[t][i] *= f;
   }
 
   // A tile of 32 * NB keys, the first at position key0.
-  template <int NB>
+  template <int NB, typename L>
   static __device__ __forceinline__ void keys(const AttendArgs &a, const AttendItem &it,
                                               const x8 *q, const lds_u8 *tile, const Places &w,
-                                              int key0, bool whole, int pos, State &st, int lane) {
+                                              int key0, bool whole, int pos, State &st, int lane,
+                                              const L &next) {
     f32x16 s[NB];
-    float top = -INFINITY;
+    s[0] = products<32 * NB, 0>(q, tile, 0, w, next);
+    if constexpr (NB == 2) s[1] = products<32 * NB, DK / 16>(q, tile, 32, w, next);
+    if (!whole) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      s[b] = scores<32 * NB>(a, it, q, tile, 32 * b, w, key0 + 32 * b, whole, pos, lane >> 5);
-      top = fmaxf(top, largest(s[b]));
+      for (int b = 0; b < NB; ++b) mask(a, it, key0 + 32 * b, pos, lane >> 5, s[b]);
     }
-    const float m = fmaxf(st.m, fmaxf(top, other_half(top, lane >> 5)));
-    const float ref = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 0
+    float top = largest(s[0]);
+    if constexpr (NB == 2) top = fmaxf(top, largest(s[1]));
+    top *= a.c;
+    const float m = next_m(st.m, fmaxf(top, other_half(top, lane >> 5)));
     if (__any(m > st.m)) {
-      rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(st.m - ref));
+      rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(st.m - finite_m(m)));
       st.m = m;
     }
     x8 p[2 * NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) st.l += weights(s[b], ref, p + 2 * b);
+    for (int b = 0; b < NB; ++b) st.l += weights(s[b], a.c, m, p + 2 * b);
     add_values<2 * NB, NT>(p, tile + 32 * NB * R0, w, 0, st.o);
   }
 
@@ -338,6 +448,13 @@ struct Attend {
     return (v < it.n_first ? it.tile0 + v : it.tile1 + v - it.n_first) * tile;
   }
 
+  // The key of the lane's load for wide tile v.  A tile's loads go out with the
+  // products of the one before; where no tile follows they all read one row,
+  // which costs less than a second form of the products without them.
+  static __device__ __forceinline__ int key_after(const AttendItem &it, int v, int mine) {
+    return v < it.n_tiles ? first_key(it, v, kWideTile) + mine : it.key_lo;
+  }
+
   // The lane's query row: its token, its head, its queries in registers.
   static __device__ __forceinline__ void load_queries(const AttendArgs &a, const AttendItem &it,
                                                       int row, int half, x8 *q, int *pos) {
@@ -349,6 +466,16 @@ struct Attend {
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d)
       q[d] = has ? *reinterpret_cast<const x8 *>(src + d * 16) : x8{};
+    // arrived before the tiles' loads start: a wait for them later would wait
+    // for those too
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) {
+      // (a latent's go to accumulation registers, from which a matrix
+      // instruction takes an operand as well: the sums need the others)
+      if (IN_KEY) asm volatile("" : "+a"(q[d]));
+      else asm volatile("" : "+v"(q[d]));
+    }
+    asm volatile("" : "+v"(*pos));
   }
 
   // What turns a row's sums and its m and l into results; a row that sees
@@ -443,7 +570,7 @@ struct Attend {
         if (whole_tile(a, it, key0, tile)) continue;
         bool odd = false;
         for (int x = 0; x < tile; ++x) {
-          const T *val = vals + row_of(a, it, base, key0 + x) * row_values;
+          const T *val = vals + whole_row(a, it, base, key0 + x) * row_values;
           for (int e = lane; e < DV; e += 64)
             odd |= not_finite(__builtin_bit_cast(uint16_t, val[e]));
         }
@@ -451,7 +578,7 @@ struct Attend {
         for (int x = 0; x < tile; ++x) {
           const int key = key0 + x;
           if (!sees(a, it, pos, key)) continue;
-          const int64_t at = row_of(a, it, base, key) * row_values;
+          const int64_t at = whole_row(a, it, base, key) * row_values;
           float s = 0.0f;
 #pragma unroll
           for (int e = 0; e < PK; ++e) s += q[e] * static_cast<float>(keys[at + e * 64 + lane]);
@@ -487,8 +614,9 @@ struct Attend {
   // Four waves, 32 rows each, tiles of 64 keys in two LDS buffers.
   static __device__ __forceinline__ void wide(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int row = wave * 32 + (lane & 31), half = lane >> 5;
+    const int mine16 = wave * 16 + (lane & 15);  // the key whose row the lane finds
     constexpr int BUF = kWideTile * ROW;
     x8 q[DK / 16];
     int pos;
@@ -503,26 +631,27 @@ struct Attend {
     bool left = false;  // a tile is left to `careful`
     if (it.n_tiles > 0) {
       const int64_t base = request_base(a, it.req);
-      uint32_t rid = row_of(a, it, base, first_key(it, 0, kWideTile) + lane);
-      load_tile<kWideTile, 4>(a, it, rid, lds, wave, lane);
-      rid = row_of(a, it, base, first_key(it, min(1, it.n_tiles - 1), kWideTile) + lane);
+      int next = first_key(it, 0, kWideTile) + mine16, page = page_of(a, it, base, next);
+      Loader<kWideTile, 4>(a, it, row_of(a, it, base, next, page), lds, wave, lane).all();
+      next = key_after(it, 1, mine16);
+      page = page_of(a, it, base, next);
       for (int v = 0; v < it.n_tiles; ++v) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        loads_done();
         __syncthreads();
         lds_u8 *now = lds + (v & 1) * BUF;
-        if (v + 1 < it.n_tiles) {
-          load_tile<kWideTile, 4>(a, it, rid, lds + (~v & 1) * BUF, wave, lane);
-          if (v + 2 < it.n_tiles)
-            rid = row_of(a, it, base, first_key(it, v + 2, kWideTile) + lane);
-        }
         const int key0 = first_key(it, v, kWideTile);
         const bool whole = whole_tile(a, it, key0, kWideTile);
-        if (!whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256))) {
-          left = true;
-          continue;
-        }
-        keys<2>(a, it, q, now, w, key0, whole, pos, st, lane);
+        const bool odd =
+            !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
+        left |= odd;
+        const Loader<kWideTile, 4> load(a, it, row_of(a, it, base, next, page),
+                                        lds + (~v & 1) * BUF, wave, lane);
+        next = key_after(it, v + 2, mine16);
+        page = page_of(a, it, base, next);
+        if (odd) load.all();
+        else keys<2>(a, it, q, now, w, key0, whole, pos, st, lane, load);
       }
+      loads_done();
     }
     const float l = st.l + other_half(st.l, half);
     if (__syncthreads_or(left)) careful(a, it, lds, row, half, st, l, 0, true);
@@ -538,9 +667,10 @@ struct Attend {
   // the weights are brought to the larger one before they are used.
   static __device__ __forceinline__ void latent(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int part = wave & 1, half = lane >> 5;
     const int row = (wave >> 1) * 32 + (lane & 31);
+    const int mine16 = wave * 16 + (lane & 15);  // the key whose row the lane finds
     const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
     constexpr int BUF = kWideTile * ROW;
     lds_u8 *mine = lds + TILES_LDS + wave * WAVE_XCHG;
@@ -560,34 +690,38 @@ struct Attend {
     bool left = false;  // a tile is left to `careful`
     if (it.n_tiles > 0) {
       const int64_t base = request_base(a, it.req);
-      uint32_t rid = row_of(a, it, base, first_key(it, 0, kWideTile) + lane);
-      load_tile<kWideTile, 4>(a, it, rid, lds, wave, lane);
-      rid = row_of(a, it, base, first_key(it, min(1, it.n_tiles - 1), kWideTile) + lane);
+      int next = first_key(it, 0, kWideTile) + mine16, page = page_of(a, it, base, next);
+      Loader<kWideTile, 4>(a, it, row_of(a, it, base, next, page), lds, wave, lane).all();
+      next = key_after(it, 1, mine16);
+      page = page_of(a, it, base, next);
       for (int v = 0; v < it.n_tiles; ++v) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        loads_done();
         __syncthreads();
         lds_u8 *now = lds + (v & 1) * BUF;
-        if (v + 1 < it.n_tiles) {
-          load_tile<kWideTile, 4>(a, it, rid, lds + (~v & 1) * BUF, wave, lane);
-          if (v + 2 < it.n_tiles)
-            rid = row_of(a, it, base, first_key(it, v + 2, kWideTile) + lane);
-        }
         const int key0 = first_key(it, v, kWideTile);
         const bool whole = whole_tile(a, it, key0, kWideTile);
-        if (!whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256))) {
-          left = true;
+        const bool odd =
+            !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
+        left |= odd;
+        const Loader<kWideTile, 4> load(a, it, row_of(a, it, base, next, page),
+                                        lds + (~v & 1) * BUF, wave, lane);
+        next = key_after(it, v + 2, mine16);
+        page = page_of(a, it, base, next);
+        if (odd) {
+          load.all();
           continue;
         }
+        f32x16 s = {};
+        if (idle) load.all();
+        else s = products<kWideTile, 0>(q, now, 32 * part, w, load);
         x8 p[2], p2[2];
         float m = -INFINITY;
         if (!idle) {
-          const f32x16 s = scores<kWideTile>(a, it, q, now, 32 * part, w, key0 + 32 * part, whole,
-                                             pos, half);
-          const float top = largest(s);
-          m = fmaxf(st.m, fmaxf(top, other_half(top, half)));
-          const float sum = weights(s, m == -INFINITY ? 0.0f : m, p);
-          if (__any(m > st.m)) st.l *= __builtin_amdgcn_exp2f(st.m - (m == -INFINITY ? 0.0f : m));
-          st.l += sum;
+          if (!whole) mask(a, it, key0 + 32 * part, pos, half, s);
+          const float top = largest(s) * a.c;
+          m = next_m(st.m, fmaxf(top, other_half(top, half)));
+          if (__any(m > st.m)) st.l *= __builtin_amdgcn_exp2f(st.m - finite_m(m));
+          st.l += weights(s, a.c, m, p);
           ((lds8 *)mine)[lane] = p[0];
           ((lds8 *)mine)[64 + lane] = p[1];
           if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
@@ -597,7 +731,7 @@ struct Attend {
           p2[0] = ((const lds8 *)theirs)[lane];
           p2[1] = ((const lds8 *)theirs)[64 + lane];
           const float m2 = ((const lds_float *)(theirs + 2048))[lane & 31];
-          const float both = fmaxf(m, m2), ref = both == -INFINITY ? 0.0f : both;
+          const float both = fmaxf(m, m2), ref = finite_m(both);
           if (__any(m != m2)) {
             const float f = __builtin_amdgcn_exp2f(m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
             st.l *= f;
@@ -618,6 +752,7 @@ struct Attend {
           add_values<2, NT>(p2, now + 32 * (1 - part) * VS, w, part * NT, st.o);
         }
       }
+      loads_done();
     }
     // each wave has summed the weights of its own keys
     float l = st.l + other_half(st.l, half);
@@ -633,7 +768,7 @@ struct Attend {
   // their sums meet in LDS at the end, the waves in order.
   static __device__ __forceinline__ void narrow(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int row = lane & 31, half = lane >> 5;
     x8 q[DK / 16];
     int pos;
@@ -649,16 +784,17 @@ struct Attend {
     lds_u8 *own = lds + wave * kNarrowTile * ROW;
     if (wave < it.n_tiles) {
       const int64_t base = request_base(a, it.req);
-      uint32_t rid = row_of(a, it, base, first_key(it, wave, kNarrowTile) + (lane & 31));
+      int next = first_key(it, wave, kNarrowTile) + (lane & 31), page = page_of(a, it, base, next);
       for (int v = wave; v < it.n_tiles; v += 4) {
-        load_tile<kNarrowTile, 1>(a, it, rid, own, 0, lane);
-        if (v + 4 < it.n_tiles)
-          rid = row_of(a, it, base, first_key(it, v + 4, kNarrowTile) + (lane & 31));
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint32_t row = row_of(a, it, base, next, page);
+        next = first_key(it, min(v + 4, it.n_tiles - 1), kNarrowTile) + (lane & 31);
+        page = page_of(a, it, base, next);
+        Loader<kNarrowTile, 1>(a, it, row, own, 0, lane).all();
+        loads_done();
         const int key0 = first_key(it, v, kNarrowTile);
         const bool whole = whole_tile(a, it, key0, kNarrowTile);
         if (!whole && __any(odd_values<kNarrowTile>(own, lane, 64))) left = true;
-        else keys<1>(a, it, q, own, w, key0, whole, pos, st, lane);
+        else keys<1>(a, it, q, own, w, key0, whole, pos, st, lane, NoLoader());
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
     }
@@ -736,7 +872,7 @@ __global__ __launch_bounds__(256, IN_KEY ? 1 : 2) void k_attend(AttendArgs a) {
 template <typename T, int DV>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   const AttendJoin j = reinterpret_cast<const AttendJoin *>(a.list + a.joins_at)[blockIdx.x];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   constexpr int PER = DV / 64;
   bool ok = j.row0 >= 0 && j.n_rows >= 1 && j.n_rows <= kNarrowRows &&
             static_cast<int64_t>(j.row0) + j.n_rows <= static_cast<int64_t>(a.n_tokens) * a.G &&
