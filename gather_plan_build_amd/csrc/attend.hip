@@ -16,13 +16,13 @@
 // transposing LDS reads (ds_read_b64_tr_b16) of four keys each.
 //
 // Keys and values go to LDS by direct loads, 16 bytes a lane, a row's 16-byte
-// chunks permuted within the row (swizzle) so that neither the reads of K (16
-// rows at one chunk) nor those of V (4 rows at 4 chunks) meet in a bank: the
+// chunks permuted within the row (swizzle) so that reads do not meet in a bank: the
 // direct load fixes the LDS place of a lane, so the lane picks its source.
 //
 // Scores, m, l and the sums are fp32; P is rounded to the row's type for the
 // second product (its errors, at most half a step each, average out; l sums
 // the unrounded ones).
+#include <algorithm>
 #include <cmath>
 
 #include "attend.h"
@@ -45,13 +45,26 @@ struct AttendArgs {
   float *sums, *ml;         // workspace: sums [partial rows][DV], (m, l) pairs
   int32_t *status;
   float c;                  // scale * log2(e)
-  int32_t row_bytes, page_rows, window, sinks;
+  int32_t row_bytes, page_rows, page_shift, n_pages, window, sinks;
   int32_t G, hkv, n_heads, n_tokens, bs, max_keys;
   int32_t n_items, n_joins, n_refs, n_partial_rows, joins_at, refs_at, positions_at;
 };
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// The same in every lane: arguments of a function that is not inlined arrive in
+// vector registers.
+template <typename V>
+__device__ __forceinline__ V uniform(V v) {
+  struct Words {
+    int w[sizeof(V) / 4];
+  };
+  Words x = __builtin_bit_cast(Words, v);
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(V) / 4; ++i) x.w[i] = __builtin_amdgcn_readfirstlane(x.w[i]);
+  return __builtin_bit_cast(V, x);
+}
 
 template <typename T>
 __device__ __forceinline__ f32x16 mma(typename Vec<T>::x8 a, typename Vec<T>::x8 b, f32x16 c);
@@ -89,6 +102,12 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *from, lds_u8 *to) {
                :
                : "s"(lds_at(to)), "v"(from));
 }
+// Four bytes a lane, 256 bytes in all.
+__device__ __forceinline__ void load4_to_lds(const int32_t *from, lds_u8 *to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds_at(to)), "v"(from));
+}
 // The lane's place is `lane16` ^ X bytes from base + off, which all lanes
 // share; the LDS place is `to` + TO.
 template <int X, int TO>
@@ -104,21 +123,48 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *base, uint64_t off, u
                  "v"(lane16), "n"(TO), "n"(X)
                : "s96", "s97", "scc");
 }
-__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the newest LEFT of the wave's loads have arrived.
+template <int LEFT = 0>
+__device__ __forceinline__ void loads_done() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+}
 
 // Keeps instructions on their side.  The products below read their operands
 // some steps ahead, and with this after every step the compiler, which would
 // put each read next to its use to save registers, leaves them there.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
-// Place of chunk c of row r.  Rows of 128 bytes start half way through the
-// banks in turn: the row's bits 1 .. 3 move the chunk among eight.  Rows of
-// whole 256 bytes all start at bank 0: its bits 0 .. 3 move it among sixteen.
-// The lowest of those bits go to the chunk bits in which the four rows of a
-// transposing read have to differ.
+// A row's 16-byte chunks are moved within groups so that the LDS reads meet in
+// no bank: of a key operand, 16 rows at one chunk; of a value operand, 16 lanes
+// at a time, four rows at 32 bytes, which have to fall into different 32 bytes
+// of 128 (and the next 16 lanes' into the other 128).  Rows of whole 256 bytes
+// all start at bank 0: the chunk's bits are turned (`turned`) so that those two
+// columns lie 128 bytes apart, and the row's four low bits added.  Rows of 128
+// bytes start half way through the banks in turn and take three.  Measured on
+// the value reads: 130 and 149 bytes a clock, 89 with the row's bits alone.
 template <int ROW_BYTES>
-__device__ __forceinline__ constexpr int swizzle(int r) {
-  return ROW_BYTES % 256 ? ((r << 1) & 4) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
+__device__ __forceinline__ constexpr int row_bits(int r) {
+  return ROW_BYTES % 256 ? ((r >> 2) & 1) | (((r ^ (r >> 3)) & 1) << 1) | (((r >> 1) & 1) << 2)
+                         : ((r & 7) << 1) | ((r >> 3) & 1);
+}
+template <int ROW_BYTES>
+__device__ __forceinline__ constexpr int turned(int c) {
+  if (ROW_BYTES % 256) return c;
+  return (c & ~15) | (((c >> 1) & 1) << 3) | (((c >> 2) & 3) << 1) | (c & 1);
+}
+template <int ROW_BYTES>
+__device__ __forceinline__ constexpr int turned_back(int c) {
+  if (ROW_BYTES % 256) return c;
+  return (c & ~15) | (((c >> 1) & 3) << 2) | (((c >> 3) & 1) << 1) | (c & 1);
+}
+// Place of chunk c of row r, and the chunk in a place.
+template <int ROW_BYTES>
+__device__ __forceinline__ constexpr int place_of(int r, int c) {
+  return turned<ROW_BYTES>(c) ^ row_bits<ROW_BYTES>(r);
+}
+template <int ROW_BYTES>
+__device__ __forceinline__ constexpr int chunk_at(int r, int place) {
+  return turned_back<ROW_BYTES>(place ^ row_bits<ROW_BYTES>(r));
 }
 
 template <typename T, int DK, int DV, bool IN_KEY>
@@ -128,9 +174,13 @@ struct Attend {
   // latent), then n rows of R1 bytes (a value, or the rest of a latent).
   static constexpr int R0 = IN_KEY ? VB : KB, R1 = IN_KEY ? KB - VB : VB;
   static constexpr int ROW = R0 + R1;                          // LDS bytes per key
-  static constexpr int TILES_LDS = 4 * kNarrowTile * ROW;      // = 2 * kWideTile * ROW
+  // wide tiles under way or in use: a 64-wide head's are over too soon for one
+  // to arrive meanwhile
+  static constexpr int BUFS = DK == 64 ? 4 : 2;
+  static constexpr int TILES_LDS = BUFS * kWideTile * ROW;     // >= 4 * kNarrowTile * ROW
   static constexpr int WAVE_XCHG = 2048 + 128;                 // latent: a wave's weights, maxima
-  static constexpr int LDS = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kWideRows);
+  static constexpr int RING = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kWideRows);
+  static constexpr int LDS = RING + 4096;
   static constexpr int NT = DV / 32 / (IN_KEY ? 2 : 1);        // output tiles of a wave
   // chunks among which a row's are moved, and steps of 16 values they make
   static constexpr int VS = IN_KEY ? R0 : R1;                  // LDS stride of values
@@ -141,41 +191,96 @@ struct Attend {
   // 2^-31 of the largest keep a value, where fp16 alone ends at 2^-25
   static constexpr float SHIFT = sizeof(T) == 2 && __is_same(T, _Float16) ? 6.0f : 0.0f;
 
-  // The row that holds key `key` of the item's request, in two steps, so that
-  // a page number is asked for a tile earlier than it is needed: its load would
-  // otherwise be waited for behind the loads of a whole tile.
-  static __device__ __forceinline__ int in_range(const AttendItem &it, int key) {
-    return min(max(key, it.key_lo), it.key_hi - 1);
-  }
-  static __device__ __forceinline__ int page_of(const AttendArgs &a, const AttendItem &it,
-                                                int64_t base, int key) {
-    if (!a.pages) return 0;
-    const int64_t at = base + static_cast<unsigned>(in_range(it, key)) /
-                                  static_cast<unsigned>(a.page_rows);
-    return at >= 0 && at < a.n_listed ? a.pages[at] : -1;
-  }
-  static __device__ __forceinline__ uint32_t row_of(const AttendArgs &a, const AttendItem &it,
-                                                    int64_t base, int key, int page) {
-    key = in_range(it, key);
-    int64_t row = base + key, instead = 0;
-    if (a.pages) {
-      instead = static_cast<unsigned>(key) % static_cast<unsigned>(a.page_rows);
-      row = page < 0 ? -1 : static_cast<int64_t>(page) * a.page_rows + instead;
+  // Where an item's keys are: key x is `offset` bytes from src, found through
+  // its page's number (paged).  A base that leads outside the rows, or outside
+  // the page list, is reported and all the item's keys read row 0; so is a page
+  // outside the pool, and its keys read page 0.
+  struct Source {
+    const uint8_t *src;
+    const int32_t *pages;  // of the request's first page
+    int32_t *status;
+    uint32_t stride;
+    int page_rows, page_shift, lo, last;
+    uint32_t n_pages;
+
+    __device__ __forceinline__ Source(const AttendArgs &a, const AttendItem &it)
+        : src(a.rows), pages(nullptr), status(a.status), stride(a.row_bytes),
+          page_rows(a.page_rows), page_shift(a.page_shift), lo(it.key_lo), last(it.key_hi - 1),
+          n_pages(0) {
+      const int64_t base = uniform<int64_t>(a.base ? a.base[it.req] : it.req * a.pages_stride);
+      bool ok;
+      if (a.pages) {
+        ok = base >= 0 && base + page_of(max(last, 0)) < a.n_listed;
+        if (ok) pages = a.pages + base;
+        n_pages = a.n_pages;
+      } else {
+        ok = base + lo >= 0 && base + last < a.n_rows;
+        if (ok) src += base * a.row_bytes;
+      }
+      if (!ok) {
+        stride = 0;
+        if (status && lo <= last) atomicOr(status, GPB_STATUS_BAD_DESCRIPTOR);
+      }
     }
-    if (row < 0 || row >= a.n_rows) {
-      row = instead;
-      if (a.status) atomicOr(a.status, GPB_STATUS_BAD_DESCRIPTOR);
+    __device__ __forceinline__ int in_range(int key) const { return min(max(key, lo), last); }
+    __device__ __forceinline__ uint32_t page_of(uint32_t key) const {
+      return page_shift >= 0 ? key >> page_shift : key / static_cast<uint32_t>(page_rows);
     }
-    return static_cast<uint32_t>(row);
+    __device__ __forceinline__ const int32_t *place(int key) const {
+      return pages + page_of(in_range(key));
+    }
+    __device__ __forceinline__ uint64_t offset(int key, uint32_t page) const {
+      uint32_t row = in_range(key);
+      if (pages) {
+        if (page >= n_pages) {
+          page = 0;
+          if (status) atomicOr(status, GPB_STATUS_BAD_DESCRIPTOR);
+        }
+        row = page * page_rows + (row - page_of(row) * page_rows);
+      }
+      return static_cast<uint64_t>(row) * stride;
+    }
+    // At once, waiting for the page's number.
+    __device__ __forceinline__ uint64_t offset(int key) const {
+      return offset(key, pages ? *place(key) : 0);
+    }
+  };
+
+  static __device__ __forceinline__ int first_key(const AttendItem &it, int v, int tile) {
+    return (v < it.n_first ? it.tile0 + v : it.tile1 + v - it.n_first) * tile;
   }
 
-  static __device__ __forceinline__ uint32_t whole_row(const AttendArgs &a, const AttendItem &it,
-                                                       int64_t base, int key) {
-    return row_of(a, it, base, key, page_of(a, it, base, key));
-  }
+  // Wide tiles: the page numbers of a tile come through LDS as its rows do,
+  // AHEAD tiles before those are asked for, so that no wait for a page number
+  // is a wait for the loads of rows behind it.  A wave has places for four
+  // tiles.
+  static constexpr int AHEAD = BUFS - 1;
+  struct Rows : Source {
+    const AttendItem &it;
+    lds_u8 *ring;
+    int mine;  // the key of a tile whose row the lane finds
+
+    __device__ __forceinline__ Rows(const AttendArgs &a, const AttendItem &it, lds_u8 *lds,
+                                    int wave, int lane)
+        : Source(a, it), it(it), ring(lds + RING + wave * 1024), mine(wave * 16 + (lane & 15)) {}
+    // A tile's loads go out with the products of an earlier one; where no tile
+    // follows they all read one row, which costs less than a second form of
+    // the products without them.
+    __device__ __forceinline__ int key(int v) const {
+      return v < it.n_tiles ? first_key(it, v, kWideTile) + mine : this->lo;
+    }
+    __device__ __forceinline__ void ask(int v) const {
+      if (this->pages) load4_to_lds(this->place(key(v)), ring + (v & 3) * 256);
+    }
+    __device__ __forceinline__ uint64_t row(int v, int lane) const {
+      typedef __attribute__((address_space(3))) int lds_int;
+      return this->offset(key(v),
+                          this->pages ? ((const lds_int *)(ring + (v & 3) * 256))[lane] : 0);
+    }
+  };
 
   // The loads of one tile of TILE keys, WAVES waves sharing them, each TILE /
-  // WAVES keys.  Lane r of `row` holds the source row of the wave's key r.
+  // WAVES keys.  Lane r of `off` holds the place of the wave's key r.
   // Instruction i of the wave, of N, goes out by issue<i>: the products of one
   // tile are under way meanwhile.
   template <int TILE, int WAVES>
@@ -187,13 +292,13 @@ struct Attend {
     uint64_t off;           // of the lane's row
     int wave, lane;
 
-    __device__ __forceinline__ Loader(const AttendArgs &a, const AttendItem &it, uint32_t row,
-                                      lds_u8 *tile, int wave, int lane)
-        : to(tile), off(static_cast<uint64_t>(row) * static_cast<uint32_t>(a.row_bytes)),
-          wave(wave), lane(lane) {
-      src[0] = a.rows + static_cast<int64_t>(it.kv_head) * KB;
+    __device__ __forceinline__ Loader(const AttendArgs &a, const AttendItem &it,
+                                      const Source &from, uint64_t off, lds_u8 *tile, int wave,
+                                      int lane)
+        : to(tile), off(off), wave(wave), lane(lane) {
+      src[0] = uniform(from.src + static_cast<int64_t>(it.kv_head) * KB);
       src[1] = IN_KEY ? src[0] + VB
-                      : a.rows + static_cast<int64_t>(a.hkv) * KB +
+                      : from.src + static_cast<int64_t>(a.hkv) * KB +
                             static_cast<int64_t>(it.kv_head) * VB;
     }
     template <int I>
@@ -205,14 +310,14 @@ struct Attend {
         if constexpr (C == 64) {  // a row each, 16 a wave: its swizzle is that of J
           const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(off), J);
           const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(off >> 32), J);
-          load_to_lds<swizzle<B>(J) * 16, J * 1024>(
-              src[0], lo | static_cast<uint64_t>(hi) << 32, lane * 16, at);
+          load_to_lds<turned_back<B>(row_bits<B>(J)) * 16, J * 1024>(
+              src[0], lo | static_cast<uint64_t>(hi) << 32, turned_back<B>(lane) * 16, at);
         } else {
           const int r = J * (64 / C) + lane / C;  // and so is the swizzle of key r
           const uint32_t lo = __shfl(static_cast<uint32_t>(off), r, 64);
           const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), r, 64);
           load_to_lds(src[I < N0 ? 0 : 1] + (lo | static_cast<uint64_t>(hi) << 32) +
-                          ((lane % C) ^ swizzle<B>(r)) * 16,
+                          chunk_at<B>(r, lane % C) * 16,
                       at + J * 1024);
         }
       }
@@ -234,6 +339,12 @@ struct Attend {
   struct State {
     f32x16 o[NT];
     float m, l;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[t] = f32x16{};
+      m = -INFINITY;
+      l = 0.0f;
+    }
   };
 
   // Where in a tile the lane reads its operands.  The swizzle moves a chunk
@@ -248,10 +359,10 @@ struct Attend {
   static __device__ __forceinline__ void find_places(Places &w, int lane) {
     const int n = lane & 31, half = lane >> 5, i = lane & 15;
 #pragma unroll
-    for (int d = 0; d < G0 / 2; ++d) w.k0[d] = n * R0 + ((2 * d + half) ^ swizzle<R0>(n)) * 16;
+    for (int d = 0; d < G0 / 2; ++d) w.k0[d] = n * R0 + place_of<R0>(n, 2 * d + half) * 16;
     if constexpr (IN_KEY)
 #pragma unroll
-      for (int d = 0; d < G1 / 2; ++d) w.k1[d] = n * R1 + ((2 * d + half) ^ swizzle<R1>(n)) * 16;
+      for (int d = 0; d < G1 / 2; ++d) w.k1[d] = n * R1 + place_of<R1>(n, 2 * d + half) * 16;
     // V^T operand of 16 keys and 32 values: lane l gets value l % 32 of keys
     // 4 half .. + 3 and 8 + 4 half .. + 3; of each 16 lanes, lane i reads four
     // values of key i / 4
@@ -261,7 +372,7 @@ struct Attend {
       for (int t = 0; t < VG / 4; ++t) {
         const int row = 8 * x + 4 * half + (i >> 2);
         const int chunk = 4 * t + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-        w.v[x][t] = row * VS + (chunk ^ swizzle<VS>(row)) * 16 + (i & 1) * 8;
+        w.v[x][t] = row * VS + place_of<VS>(row, chunk) * 16 + (i & 1) * 8;
       }
   }
 
@@ -272,12 +383,6 @@ struct Attend {
     const s16x4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(v + w.v[0][t % (VG / 4)] + off));
     const s16x4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(v + w.v[1][t % (VG / 4)] + off));
     return __builtin_bit_cast(x8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
-  }
-
-  static __device__ __forceinline__ bool sees(const AttendArgs &a, const AttendItem &it, int pos,
-                                              int key) {
-    return key <= pos && key >= it.key_lo && key < it.key_hi &&
-           (a.window == 0 || pos - key < a.window || key < a.sinks);
   }
 
   // 16 values of the 32 keys in LDS rows row0 .. of a tile of TILE.
@@ -294,8 +399,9 @@ struct Attend {
   }
 
   // q.k of the 32 keys in LDS rows row0 .. of a tile of TILE and the lane's
-  // query row; the next tile's loads FIRST .. go out between the steps.
-  template <int TILE, int FIRST, typename L>
+  // query row; with every EVERY steps one of the next tile's loads goes out,
+  // the first FIRST.
+  template <int TILE, int FIRST, int EVERY, typename L>
   static __device__ __forceinline__ f32x16 products(const x8 *q, const lds_u8 *tile, int row0,
                                                     const Places &w, const L &next) {
     constexpr int AHEAD = DK / 16 < 6 ? DK / 16 : 6;
@@ -303,10 +409,10 @@ struct Attend {
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) k[d] = key_operand<TILE>(tile, row0, w, d);
     f32x16 s = {};
-    product_steps<TILE, FIRST, 0, AHEAD>(q, tile, row0, w, next, k, s);
+    product_steps<TILE, FIRST, EVERY, 0, AHEAD>(q, tile, row0, w, next, k, s);
     return s;
   }
-  template <int TILE, int FIRST, int D, int AHEAD, typename L>
+  template <int TILE, int FIRST, int EVERY, int D, int AHEAD, typename L>
   static __device__ __forceinline__ void product_steps(const x8 *q, const lds_u8 *tile, int row0,
                                                        const Places &w, const L &next, x8 *k,
                                                        f32x16 &s) {
@@ -314,27 +420,50 @@ struct Attend {
       s = mma<T>(k[D % AHEAD], q[D], s);
       if constexpr (D + AHEAD < DK / 16)
         k[D % AHEAD] = key_operand<TILE>(tile, row0, w, D + AHEAD);
-      next.template issue<FIRST + D>();
+      if constexpr (D % EVERY == EVERY - 1) next.template issue<FIRST + D / EVERY>();
       in_order();
-      product_steps<TILE, FIRST, D + 1, AHEAD>(q, tile, row0, w, next, k, s);
+      product_steps<TILE, FIRST, EVERY, D + 1, AHEAD>(q, tile, row0, w, next, k, s);
     }
   }
 
+  // What a row sees of an item's keys: n keys from `from` on and, of a window's
+  // first tokens, `sunk` from key_lo on.
+  struct Sight {
+    int from;
+    unsigned n, sunk;
+  };
+  static __device__ __forceinline__ Sight sight(const AttendArgs &a, const AttendItem &it,
+                                                int pos) {
+    const int end = min(pos + 1, it.key_hi);  // pos < 2^30
+    Sight x;
+    x.from = a.window > 0 ? max(it.key_lo, pos + 1 - a.window) : it.key_lo;
+    x.n = max(end - x.from, 0);
+    x.sunk = a.window > 0 ? max(min(end, a.sinks) - it.key_lo, 0) : 0;
+    return x;
+  }
+
   // The keys that the row does not see go to -infinity.
-  static __device__ __forceinline__ void mask(const AttendArgs &a, const AttendItem &it, int key0,
-                                              int pos, int half, f32x16 &s) {
+  static __device__ __forceinline__ void mask(const AttendArgs &a, const AttendItem &it,
+                                              const Sight &see, int key0, int half, f32x16 &s) {
+    const unsigned at = key0 + 4 * half - see.from;
+    if (a.window == 0 || key0 >= a.sinks) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int key = key0 + 8 * (i / 4) + 4 * half + i % 4;
-      s[i] = sees(a, it, pos, key) ? s[i] : -INFINITY;
+      for (int i = 0; i < 16; ++i) s[i] = at + 8 * (i / 4) + i % 4 < see.n ? s[i] : -INFINITY;
+    } else {
+      const unsigned first = key0 + 4 * half - it.key_lo;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const unsigned x = 8 * (i / 4) + i % 4;
+        s[i] = at + x < see.n || first + x < see.sunk ? s[i] : -INFINITY;
+      }
     }
   }
 
   static __device__ __forceinline__ float largest(const f32x16 &s) {
-    float top = s[0];
+    float top[4];  // four chains: a wave may be alone on its SIMD
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    return top;
+    for (int i = 0; i < 4; ++i) top[i] = fmaxf(fmaxf(s[i], s[i + 4]), fmaxf(s[i + 8], s[i + 12]));
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   }
 
   // The m to weigh by, given the largest score of new keys: m stays until it is
@@ -350,41 +479,50 @@ struct Attend {
   // Weights 2^(c s - m) of 32 keys, as two right operands of the second
   // product; returns their sum.
   static __device__ __forceinline__ float weights(const f32x16 &s, float c, float m, x8 *p) {
-    float sum = 0.0f;
+    float sum[4] = {};
     const float ref = finite_m(m) - SHIFT;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ref));
-      sum += x;
+      sum[i % 4] += x;
       p[i / 8][i % 8] = static_cast<T>(x);
     }
-    return sum;
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 
   // Sums of N output tiles (values 32 t0 ..) += weights of 16 * NP keys (LDS
-  // rows 0 .. of v).
-  template <int NP, int N>
+  // rows 0 .. of v); with every second step one of the next tile's loads from
+  // FIRST on goes out.
+  template <int NP, int N, int FIRST, typename L>
   static __device__ __forceinline__ void add_values(const x8 *p, const lds_u8 *v, const Places &w,
-                                                    int t0, f32x16 *o) {
-    constexpr int ALL = NP * N, AHEAD = 4;
+                                                    int t0, f32x16 *o, const L &next) {
+    constexpr int AHEAD = 4;
     const lds_u8 *at = v + t0 / (VG / 4) * VG * 16;
     x8 x[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD && i < ALL; ++i) x[i] = value_operand(at, w, i / N * 16, i % N);
-#pragma unroll
-    for (int i = 0; i < ALL; ++i) {
-      o[i % N] = mma<T>(x[i % AHEAD], p[i / N], o[i % N]);
-      if (i + AHEAD < ALL)
-        x[i % AHEAD] = value_operand(at, w, (i + AHEAD) / N * 16, (i + AHEAD) % N);
+    for (int i = 0; i < AHEAD; ++i) x[i] = value_operand(at, w, i / N * 16, i % N);
+    value_steps<NP * N, N, FIRST, 0, AHEAD>(p, at, w, o, next, x);
+  }
+  template <int ALL, int N, int FIRST, int I, int AHEAD, typename L>
+  static __device__ __forceinline__ void value_steps(const x8 *p, const lds_u8 *at,
+                                                     const Places &w, f32x16 *o, const L &next,
+                                                     x8 *x) {
+    if constexpr (I < ALL) {
+      o[I % N] = mma<T>(x[I % AHEAD], p[I / N], o[I % N]);
+      if constexpr (I + AHEAD < ALL)
+        x[I % AHEAD] = value_operand(at, w, (I + AHEAD) / N * 16, (I + AHEAD) % N);
+      if constexpr (I % 2 == 0) next.template issue<FIRST + I / 2>();
       in_order();
+      value_steps<ALL, N, FIRST, I + 1, AHEAD>(p, at, w, o, next, x);
     }
   }
 
   // A key that one row sees and another does not has weight 0 in the other's
-  // product, and 0 times infinity or NaN is NaN.  Tiles that are not whole are
-  // therefore looked through: one with such a value is left out of the
-  // products, and `careful` adds it at the end, row by row.  These lanes'
-  // share (id of ids) of the keys' values:
+  // product, and 0 times infinity or NaN is NaN.  An item whose sums end up
+  // with such a value is therefore done again: the tiles that are not whole are
+  // looked through, those that hold one are left out of the products, and
+  // `careful` adds them at the end, row by row.  These lanes' share (id of
+  // ids) of a tile's values:
   template <int TILE>
   static __device__ __forceinline__ bool odd_values(const lds_u8 *tile, int id, int ids) {
     typedef __attribute__((address_space(3))) u32x4 lds16;
@@ -402,6 +540,16 @@ struct Attend {
     return (bits & kExp) == kExp;
   }
 
+  // Whether a row's sums hold an infinity or NaN.
+  static __device__ __forceinline__ bool odd_sums(const f32x16 *o, float l) {
+    float x = l * 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x = __builtin_fmaf(o[t][i], 0.0f, x);
+    return !(x == 0.0f);
+  }
+
   template <int N>
   static __device__ __forceinline__ void rescale(f32x16 *o, float *l, float f) {
     *l *= f;
@@ -415,14 +563,14 @@ struct Attend {
   template <int NB, typename L>
   static __device__ __forceinline__ void keys(const AttendArgs &a, const AttendItem &it,
                                               const x8 *q, const lds_u8 *tile, const Places &w,
-                                              int key0, bool whole, int pos, State &st, int lane,
-                                              const L &next) {
+                                              int key0, bool whole, const Sight &see, State &st,
+                                              int lane, const L &next) {
     f32x16 s[NB];
-    s[0] = products<32 * NB, 0>(q, tile, 0, w, next);
-    if constexpr (NB == 2) s[1] = products<32 * NB, DK / 16>(q, tile, 32, w, next);
+    s[0] = products<32 * NB, 0, 2>(q, tile, 0, w, next);
+    if constexpr (NB == 2) s[1] = products<32 * NB, DK / 32, 2>(q, tile, 32, w, next);
     if (!whole) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) mask(a, it, key0 + 32 * b, pos, lane >> 5, s[b]);
+      for (int b = 0; b < NB; ++b) mask(a, it, see, key0 + 32 * b, lane >> 5, s[b]);
     }
     float top = largest(s[0]);
     if constexpr (NB == 2) top = fmaxf(top, largest(s[1]));
@@ -435,24 +583,13 @@ struct Attend {
     x8 p[2 * NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) st.l += weights(s[b], a.c, m, p + 2 * b);
-    add_values<2 * NB, NT>(p, tile + 32 * NB * R0, w, 0, st.o);
+    add_values<2 * NB, NT, 0>(p, tile + 32 * NB * R0, w, 0, st.o, NoLoader());
   }
 
   static __device__ __forceinline__ bool whole_tile(const AttendArgs &a, const AttendItem &it,
                                                     int key0, int n) {
     return key0 >= it.key_lo && key0 + n <= it.key_hi && key0 + n - 1 <= it.pos_min &&
            (a.window == 0 || it.pos_max - key0 < a.window || key0 + n <= a.sinks);
-  }
-
-  static __device__ __forceinline__ int first_key(const AttendItem &it, int v, int tile) {
-    return (v < it.n_first ? it.tile0 + v : it.tile1 + v - it.n_first) * tile;
-  }
-
-  // The key of the lane's load for wide tile v.  A tile's loads go out with the
-  // products of the one before; where no tile follows they all read one row,
-  // which costs less than a second form of the products without them.
-  static __device__ __forceinline__ int key_after(const AttendItem &it, int v, int mine) {
-    return v < it.n_tiles ? first_key(it, v, kWideTile) + mine : it.key_lo;
   }
 
   // The lane's query row: its token, its head, its queries in registers.
@@ -522,10 +659,6 @@ struct Attend {
       a.lse[static_cast<int64_t>(token) * a.n_heads + h] = log_sum(st.m, l);
   }
 
-  static __device__ __forceinline__ int64_t request_base(const AttendArgs &a, int req) {
-    return a.base ? a.base[req] : req * a.pages_stride;
-  }
-
   // The end of an item whose products left tiles out (see odd_values): the
   // sums so far go to LDS, and a wave takes a row at a time through the left
   // tiles, key by key, only those that the row sees.
@@ -549,16 +682,15 @@ struct Attend {
     }
     __syncthreads();
     const int tile = it.wide ? kWideTile : kNarrowTile;
-    const int64_t base = request_base(a, it.req);
-    const T *keys = reinterpret_cast<const T *>(a.rows) + static_cast<int64_t>(it.kv_head) * DK;
-    const T *vals = IN_KEY ? keys : reinterpret_cast<const T *>(a.rows) +
+    const Source from(a, it);
+    const T *keys = reinterpret_cast<const T *>(from.src) + static_cast<int64_t>(it.kv_head) * DK;
+    const T *vals = IN_KEY ? keys : reinterpret_cast<const T *>(from.src) +
                                         static_cast<int64_t>(a.hkv) * DK +
                                         static_cast<int64_t>(it.kv_head) * DV;
-    const int64_t row_values = a.row_bytes / 2;
     for (int r = threadIdx.x >> 6; r < it.n_rows; r += 4) {
       const int g = it.row0 + r;
       const int token = g / a.G, h = g - token * a.G + it.kv_head * a.G;
-      const int pos = a.list[a.positions_at + token];
+      const Sight see = sight(a, it, a.list[a.positions_at + token]);
       const T *src = reinterpret_cast<const T *>(a.q + token * a.q_ts + h * a.q_hs);
       float q[PK], o[PV], m = ml[2 * r], sum = ml[2 * r + 1];
 #pragma unroll
@@ -570,15 +702,15 @@ struct Attend {
         if (whole_tile(a, it, key0, tile)) continue;
         bool odd = false;
         for (int x = 0; x < tile; ++x) {
-          const T *val = vals + whole_row(a, it, base, key0 + x) * row_values;
+          const T *val = vals + from.offset(key0 + x) / 2;
           for (int e = lane; e < DV; e += 64)
             odd |= not_finite(__builtin_bit_cast(uint16_t, val[e]));
         }
         if (!__any(odd)) continue;
         for (int x = 0; x < tile; ++x) {
-          const int key = key0 + x;
-          if (!sees(a, it, pos, key)) continue;
-          const int64_t at = whole_row(a, it, base, key) * row_values;
+          const unsigned key = key0 + x;
+          if (key - see.from >= see.n && key - it.key_lo >= see.sunk) continue;
+          const int64_t at = from.offset(key) / 2;
           float s = 0.0f;
 #pragma unroll
           for (int e = 0; e < PK; ++e) s += q[e] * static_cast<float>(keys[at + e * 64 + lane]);
@@ -611,66 +743,77 @@ struct Attend {
     }
   }
 
-  // Four waves, 32 rows each, tiles of 64 keys in two LDS buffers.
-  static __device__ __forceinline__ void wide(const AttendArgs &a, const AttendItem &it,
+  // Four waves, 32 rows each, tiles of 64 keys in BUFS LDS buffers.
+  template <bool SCAN>
+  static __device__ __forceinline__ bool wide(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int row = wave * 32 + (lane & 31), half = lane >> 5;
-    const int mine16 = wave * 16 + (lane & 15);  // the key whose row the lane finds
     constexpr int BUF = kWideTile * ROW;
+    typedef Loader<kWideTile, 4> Load;
+    const Rows rows(a, it, lds, wave, lane);
     x8 q[DK / 16];
     int pos;
     load_queries(a, it, row, half, q, &pos);
+    const Sight see = sight(a, it, pos);
     Places w;
     find_places(w, lane);
     State st;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) st.o[t] = f32x16{};
-    st.m = -INFINITY;
-    st.l = 0.0f;
-    bool left = false;  // a tile is left to `careful`
+    st.clear();
+    bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
-      const int64_t base = request_base(a, it.req);
-      int next = first_key(it, 0, kWideTile) + mine16, page = page_of(a, it, base, next);
-      Loader<kWideTile, 4>(a, it, row_of(a, it, base, next, page), lds, wave, lane).all();
-      next = key_after(it, 1, mine16);
-      page = page_of(a, it, base, next);
+#pragma unroll
+      for (int v = 0; v < AHEAD; ++v) rows.ask(v);
+      loads_done();
+#pragma unroll
+      for (int v = 0; v < AHEAD; ++v) {
+        Load(a, it, rows, rows.row(v, lane), lds + v * BUF, wave, lane).all();
+        rows.ask(v + AHEAD);
+      }
       for (int v = 0; v < it.n_tiles; ++v) {
-        loads_done();
+        loads_done<(BUFS - 2) * Load::N>();
         __syncthreads();
-        lds_u8 *now = lds + (v & 1) * BUF;
+        lds_u8 *now = lds + v % BUFS * BUF;
         const int key0 = first_key(it, v, kWideTile);
         const bool whole = whole_tile(a, it, key0, kWideTile);
-        const bool odd =
-            !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
+        const bool odd = SCAN && !whole &&
+                         __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const Loader<kWideTile, 4> load(a, it, row_of(a, it, base, next, page),
-                                        lds + (~v & 1) * BUF, wave, lane);
-        next = key_after(it, v + 2, mine16);
-        page = page_of(a, it, base, next);
+        const Load load(a, it, rows, rows.row(v + AHEAD, lane), lds + (v + AHEAD) % BUFS * BUF, wave,
+                        lane);
+        rows.ask(v + 2 * AHEAD);
         if (odd) load.all();
-        else keys<2>(a, it, q, now, w, key0, whole, pos, st, lane, load);
+        else keys<2>(a, it, q, now, w, key0, whole, see, st, lane, load);
       }
       loads_done();
     }
-    const float l = st.l + other_half(st.l, half);
-    if (__syncthreads_or(left)) careful(a, it, lds, row, half, st, l, 0, true);
-    else store(a, it, row, half, st, l, 0);
+    float l = st.l + other_half(st.l, half);
+    if constexpr (SCAN) {
+      if (__syncthreads_or(left)) {
+        careful(a, it, lds, row, half, st, l, 0, true);
+        return true;
+      }
+    } else if (__syncthreads_or(row < it.n_rows && odd_sums(st.o, l))) {
+      return false;
+    }
+    store(a, it, row, half, st, l, 0);
+    return true;
   }
 
   // Latent rows: 64 query rows, two waves to each 32 of them.  The sums of a
   // row are 512 values, too many registers beside its 576 of query for one
   // wave, so of a tile's 64 keys each wave of a pair scores 32, hands its
   // weights to the other through LDS, and both add all 64 keys to their half
-  // of the values.  A wave weighs by the larger of the pair's last common
-  // maximum and its own keys' maximum; where the two differ (a new maximum)
-  // the weights are brought to the larger one before they are used.
-  static __device__ __forceinline__ void latent(const AttendArgs &a, const AttendItem &it,
+  // of the values, their own keys first.  A pair ends every tile with one m;
+  // where their keys move it apart, each brings its sums, and the weights it
+  // was handed, to the larger.
+  template <bool SCAN>
+  static __device__ __forceinline__ bool latent(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int part = wave & 1, half = lane >> 5;
     const int row = (wave >> 1) * 32 + (lane & 31);
-    const int mine16 = wave * 16 + (lane & 15);  // the key whose row the lane finds
+    const Rows rows(a, it, lds, wave, lane);
     const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
     constexpr int BUF = kWideTile * ROW;
     lds_u8 *mine = lds + TILES_LDS + wave * WAVE_XCHG;
@@ -682,18 +825,16 @@ struct Attend {
     load_queries(a, it, row, half, q, &pos);
     Places w;
     find_places(w, lane);
+    const Sight see = sight(a, it, pos);
     State st;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) st.o[t] = f32x16{};
-    st.m = -INFINITY;
-    st.l = 0.0f;
-    bool left = false;  // a tile is left to `careful`
+    st.clear();
+    bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
-      const int64_t base = request_base(a, it.req);
-      int next = first_key(it, 0, kWideTile) + mine16, page = page_of(a, it, base, next);
-      Loader<kWideTile, 4>(a, it, row_of(a, it, base, next, page), lds, wave, lane).all();
-      next = key_after(it, 1, mine16);
-      page = page_of(a, it, base, next);
+      typedef Loader<kWideTile, 4> Load;
+      rows.ask(0);
+      loads_done();
+      Load(a, it, rows, rows.row(0, lane), lds, wave, lane).all();
+      rows.ask(1);
       for (int v = 0; v < it.n_tiles; ++v) {
         loads_done();
         __syncthreads();
@@ -701,56 +842,44 @@ struct Attend {
         const int key0 = first_key(it, v, kWideTile);
         const bool whole = whole_tile(a, it, key0, kWideTile);
         const bool odd =
-            !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
+            SCAN && !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const Loader<kWideTile, 4> load(a, it, row_of(a, it, base, next, page),
-                                        lds + (~v & 1) * BUF, wave, lane);
-        next = key_after(it, v + 2, mine16);
-        page = page_of(a, it, base, next);
-        if (odd) {
+        const Load load(a, it, rows, rows.row(v + 1, lane), lds + (~v & 1) * BUF, wave, lane);
+        rows.ask(v + 2);
+        if (odd || idle) {
           load.all();
+          if (!odd) __syncthreads();
           continue;
         }
-        f32x16 s = {};
-        if (idle) load.all();
-        else s = products<kWideTile, 0>(q, now, 32 * part, w, load);
-        x8 p[2], p2[2];
-        float m = -INFINITY;
-        if (!idle) {
-          if (!whole) mask(a, it, key0 + 32 * part, pos, half, s);
-          const float top = largest(s) * a.c;
-          m = next_m(st.m, fmaxf(top, other_half(top, half)));
-          if (__any(m > st.m)) st.l *= __builtin_amdgcn_exp2f(st.m - finite_m(m));
-          st.l += weights(s, a.c, m, p);
-          ((lds8 *)mine)[lane] = p[0];
-          ((lds8 *)mine)[64 + lane] = p[1];
-          if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
+        x8 p[2];
+        f32x16 s = products<kWideTile, 0, 3>(q, now, 32 * part, w, load);
+        if (!whole) mask(a, it, see, key0 + 32 * part, half, s);
+        const float top = largest(s) * a.c;
+        const float m = next_m(st.m, fmaxf(top, other_half(top, half)));
+        if (__any(m > st.m)) {
+          rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(st.m - finite_m(m)));
+          st.m = m;
         }
+        st.l += weights(s, a.c, m, p);
+        ((lds8 *)mine)[lane] = p[0];
+        ((lds8 *)mine)[64 + lane] = p[1];
+        if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
+        add_values<2, NT, DK / 48>(p, now + 32 * part * VS, w, part * NT, st.o, load);
         __syncthreads();
-        if (!idle) {
-          p2[0] = ((const lds8 *)theirs)[lane];
-          p2[1] = ((const lds8 *)theirs)[64 + lane];
-          const float m2 = ((const lds_float *)(theirs + 2048))[lane & 31];
-          const float both = fmaxf(m, m2), ref = finite_m(both);
-          if (__any(m != m2)) {
-            const float f = __builtin_amdgcn_exp2f(m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
-            st.l *= f;
+        p[0] = ((const lds8 *)theirs)[lane];
+        p[1] = ((const lds8 *)theirs)[64 + lane];
+        const float m2 = ((const lds_float *)(theirs + 2048))[lane & 31];
+        if (__any(m2 != m)) {
+          const float both = fmaxf(m, m2), f2 = __builtin_amdgcn_exp2f(m2 - finite_m(both));
+          rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(m - finite_m(both)));
+          st.m = both;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                p[b][j] = static_cast<T>(static_cast<float>(p[b][j]) * f);
-                p2[b][j] = static_cast<T>(static_cast<float>(p2[b][j]) * f2);
-              }
-          }
-          if (__any(both > st.m)) {
-            float unused = 0.0f;
-            rescale<NT>(st.o, &unused, __builtin_amdgcn_exp2f(st.m - ref));
-            st.m = both;
-          }
-          add_values<2, NT>(p, now + 32 * part * VS, w, part * NT, st.o);
-          add_values<2, NT>(p2, now + 32 * (1 - part) * VS, w, part * NT, st.o);
+            for (int j = 0; j < 8; ++j)
+              p[b][j] = static_cast<T>(static_cast<float>(p[b][j]) * f2);
         }
+        add_values<2, NT, 0>(p, now + 32 * (1 - part) * VS, w, part * NT, st.o, NoLoader());
       }
       loads_done();
     }
@@ -760,13 +889,22 @@ struct Attend {
     ((lds_float *)mine)[lane] = l;
     __syncthreads();
     l += ((const lds_float *)theirs)[lane];
-    if (__syncthreads_or(left)) careful(a, it, lds, row, half, st, l, part * NT, true);
-    else store(a, it, row, half, st, l, part * NT);
+    if constexpr (SCAN) {
+      if (__syncthreads_or(left)) {
+        careful(a, it, lds, row, half, st, l, part * NT, true);
+        return true;
+      }
+    } else if (__syncthreads_or(row < it.n_rows && odd_sums(st.o, l))) {
+      return false;
+    }
+    store(a, it, row, half, st, l, part * NT);
+    return true;
   }
 
   // Four waves over the same rows, each with tiles of 32 keys of its own;
   // their sums meet in LDS at the end, the waves in order.
-  static __device__ __forceinline__ void narrow(const AttendArgs &a, const AttendItem &it,
+  template <bool SCAN>
+  static __device__ __forceinline__ bool narrow(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int row = lane & 31, half = lane >> 5;
@@ -775,35 +913,33 @@ struct Attend {
     load_queries(a, it, row, half, q, &pos);
     Places w;
     find_places(w, lane);
+    const Sight see = sight(a, it, pos);
     State st;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) st.o[t] = f32x16{};
-    st.m = -INFINITY;
-    st.l = 0.0f;
-    bool left = false;  // a tile is left to `careful`
+    const Source from(a, it);
     lds_u8 *own = lds + wave * kNarrowTile * ROW;
-    if (wave < it.n_tiles) {
-      const int64_t base = request_base(a, it.req);
-      int next = first_key(it, wave, kNarrowTile) + (lane & 31), page = page_of(a, it, base, next);
-      for (int v = wave; v < it.n_tiles; v += 4) {
-        const uint32_t row = row_of(a, it, base, next, page);
-        next = first_key(it, min(v + 4, it.n_tiles - 1), kNarrowTile) + (lane & 31);
-        page = page_of(a, it, base, next);
-        Loader<kNarrowTile, 1>(a, it, row, own, 0, lane).all();
-        loads_done();
-        const int key0 = first_key(it, v, kNarrowTile);
-        const bool whole = whole_tile(a, it, key0, kNarrowTile);
-        if (!whole && __any(odd_values<kNarrowTile>(own, lane, 64))) left = true;
-        else keys<1>(a, it, q, own, w, key0, whole, pos, st, lane, NoLoader());
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      }
+    typedef __attribute__((address_space(3))) float lds_float;
+    lds_float *slot = (lds_float *)lds;
+    constexpr int SLOT = (NT * 16 + 2) * 64;
+    st.clear();
+    bool left = false;  // SCAN: a tile is left to `careful`
+    int next = first_key(it, wave, kNarrowTile) + (lane & 31);
+    int page = wave < it.n_tiles && from.pages ? *from.place(next) : 0;
+    for (int v = wave; v < it.n_tiles; v += 4) {
+      const uint64_t off = from.offset(next, page);
+      next = first_key(it, min(v + 4, it.n_tiles - 1), kNarrowTile) + (lane & 31);
+      if (from.pages) page = *from.place(next);
+      Loader<kNarrowTile, 1>(a, it, from, off, own, 0, lane).all();
+      loads_done();
+      const int key0 = first_key(it, v, kNarrowTile);
+      const bool whole = whole_tile(a, it, key0, kNarrowTile);
+      if (SCAN && !whole && __any(odd_values<kNarrowTile>(own, lane, 64))) left = true;
+      else keys<1>(a, it, q, own, w, key0, whole, see, st, lane, NoLoader());
+      // the tile has been read before the next one's loads overwrite it
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     float l = st.l + other_half(st.l, half);
 
     // waves 2 and 3 hand over to 0 and 1, then 1 to 0
-    typedef __attribute__((address_space(3))) float lds_float;
-    lds_float *slot = (lds_float *)lds;
-    constexpr int SLOT = (NT * 16 + 2) * 64;
 #pragma unroll
     for (int step = 2; step >= 1; step >>= 1) {
       __syncthreads();
@@ -820,7 +956,7 @@ struct Attend {
       if (wave < step) {
         const lds_float *from = slot + wave * SLOT + lane;
         const float m2 = from[NT * 16 * 64], l2 = from[NT * 16 * 64 + 64];
-        const float m = fmaxf(st.m, m2), ref = m == -INFINITY ? 0.0f : m;
+        const float m = fmaxf(st.m, m2), ref = finite_m(m);
         const float f1 = __builtin_amdgcn_exp2f(st.m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
         l = l * f1 + l2 * f2;
         st.m = m;
@@ -831,8 +967,29 @@ struct Attend {
             st.o[t][i] = st.o[t][i] * f1 + from[(t * 16 + i) * 64] * f2;
       }
     }
-    if (__syncthreads_or(left)) careful(a, it, lds, row, half, st, l, 0, wave == 0);
-    else if (wave == 0) store(a, it, row, half, st, l, 0);
+    if constexpr (SCAN) {
+      if (__syncthreads_or(left)) {
+        careful(a, it, lds, row, half, st, l, 0, wave == 0);
+        return true;
+      }
+    } else if (__syncthreads_or(wave == 0 && row < it.n_rows && odd_sums(st.o, l))) {
+      return false;
+    }
+    if (wave == 0) store(a, it, row, half, st, l, 0);
+    return true;
+  }
+
+  // An item's work.  False: its sums hold an infinity or NaN, nothing has been
+  // written, and the item is to be done again with SCAN.
+  template <bool SCAN>
+  static __device__ __forceinline__ bool item(const AttendArgs &a, const AttendItem &it,
+                                              lds_u8 *lds) {
+    if constexpr (IN_KEY) return latent<SCAN>(a, it, lds);
+    else return it.wide ? wide<SCAN>(a, it, lds) : narrow<SCAN>(a, it, lds);
+  }
+  // Apart, so that the registers of the common case are allotted without it.
+  static __device__ __attribute__((noinline)) void again(AttendArgs a, AttendItem it, lds_u8 *lds) {
+    item<true>(uniform(a), uniform(it), uniform(lds));
   }
 };
 
@@ -859,12 +1016,7 @@ __global__ __launch_bounds__(256, IN_KEY ? 1 : 2) void k_attend(AttendArgs a) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, GPB_STATUS_BAD_PLAN_INPUT);
     return;
   }
-  if constexpr (IN_KEY) {
-    A::latent(a, it, lds);
-  } else {
-    if (it.wide) A::wide(a, it, lds);
-    else A::narrow(a, it, lds);
-  }
+  if (!A::template item<false>(a, it, lds)) A::again(a, it, lds);
 }
 
 // The rows of one token and KV head: parts weighted by 2^(m - max m), in the
@@ -990,7 +1142,10 @@ int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io 
   a.status = d_status;
   a.c = io->scale * 1.44269504088896341f;
   a.row_bytes = p->format.row_bytes; a.page_rows = p->page_rows;
-  a.window = p->window; a.sinks = p->sinks;
+  a.page_shift = p->page_rows & (p->page_rows - 1) ? -1 : __builtin_ctz(p->page_rows);
+  a.n_pages = static_cast<int32_t>(usable / p->page_rows);
+  // (no position reaches 2^30, so a larger window is no window)
+  a.window = std::min(p->window, 1 << 30); a.sinks = std::min(p->sinks, 1 << 30);
   a.hkv = p->format.n_kv_heads; a.n_heads = p->n_heads; a.G = p->n_heads / a.hkv;
   a.n_tokens = p->n_tokens; a.bs = p->bs; a.max_keys = p->max_keys;
   a.n_items = p->n_items; a.n_joins = p->n_joins; a.n_refs = p->n_refs;
