@@ -115,7 +115,7 @@ class gpb_attend_shape(ctypes.Structure):
 class gpb_attend_plan(ctypes.Structure):
     _fields_ = [("format", gpb_row_format)] + [(n, ctypes.c_int32) for n in (
         "bs", "n_heads", "window", "sinks", "page_rows", "n_groups", "n_tokens", "max_keys",
-        "n_items", "n_joins", "n_refs", "n_partial_rows", "joins_at", "refs_at",
+        "n_items", "n_wide", "n_joins", "n_refs", "n_partial_rows", "joins_at", "refs_at",
         "positions_at", "list_ints")] + [("workspace_bytes", ctypes.c_int64)]
 
 
@@ -629,6 +629,7 @@ class RowFormat:
         self.row_bytes = payload if row_bytes is None else int(row_bytes)
         self.c = gpb_row_format(codes[dtype], self.n_kv_heads, self.k_dim, self.v_dim,
                                 int(self.values_in_key), self.row_bytes)
+        self.ref = ctypes.byref(self.c)
 
 
 class Rotation:
@@ -643,31 +644,34 @@ class Rotation:
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq: a contiguous float32 vector, got %s %s"
                              % (inv_freq.dtype, tuple(inv_freq.shape)))
-        self.inv_freq, self.start, self.interleaved = inv_freq, int(start), bool(interleaved)
-        pairs = inv_freq.numel()
+        self.inv_freq, self.start, self.interleaved = inv_freq, int(start), int(bool(interleaved))
+        self.pairs = pairs = inv_freq.numel()
+        self.index_dtype = torch.int32
         self.sections = [pairs] if sections is None else [int(n) for n in sections]
         if not 1 <= len(self.sections) <= MAX_AXES or sum(self.sections) != pairs:
             raise ValueError("sections %s do not name the axis of %d pairs (at most %d axes)"
                              % (self.sections, pairs, MAX_AXES))
+        self.c_sections = (ctypes.c_int32 * MAX_AXES)(*self.sections)
 
 
-def _same_device(device, **tensors):
-    """Every tensor on ``device``; the launch goes there whatever the current
+def _same_device(index, **tensors):
+    """Every tensor on GPU ``index``: the launch goes there, whatever the current
     device is."""
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, the call runs on %s" % (name, t.device, device))
+        if t is not None and t.get_device() != index:
+            raise ValueError("%s is on %s, the call runs on GPU %d" % (name, t.device, index))
 
 
 def _heads(t, n_tokens, n_heads, dim, dtype, what):
     """Strides (token, head) in elements of a [tokens, heads, dim] tensor whose
     last dimension is contiguous."""
-    if t.dim() != 3 or t.dtype != dtype or t.shape[0] < n_tokens or t.shape[1] != n_heads \
-            or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype != dtype or shape[0] < n_tokens or shape[1] != n_heads \
+            or shape[2] != dim or stride[2] != 1:
         raise ValueError("%s: need %s [>= %d, %d, %d] with its last dimension contiguous, got "
                          "%s %s, strides %s" % (what, dtype, n_tokens, n_heads, dim, t.dtype,
-                                                tuple(t.shape), t.stride()))
-    return t.stride(0), t.stride(1)
+                                                tuple(shape), stride))
+    return stride[0], stride[1]
 
 
 def _int32(t, numel, what):
@@ -675,7 +679,7 @@ def _int32(t, numel, what):
     if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < numel:
         raise ValueError("%s: need a contiguous int32 tensor of %d, got %s %s"
                          % (what, numel, t.dtype, tuple(t.shape)))
-    return t
+    return t.data_ptr()
 
 
 def _rows_of(t, row_bytes, what):
@@ -685,32 +689,41 @@ def _rows_of(t, row_bytes, what):
     return t.numel() * t.element_size() // row_bytes
 
 
-class _on:
-    """The device of a call made current, and the stream it is given."""
+def _device_index(t, what):
+    if not t.is_cuda:
+        raise ValueError("%s is in host memory: the rows are made and read on the GPU" % what)
+    return t.get_device()
 
-    def __init__(self, device, stream):
+
+class _on:
+    """The device of a call made current (where it is not), and the stream."""
+
+    def __init__(self, index, stream):
         import torch
-        if device.type != "cuda":
-            raise ValueError("the rows are made and read on the GPU: device %s is not a GPU "
-                             "device" % device)
-        self.guard = torch.cuda.device(device)
+        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+        self.other = None   # a stream that is not the device's current one
         if stream is None:
-            self.stream = torch.cuda.current_stream(device)
+            self.raw = torch.cuda.current_stream(index).cuda_stream
         elif isinstance(stream, int):
-            self.stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
-                torch.cuda.default_stream(device)
+            self.raw = stream
+            if stream != torch.cuda.current_stream(index).cuda_stream:
+                self.other = torch.cuda.ExternalStream(stream, device=index) if stream else \
+                    torch.cuda.default_stream(index)
         else:
-            if stream.device != device:
-                raise ValueError("the stream is on %s, the tensors on %s"
-                                 % (stream.device, device))
-            self.stream = stream
+            if stream.device.index != index:
+                raise ValueError("the stream is on %s, the tensors on GPU %d"
+                                 % (stream.device, index))
+            self.raw = stream.cuda_stream
+            self.other = stream
 
     def __enter__(self):
-        self.guard.__enter__()
-        return self.stream.cuda_stream
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.raw
 
     def __exit__(self, *a):
-        return self.guard.__exit__(*a)
+        if self.guard is not None:
+            return self.guard.__exit__(*a)
 
 
 def row_append(fmt, k, v, pool, pool_locs, rotation=None, positions=None, rows=None, q=None,
@@ -722,61 +735,62 @@ def row_append(fmt, k, v, pool, pool_locs, rotation=None, positions=None, rows=N
     ``q`` [T, heads, k_dim] are rotated into ``q_out`` (``q`` itself by default).
     One launch.  T is the length of ``pool_locs`` (of ``k`` without a pool)."""
     T = k.shape[0] if pool_locs is None else pool_locs.numel()
-    dev = k.device
+    dev = _device_index(k, "k")
     if q is not None and q_out is None:
         q_out = q
     _same_device(dev, v=v, pool=pool, pool_locs=pool_locs, rows=rows, q=q, q_out=q_out,
                  positions=positions, status=status,
                  inv_freq=None if rotation is None else rotation.inv_freq)
-    a = gpb_append()
-    a.n_rows = T
-    a.d_k = _ptr(k)
-    a.k_token_stride, a.k_head_stride = _heads(k, T, fmt.n_kv_heads, fmt.k_dim, fmt.dtype, "k")
+    dtype, kd = fmt.dtype, fmt.k_dim
+    k_ts, k_hs = _heads(k, T, fmt.n_kv_heads, kd, dtype, "k")
+    v_ptr = v_ts = v_hs = 0
     if not fmt.values_in_key:
         if v is None:
             raise ValueError("v: the row format holds values apart from the keys")
-        a.d_v = _ptr(v)
-        a.v_token_stride, a.v_head_stride = _heads(v, T, fmt.n_kv_heads, fmt.v_dim, fmt.dtype,
-                                                   "v")
+        v_ts, v_hs = _heads(v, T, fmt.n_kv_heads, fmt.v_dim, dtype, "v")
+        v_ptr = v.data_ptr()
     elif v is not None:
         raise ValueError("v: the row format holds the values in the keys")
+    pool_ptr = locs_ptr = n_pool_rows = rows_ptr = 0
     if pool is not None:
         if pool_locs is None:
             raise ValueError("pool_locs: a pool needs the rows to store at")
-        a.d_pool, a.n_pool_rows = _ptr(pool), _rows_of(pool, fmt.row_bytes, "pool")
-        a.d_pool_locs = _ptr(_int32(pool_locs, T, "pool_locs"))
+        pool_ptr, n_pool_rows = pool.data_ptr(), _rows_of(pool, fmt.row_bytes, "pool")
+        locs_ptr = _int32(pool_locs, T, "pool_locs")
     elif pool_locs is not None:
         raise ValueError("pool_locs without a pool")
     if rows is not None:
         if _rows_of(rows, fmt.row_bytes, "rows") < T:
             raise ValueError("rows: %d rows of %d bytes do not fit" % (T, fmt.row_bytes))
-        a.d_rows = _ptr(rows)
+        rows_ptr = rows.data_ptr()
+    heads = q_ptr = qo_ptr = q_ts = q_hs = qo_ts = qo_hs = 0
     if q is not None:
-        a.n_q_heads = q.shape[1] if q.dim() == 3 else 0
-        a.d_q, a.d_q_out = _ptr(q), _ptr(q_out)
-        a.q_token_stride, a.q_head_stride = _heads(q, T, a.n_q_heads, fmt.k_dim, fmt.dtype, "q")
-        a.qo_token_stride, a.qo_head_stride = _heads(q_out, T, a.n_q_heads, fmt.k_dim,
-                                                     fmt.dtype, "q_out")
-    if rotation is not None and rotation.inv_freq.numel():
+        heads = q.shape[1] if q.dim() == 3 else 0
+        q_ts, q_hs = _heads(q, T, heads, kd, dtype, "q")
+        qo_ts, qo_hs = _heads(q_out, T, heads, kd, dtype, "q_out")
+        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
+    if rotation is not None and rotation.pairs:
         if positions is None:
             raise ValueError("positions: a rotation needs them")
-        n = len(rotation.sections)
-        if positions.dim() == 1:
-            positions = positions.unsqueeze(0)
-        import torch
-        if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[0] != n \
-                or positions.shape[1] < T or (T > 1 and positions.stride(1) != 1):
+        n, shape = len(rotation.sections), positions.shape
+        stride = positions.stride()
+        if positions.dtype != rotation.index_dtype or len(shape) not in (1, 2) or \
+                (shape[0] if len(shape) == 2 else 1) != n or shape[-1] < T or \
+                (T > 1 and stride[-1] != 1):
             raise ValueError("positions: need int32 [%d, >= %d], got %s %s"
-                             % (n, T, positions.dtype, tuple(positions.shape)))
-        a.rot_start, a.rot_dim = rotation.start, 2 * rotation.inv_freq.numel()
-        a.interleaved, a.n_axes = int(rotation.interleaved), n
-        for i, s in enumerate(rotation.sections):
-            a.section[i] = s
-        a.d_inv_freq, a.d_positions = _ptr(rotation.inv_freq), _ptr(positions)
-        a.positions_stride = positions.stride(0)
+                             % (n, T, positions.dtype, tuple(shape)))
+        turn = (rotation.start, 2 * rotation.pairs, rotation.interleaved, n, rotation.c_sections,
+                rotation.inv_freq.data_ptr(), positions.data_ptr(),
+                stride[0] if len(shape) == 2 else 0)
+    else:
+        turn = ()
+    a = gpb_append(T, heads, k.data_ptr(), v_ptr, k_ts, k_hs, v_ts, v_hs, pool_ptr, n_pool_rows,
+                   locs_ptr, rows_ptr, q_ptr, qo_ptr, q_ts, q_hs, qo_ts, qo_hs, *turn)
     with _on(dev, stream) as st:
-        _check(lib.gpb_row_append(ctypes.byref(fmt.c), ctypes.byref(a), _ptr(status), st),
-               "gpb_row_append")
+        rc = lib.gpb_row_append(fmt.ref, ctypes.byref(a),
+                                None if status is None else status.data_ptr(), st)
+    if rc != OK:
+        _check(rc, "gpb_row_append")
 
 
 class AttendPlan:
@@ -815,6 +829,20 @@ class AttendPlan:
         self.device = torch.device("cuda", torch.cuda.current_device()) \
             if dev.index is None else dev
         self.list = torch.from_numpy(self.list_host).to(self.device)
+        self.list_ptr, self.ref = self.list.data_ptr(), ctypes.byref(self.c)
+
+    def room(self, out, lse, own_lse, workspace):
+        """Results and workspace of one call, where the caller has none."""
+        import torch
+        if out is None:
+            out = torch.empty(self.n_tokens, self.n_heads, self.fmt.v_dim, dtype=self.fmt.dtype,
+                              device=self.device)
+        if own_lse:
+            lse = torch.empty(self.n_tokens, self.n_heads, dtype=torch.float32,
+                              device=self.device)
+        if workspace is None and self.workspace_bytes:
+            workspace = self.workspace()
+        return out, lse, workspace
 
     def workspace(self):
         """A workspace for one call at a time."""
@@ -825,36 +853,34 @@ class AttendPlan:
 def _attend(plan, q, scale, out, lse, workspace, status, stream, call, what, **tensors):
     import torch
     fmt, T, dev = plan.fmt, plan.n_tokens, plan.device
-    _same_device(dev, q=q, out=out, lse=lse if torch.is_tensor(lse) else None,
-                 workspace=workspace, status=status, **tensors)
-    io = gpb_attend_io()
-    io.q_token_stride, io.q_head_stride = _heads(q, T, plan.n_heads, fmt.k_dim, fmt.dtype, "q")
-    io.scale = float(scale)
-    on = _on(dev, stream)
+    own_lse = lse is True
+    if lse is True or lse is False:
+        lse = None
+    _same_device(dev.index, q=q, out=out, lse=lse, workspace=workspace, status=status, **tensors)
+    q_ts, q_hs = _heads(q, T, plan.n_heads, fmt.k_dim, fmt.dtype, "q")
+    on = _on(dev.index, stream)
     with on as st:
-        # what is allocated here belongs to the stream the kernels run on
-        with torch.cuda.stream(on.stream):
-            if out is None:
-                out = torch.empty(T, plan.n_heads, fmt.v_dim, dtype=fmt.dtype, device=dev)
-            if lse is True:
-                lse = torch.empty(T, plan.n_heads, dtype=torch.float32, device=dev)
-            if workspace is None and plan.workspace_bytes:
-                workspace = plan.workspace()
-        io.out_token_stride, io.out_head_stride = _heads(out, T, plan.n_heads, fmt.v_dim,
-                                                         fmt.dtype, "out")
-        if torch.is_tensor(lse):
-            if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.dim() != 2 or \
-                    lse.shape[0] < T or lse.shape[1] != plan.n_heads:
-                raise ValueError("lse: need a contiguous float32 [>= %d, %d], got %s %s"
-                                 % (T, plan.n_heads, lse.dtype, tuple(lse.shape)))
-            io.d_lse = _ptr(lse)
-        else:
-            lse = None
-        io.d_q, io.d_out = _ptr(q), _ptr(out)
-        if workspace is not None and not workspace.is_contiguous():
-            raise ValueError("workspace: need a contiguous tensor")
-        n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(call(io, _ptr(workspace) if n else None, n, _ptr(status), st), what)
+        if out is None or own_lse or (workspace is None and plan.workspace_bytes):
+            if on.other is None:
+                out, lse, workspace = plan.room(out, lse, own_lse, workspace)
+            else:   # what is allocated here belongs to the stream the kernels run on
+                with torch.cuda.stream(on.other):
+                    out, lse, workspace = plan.room(out, lse, own_lse, workspace)
+        o_ts, o_hs = _heads(out, T, plan.n_heads, fmt.v_dim, fmt.dtype, "out")
+        if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
+                                lse.dim() != 2 or lse.shape[0] < T or
+                                lse.shape[1] != plan.n_heads):
+            raise ValueError("lse: need a contiguous float32 [>= %d, %d], got %s %s"
+                             % (T, plan.n_heads, lse.dtype, tuple(lse.shape)))
+        n = 0
+        if workspace is not None:
+            n = _rows_of(workspace, 1, "workspace")
+        io = gpb_attend_io(q.data_ptr(), q_ts, q_hs, out.data_ptr(), o_ts, o_hs,
+                           0 if lse is None else lse.data_ptr(), scale)
+        rc = call(ctypes.byref(io), workspace.data_ptr() if n else None, n,
+                  None if status is None else status.data_ptr(), st)
+    if rc != OK:
+        _check(rc, what)
     return out, lse
 
 
@@ -864,12 +890,11 @@ def attend_dense(plan, q, dense, k_bases, scale, out=None, lse=True, workspace=N
     a compose: key x of request r is row ``k_bases[r] + x`` of ``dense``.  Returns
     (out [T, heads, v_dim], lse [T, heads] float32, or None with ``lse=None``).
     Without a workspace one is allocated for the call."""
-    rows = _rows_of(dense, plan.fmt.row_bytes, "dense")
-    _int32(k_bases, plan.bs, "k_bases")
+    rows, bases = _rows_of(dense, plan.fmt.row_bytes, "dense"), _int32(k_bases, plan.bs, "k_bases")
     return _attend(plan, q, scale, out, lse, workspace, status, stream,
-                   lambda io, ws, n, st, s: lib.gpb_attend_dense(
-                       ctypes.byref(plan.c), _ptr(plan.list), ctypes.byref(io), _ptr(dense),
-                       rows, _ptr(k_bases), ws, n, st, s),
+                   lambda io, ws, n, word, st: lib.gpb_attend_dense(
+                       plan.ref, plan.list_ptr, io, dense.data_ptr(), rows, bases, ws, n, word,
+                       st),
                    "gpb_attend_dense", dense=dense, k_bases=k_bases)
 
 
@@ -880,17 +905,17 @@ def attend_paged(plan, q, pool, pages, scale, page_base=None, out=None, lse=True
     which request r's pages start at entry ``page_base[r]`` (a compose plan's
     slot_pages and slot_base).  Returns as attend_dense."""
     rows = _rows_of(pool, plan.fmt.row_bytes, "pool")
-    stride = 0
+    stride = base = 0
     if page_base is None:
         if pages.dim() != 2 or pages.shape[0] < plan.bs:
             raise ValueError("pages: need a table [>= %d, pages], got %s"
                              % (plan.bs, tuple(pages.shape)))
         stride = pages.shape[1]
     else:
-        _int32(page_base, plan.bs, "page_base")
-    _int32(pages, 0, "pages")
+        base = _int32(page_base, plan.bs, "page_base")
+    listed, table = pages.numel(), _int32(pages, 0, "pages")
     return _attend(plan, q, scale, out, lse, workspace, status, stream,
-                   lambda io, ws, n, st, s: lib.gpb_attend_paged(
-                       ctypes.byref(plan.c), _ptr(plan.list), ctypes.byref(io), _ptr(pool),
-                       rows, _ptr(pages), pages.numel(), _ptr(page_base), stride, ws, n, st, s),
+                   lambda io, ws, n, word, st: lib.gpb_attend_paged(
+                       plan.ref, plan.list_ptr, io, pool.data_ptr(), rows, table, listed,
+                       base or None, stride, ws, n, word, st),
                    "gpb_attend_paged", pool=pool, pages=pages, page_base=page_base)

@@ -44,4 +44,11 @@ inline int attend_kernel(const gpb_row_format &f) {
   return -1;
 }
 
+// Workgroups a CU holds of attention kernel `which`: the registers that a
+// wave's rows take allow one of latent rows and two of wide items; LDS two, and
+// more of narrow items alone.
+constexpr int blocks_per_cu(int which, bool narrow) {
+  return which == 2 ? 1 : which == 0 && narrow ? 3 : 2;
+}
+
 }  // namespace gpb

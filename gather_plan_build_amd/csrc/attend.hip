@@ -123,6 +123,10 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *base, uint64_t off, u
                  "v"(lane16), "n"(TO), "n"(X)
                : "s96", "s97", "scc");
 }
+// What the wave asked of LDS has arrived.
+__device__ __forceinline__ void lds_reads_done() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
 // All but the newest LEFT of the wave's loads have arrived.
 template <int LEFT = 0>
 __device__ __forceinline__ void loads_done() {
@@ -167,7 +171,8 @@ __device__ __forceinline__ constexpr int chunk_at(int r, int place) {
   return turned_back<ROW_BYTES>(place ^ row_bits<ROW_BYTES>(r));
 }
 
-template <typename T, int DK, int DV, bool IN_KEY>
+// NARROW: a kernel of narrow items alone, with the LDS of those.
+template <typename T, int DK, int DV, bool IN_KEY, bool NARROW>
 struct Attend {
   static constexpr int KB = DK * 2, VB = DV * 2;              // bytes of a key, a value
   // A tile of n keys in LDS: n rows of K0 bytes (a key, or the value part of a
@@ -177,7 +182,7 @@ struct Attend {
   // wide tiles under way or in use: a 64-wide head's are over too soon for one
   // to arrive meanwhile
   static constexpr int BUFS = DK == 64 ? 4 : 2;
-  static constexpr int TILES_LDS = BUFS * kWideTile * ROW;     // >= 4 * kNarrowTile * ROW
+  static constexpr int TILES_LDS = NARROW ? 4 * kNarrowTile * ROW : BUFS * kWideTile * ROW;
   static constexpr int WAVE_XCHG = 2048 + 128;                 // latent: a wave's weights, maxima
   static constexpr int RING = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kWideRows);
   static constexpr int LDS = RING + 4096;
@@ -250,11 +255,12 @@ struct Attend {
     return (v < it.n_first ? it.tile0 + v : it.tile1 + v - it.n_first) * tile;
   }
 
-  // Wide tiles: the page numbers of a tile come through LDS as its rows do,
-  // AHEAD tiles before those are asked for, so that no wait for a page number
-  // is a wait for the loads of rows behind it.  A wave has places for four
-  // tiles.
-  static constexpr int AHEAD = BUFS - 1;
+  // The places of a wave's keys of tiles of TILE, of which it loads KEYS.  Page
+  // numbers come through LDS as the rows do, some tiles before those are asked
+  // for, so that no wait for a page number is a wait for the loads of rows
+  // behind it.  A wave has room for four tiles' numbers.
+  static constexpr int AHEAD = BUFS - 1;  // wide tiles asked for before their turn
+  template <int TILE, int KEYS>
   struct Rows : Source {
     const AttendItem &it;
     lds_u8 *ring;
@@ -262,20 +268,22 @@ struct Attend {
 
     __device__ __forceinline__ Rows(const AttendArgs &a, const AttendItem &it, lds_u8 *lds,
                                     int wave, int lane)
-        : Source(a, it), it(it), ring(lds + RING + wave * 1024), mine(wave * 16 + (lane & 15)) {}
+        : Source(a, it), it(it), ring(lds + RING + wave * 1024),
+          mine((TILE == KEYS ? 0 : wave * KEYS) + lane % KEYS) {}
     // A tile's loads go out with the products of an earlier one; where no tile
     // follows they all read one row, which costs less than a second form of
     // the products without them.
     __device__ __forceinline__ int key(int v) const {
-      return v < it.n_tiles ? first_key(it, v, kWideTile) + mine : this->lo;
+      return v < it.n_tiles ? first_key(it, v, TILE) + mine : this->lo;
     }
-    __device__ __forceinline__ void ask(int v) const {
-      if (this->pages) load4_to_lds(this->place(key(v)), ring + (v & 3) * 256);
+    // For the page numbers of tile v in room `slot`.
+    __device__ __forceinline__ void ask(int v, int slot) const {
+      if (this->pages) load4_to_lds(this->place(key(v)), ring + (slot & 3) * 256);
     }
-    __device__ __forceinline__ uint64_t row(int v, int lane) const {
+    __device__ __forceinline__ uint64_t row(int v, int slot, int lane) const {
       typedef __attribute__((address_space(3))) int lds_int;
       return this->offset(key(v),
-                          this->pages ? ((const lds_int *)(ring + (v & 3) * 256))[lane] : 0);
+                          this->pages ? ((const lds_int *)(ring + (slot & 3) * 256))[lane] : 0);
     }
   };
 
@@ -322,11 +330,11 @@ struct Attend {
         }
       }
     }
-    template <int I = 0>
+    template <int I = 0, int END = N>
     __device__ __forceinline__ void all() const {
-      if constexpr (I < N) {
+      if constexpr (I < END) {
         issue<I>();
-        all<I + 1>();
+        all<I + 1, END>();
       }
     }
   };
@@ -559,31 +567,26 @@ struct Attend {
       for (int i = 0; i < 16; ++i) o[t][i] *= f;
   }
 
-  // A tile of 32 * NB keys, the first at position key0.
-  template <int NB, typename L>
-  static __device__ __forceinline__ void keys(const AttendArgs &a, const AttendItem &it,
-                                              const x8 *q, const lds_u8 *tile, const Places &w,
-                                              int key0, bool whole, const Sight &see, State &st,
-                                              int lane, const L &next) {
-    f32x16 s[NB];
-    s[0] = products<32 * NB, 0, 2>(q, tile, 0, w, next);
-    if constexpr (NB == 2) s[1] = products<32 * NB, DK / 32, 2>(q, tile, 32, w, next);
+  // The weights of 32 * NB keys from their products, the first at position
+  // key0, as operands p; the sums so far brought to their m.
+  template <int NB>
+  static __device__ __forceinline__ void weigh(const AttendArgs &a, const AttendItem &it,
+                                               f32x16 *s, int key0, bool whole, const Sight &see,
+                                               State &st, int half, x8 *p) {
     if (!whole) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) mask(a, it, see, key0 + 32 * b, lane >> 5, s[b]);
+      for (int b = 0; b < NB; ++b) mask(a, it, see, key0 + 32 * b, half, s[b]);
     }
     float top = largest(s[0]);
     if constexpr (NB == 2) top = fmaxf(top, largest(s[1]));
     top *= a.c;
-    const float m = next_m(st.m, fmaxf(top, other_half(top, lane >> 5)));
+    const float m = next_m(st.m, fmaxf(top, other_half(top, half)));
     if (__any(m > st.m)) {
       rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(st.m - finite_m(m)));
       st.m = m;
     }
-    x8 p[2 * NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) st.l += weights(s[b], a.c, m, p + 2 * b);
-    add_values<2 * NB, NT, 0>(p, tile + 32 * NB * R0, w, 0, st.o, NoLoader());
   }
 
   static __device__ __forceinline__ bool whole_tile(const AttendArgs &a, const AttendItem &it,
@@ -751,7 +754,7 @@ struct Attend {
     const int row = wave * 32 + (lane & 31), half = lane >> 5;
     constexpr int BUF = kWideTile * ROW;
     typedef Loader<kWideTile, 4> Load;
-    const Rows rows(a, it, lds, wave, lane);
+    const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
     x8 q[DK / 16];
     int pos;
     load_queries(a, it, row, half, q, &pos);
@@ -763,12 +766,12 @@ struct Attend {
     bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
 #pragma unroll
-      for (int v = 0; v < AHEAD; ++v) rows.ask(v);
+      for (int v = 0; v < AHEAD; ++v) rows.ask(v, v);
       loads_done();
 #pragma unroll
       for (int v = 0; v < AHEAD; ++v) {
-        Load(a, it, rows, rows.row(v, lane), lds + v * BUF, wave, lane).all();
-        rows.ask(v + AHEAD);
+        Load(a, it, rows, rows.row(v, v, lane), lds + v * BUF, wave, lane).all();
+        rows.ask(v + AHEAD, v + AHEAD);
       }
       for (int v = 0; v < it.n_tiles; ++v) {
         loads_done<(BUFS - 2) * Load::N>();
@@ -779,11 +782,18 @@ struct Attend {
         const bool odd = SCAN && !whole &&
                          __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const Load load(a, it, rows, rows.row(v + AHEAD, lane), lds + (v + AHEAD) % BUFS * BUF, wave,
+        const Load load(a, it, rows, rows.row(v + AHEAD, v + AHEAD, lane), lds + (v + AHEAD) % BUFS * BUF, wave,
                         lane);
-        rows.ask(v + 2 * AHEAD);
-        if (odd) load.all();
-        else keys<2>(a, it, q, now, w, key0, whole, see, st, lane, load);
+        rows.ask(v + 2 * AHEAD, v + 2 * AHEAD);
+        if (odd) {
+          load.all();
+          continue;
+        }
+        f32x16 s[2] = {products<kWideTile, 0, 2>(q, now, 0, w, load),
+                       products<kWideTile, DK / 32, 2>(q, now, 32, w, load)};
+        x8 p[4];
+        weigh<2>(a, it, s, key0, whole, see, st, half, p);
+        add_values<4, NT, 0>(p, now + kWideTile * R0, w, 0, st.o, NoLoader());
       }
       loads_done();
     }
@@ -813,7 +823,7 @@ struct Attend {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int part = wave & 1, half = lane >> 5;
     const int row = (wave >> 1) * 32 + (lane & 31);
-    const Rows rows(a, it, lds, wave, lane);
+    const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
     const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
     constexpr int BUF = kWideTile * ROW;
     lds_u8 *mine = lds + TILES_LDS + wave * WAVE_XCHG;
@@ -831,10 +841,10 @@ struct Attend {
     bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
       typedef Loader<kWideTile, 4> Load;
-      rows.ask(0);
+      rows.ask(0, 0);
       loads_done();
-      Load(a, it, rows, rows.row(0, lane), lds, wave, lane).all();
-      rows.ask(1);
+      Load(a, it, rows, rows.row(0, 0, lane), lds, wave, lane).all();
+      rows.ask(1, 1);
       for (int v = 0; v < it.n_tiles; ++v) {
         loads_done();
         __syncthreads();
@@ -844,8 +854,8 @@ struct Attend {
         const bool odd =
             SCAN && !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const Load load(a, it, rows, rows.row(v + 1, lane), lds + (~v & 1) * BUF, wave, lane);
-        rows.ask(v + 2);
+        const Load load(a, it, rows, rows.row(v + 1, v + 1, lane), lds + (~v & 1) * BUF, wave, lane);
+        rows.ask(v + 2, v + 2);
         if (odd || idle) {
           load.all();
           if (!odd) __syncthreads();
@@ -853,14 +863,8 @@ struct Attend {
         }
         x8 p[2];
         f32x16 s = products<kWideTile, 0, 3>(q, now, 32 * part, w, load);
-        if (!whole) mask(a, it, see, key0 + 32 * part, half, s);
-        const float top = largest(s) * a.c;
-        const float m = next_m(st.m, fmaxf(top, other_half(top, half)));
-        if (__any(m > st.m)) {
-          rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(st.m - finite_m(m)));
-          st.m = m;
-        }
-        st.l += weights(s, a.c, m, p);
+        weigh<1>(a, it, &s, key0 + 32 * part, whole, see, st, half, p);
+        const float m = st.m;
         ((lds8 *)mine)[lane] = p[0];
         ((lds8 *)mine)[64 + lane] = p[1];
         if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
@@ -910,32 +914,58 @@ struct Attend {
     const int row = lane & 31, half = lane >> 5;
     x8 q[DK / 16];
     int pos;
+    const Rows<kNarrowTile, kNarrowTile> rows(a, it, lds, wave, lane);
+    if (wave < it.n_tiles) {
+      rows.ask(wave, 0);
+      rows.ask(wave + 4, 1);
+    }
     load_queries(a, it, row, half, q, &pos);
     Places w;
     find_places(w, lane);
     const Sight see = sight(a, it, pos);
     State st;
-    const Source from(a, it);
     lds_u8 *own = lds + wave * kNarrowTile * ROW;
     typedef __attribute__((address_space(3))) float lds_float;
     lds_float *slot = (lds_float *)lds;
     constexpr int SLOT = (NT * 16 + 2) * 64;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
-    int next = first_key(it, wave, kNarrowTile) + (lane & 31);
-    int page = wave < it.n_tiles && from.pages ? *from.place(next) : 0;
-    for (int v = wave; v < it.n_tiles; v += 4) {
-      const uint64_t off = from.offset(next, page);
-      next = first_key(it, min(v + 4, it.n_tiles - 1), kNarrowTile) + (lane & 31);
-      if (from.pages) page = *from.place(next);
-      Loader<kNarrowTile, 1>(a, it, from, off, own, 0, lane).all();
+    if (wave < it.n_tiles) {
+      typedef Loader<kNarrowTile, 1> Load;
       loads_done();
-      const int key0 = first_key(it, v, kNarrowTile);
-      const bool whole = whole_tile(a, it, key0, kNarrowTile);
-      if (SCAN && !whole && __any(odd_values<kNarrowTile>(own, lane, 64))) left = true;
-      else keys<1>(a, it, q, own, w, key0, whole, see, st, lane, NoLoader());
-      // the tile has been read before the next one's loads overwrite it
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      Load(a, it, rows, rows.row(wave, 0, lane), own, 0, lane).all();
+      int n = 0;  // tiles of the wave so far
+      for (int v = wave; v < it.n_tiles; v += 4, ++n) {
+        const int key0 = first_key(it, v, kNarrowTile);
+        const bool whole = whole_tile(a, it, key0, kNarrowTile);
+        if constexpr (SCAN) loads_done();
+        else loads_done<Load::N1>();  // the keys; the values may be on their way
+        if (SCAN && !whole && __any(odd_values<kNarrowTile>(own, lane, 64))) {
+          left = true;
+          rows.ask(v + 8, n + 2);
+          lds_reads_done();
+          Load(a, it, rows, rows.row(v + 4, n + 1, lane), own, 0, lane).all();
+          continue;
+        }
+        f32x16 s = products<kNarrowTile, 0, 1>(q, own, 0, w, NoLoader());
+        // the keys have been read: the next ones' loads may overwrite them
+        const bool more = v + 4 < it.n_tiles;
+        const Load load(a, it, rows, rows.row(v + 4, n + 1, lane), own, 0, lane);
+        lds_reads_done();
+        if (more) {
+          rows.ask(v + 8, n + 2);
+          load.template all<0, Load::N0>();
+        }
+        x8 p[2];
+        weigh<1>(a, it, &s, key0, whole, see, st, half, p);
+        if (!more) loads_done();
+        else if (rows.pages) loads_done<Load::N0 + 1>();
+        else loads_done<Load::N0>();
+        add_values<2, NT, 0>(p, own + kNarrowTile * R0, w, 0, st.o, NoLoader());
+        lds_reads_done();
+        if (more) load.template all<Load::N0, Load::N>();
+      }
+      loads_done();
     }
     float l = st.l + other_half(st.l, half);
 
@@ -985,6 +1015,7 @@ struct Attend {
   static __device__ __forceinline__ bool item(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
     if constexpr (IN_KEY) return latent<SCAN>(a, it, lds);
+    else if constexpr (NARROW) return narrow<SCAN>(a, it, lds);
     else return it.wide ? wide<SCAN>(a, it, lds) : narrow<SCAN>(a, it, lds);
   }
   // Apart, so that the registers of the common case are allotted without it.
@@ -993,9 +1024,9 @@ struct Attend {
   }
 };
 
-template <typename T, int DK, int DV, bool IN_KEY>
-__global__ __launch_bounds__(256, IN_KEY ? 1 : 2) void k_attend(AttendArgs a) {
-  typedef Attend<T, DK, DV, IN_KEY> A;
+template <typename T, int DK, int DV, bool IN_KEY, bool NARROW>
+__global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128, NARROW)) void k_attend(AttendArgs a) {
+  typedef Attend<T, DK, DV, IN_KEY, NARROW> A;
   __shared__ __attribute__((aligned(1024))) uint8_t memory[A::LDS];
   lds_u8 *lds = (lds_u8 *)memory;
   const AttendItem it = reinterpret_cast<const AttendItem *>(a.list)[blockIdx.x];
@@ -1004,6 +1035,7 @@ __global__ __launch_bounds__(256, IN_KEY ? 1 : 2) void k_attend(AttendArgs a) {
   const int64_t all = static_cast<int64_t>(a.n_tokens) * a.G;
   const bool ok = it.req >= 0 && it.req < a.bs && it.row0 >= 0 && it.n_rows >= 1 &&
                   it.n_rows <= (IN_KEY ? kLatentRows : it.wide ? kWideRows : kNarrowRows) &&
+                  !(NARROW && it.wide) &&
                   it.row0 + it.n_rows <= all &&
                   it.kv_head >= 0 && it.kv_head < a.hkv && it.key_lo >= 0 &&
                   it.key_lo <= it.key_hi && it.key_hi <= a.max_keys &&
@@ -1020,62 +1052,95 @@ __global__ __launch_bounds__(256, IN_KEY ? 1 : 2) void k_attend(AttendArgs a) {
 }
 
 // The rows of one token and KV head: parts weighted by 2^(m - max m), in the
-// order of the list.  A wave a row, a lane DV / 64 values.
+// order of the list.  A wave a row; a lane first takes a part's m and l, then
+// DV / 64 values of every part.
 template <typename T, int DV>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+  typedef Attend<T, 64, 64, false, false> A;  // for what depends on T alone
   const AttendJoin j = reinterpret_cast<const AttendJoin *>(a.list + a.joins_at)[blockIdx.x];
-  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int lane = threadIdx.x & 63, r = blockIdx.y * 4 + wave_id();
   constexpr int PER = DV / 64;
+  typedef float Values __attribute__((ext_vector_type(PER)));
   bool ok = j.row0 >= 0 && j.n_rows >= 1 && j.n_rows <= kNarrowRows &&
             static_cast<int64_t>(j.row0) + j.n_rows <= static_cast<int64_t>(a.n_tokens) * a.G &&
             j.kv_head >= 0 && j.kv_head < a.hkv && j.ref0 >= 0 && j.n_refs >= 1 &&
             j.ref0 <= a.n_refs - j.n_refs;
   const int32_t *refs = a.list + a.refs_at + (ok ? j.ref0 : 0);
-  for (int i = lane; ok && i < j.n_refs; i += 64)
+  const int n = ok ? j.n_refs : 0;
+  float top = -INFINITY;
+  if (ok && r >= j.n_rows) return;
+  for (int i = lane; i < n; i += 64) {
     if (refs[i] < 0 || refs[i] > a.n_partial_rows - j.n_rows) ok = false;
+    else top = fmaxf(top, a.ml[2 * (static_cast<int64_t>(refs[i]) + r)]);
+  }
   if (__any(!ok)) {
-    if (threadIdx.x == 0 && a.status) atomicOr(a.status, GPB_STATUS_BAD_PLAN_INPUT);
+    if (lane == 0 && a.status) atomicOr(a.status, GPB_STATUS_BAD_PLAN_INPUT);
     return;
   }
-  typedef Attend<T, 64, 64, false> A;  // for what depends on T alone
-  for (int r = wave; r < j.n_rows; r += 4) {
-    float top = -INFINITY;
-    for (int i = 0; i < j.n_refs; ++i)
-      top = fmaxf(top, a.ml[2 * (static_cast<int64_t>(refs[i]) + r)]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f, o[PER] = {};
-    for (int i = 0; i < j.n_refs; ++i) {
-      const int64_t at = static_cast<int64_t>(refs[i]) + r;
-      const f32x2 ml = *reinterpret_cast<const f32x2 *>(a.ml + 2 * at);
-      const float f = __builtin_amdgcn_exp2f(ml[0] - ref);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  const float ref = A::finite_m(top);
+  float l = 0.0f;
+  Values o = {};
+  for (int i0 = 0; i0 < n; i0 += 64) {
+    int at = refs[min(i0 + lane, n - 1)] + r;
+    float f = 0.0f;
+    if (i0 + lane < n) {
+      const f32x2 ml = *reinterpret_cast<const f32x2 *>(a.ml + 2 * static_cast<int64_t>(at));
+      f = __builtin_amdgcn_exp2f(ml[0] - ref);
       l += ml[1] * f;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] += a.sums[at * DV + lane * PER + e] * f;
     }
-    const int g = j.row0 + r;
-    const int t = g / a.G, h = g - t * a.G + j.kv_head * a.G;
-    const float inv = A::inverse(l);
-    T *dst = reinterpret_cast<T *>(a.out + t * a.o_ts + h * a.o_hs) + lane * PER;
+    const int some = min(64, n - i0);
+    for (int i = 0; i < some; i += 4) {  // four parts' values under way at once
+      Values x[4];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(o[e] * inv);
-    if (lane == 0 && a.lse)
-      a.lse[static_cast<int64_t>(t) * a.n_heads + h] = A::log_sum(top, l);
+      for (int u = 0; u < 4; ++u)
+        x[u] = *reinterpret_cast<const Values *>(
+            a.sums + static_cast<int64_t>(__builtin_amdgcn_readlane(at, min(i + u, some - 1))) * DV +
+            lane * PER);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u < some)
+          o += x[u] * __builtin_bit_cast(
+                          float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), i + u));
+    }
   }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d, 64);
+  const int g = j.row0 + r;
+  const int t = g / a.G, h = g - t * a.G + j.kv_head * a.G;
+  const float inv = A::inverse(l);
+  typedef T Out __attribute__((ext_vector_type(PER > 4 ? 4 : PER)));
+  T *dst = reinterpret_cast<T *>(a.out + t * a.o_ts + h * a.o_hs) + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; e += PER > 4 ? 4 : PER) {
+    Out x;
+#pragma unroll
+    for (int y = 0; y < (PER > 4 ? 4 : PER); ++y) x[y] = static_cast<T>(o[e + y] * inv);
+    *reinterpret_cast<Out *>(dst + e) = x;
+  }
+  if (lane == 0 && a.lse) a.lse[static_cast<int64_t>(t) * a.n_heads + h] = A::log_sum(top, l);
 }
 
 template <typename T, int DK, int DV, bool IN_KEY>
-int launch_attend(const AttendArgs &a, hipStream_t st) {
-  int rc = launch(k_attend<T, DK, DV, IN_KEY>, dim3(a.n_items), dim3(256), st, a);
+int launch_attend(const AttendArgs &a, bool narrow, hipStream_t st) {
+  const dim3 items(a.n_items), block(256);
+  int rc;
+  if constexpr (IN_KEY) rc = launch(k_attend<T, DK, DV, true, false>, items, block, st, a);
+  else rc = narrow ? launch(k_attend<T, DK, DV, false, true>, items, block, st, a)
+                   : launch(k_attend<T, DK, DV, false, false>, items, block, st, a);
   if (rc == GPB_OK && a.n_joins > 0)
-    rc = launch(k_attend_join<T, DV>, dim3(a.n_joins), dim3(256), st, a);
+    rc = launch(k_attend_join<T, DV>,
+                dim3(a.n_joins, static_cast<uint32_t>(std::min(a.G, kNarrowRows) + 3) / 4), block,
+                st, a);
   return rc;
 }
 
 template <typename T>
-int launch_format(int which, const AttendArgs &a, hipStream_t st) {
-  if (which == 0) return launch_attend<T, 64, 64, false>(a, st);
-  if (which == 1) return launch_attend<T, 128, 128, false>(a, st);
-  return launch_attend<T, 576, 512, true>(a, st);
+int launch_format(int which, const AttendArgs &a, bool narrow, hipStream_t st) {
+  if (which == 0) return launch_attend<T, 64, 64, false>(a, narrow, st);
+  if (which == 1) return launch_attend<T, 128, 128, false>(a, narrow, st);
+  return launch_attend<T, 576, 512, true>(a, narrow, st);
 }
 
 int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io *io,
@@ -1087,7 +1152,7 @@ int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io 
   if (rc != GPB_OK) return rc;
   const int which = attend_kernel(p->format);
   if (which < 0 || p->bs < 0 || p->n_heads < 1 || p->n_heads % p->format.n_kv_heads ||
-      p->n_tokens < 0 || p->max_keys < 0 || p->n_items < 0 || p->n_joins < 0 || p->n_refs < 0 ||
+      p->n_tokens < 0 || p->max_keys < 0 || p->n_items < 0 || p->n_wide < 0 || p->n_joins < 0 || p->n_refs < 0 ||
       p->n_partial_rows < 0 || p->window < 0 || p->sinks < 0 || p->page_rows < 1 ||
       p->list_ints < 0)
     return GPB_EINVAL;
@@ -1151,8 +1216,10 @@ int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io 
   a.n_items = p->n_items; a.n_joins = p->n_joins; a.n_refs = p->n_refs;
   a.n_partial_rows = p->n_partial_rows;
   a.joins_at = p->joins_at; a.refs_at = p->refs_at; a.positions_at = p->positions_at;
-  return p->format.dtype == GPB_BF16 ? launch_format<__bf16>(which, a, as_stream(stream))
-                                     : launch_format<_Float16>(which, a, as_stream(stream));
+  const bool narrow = p->n_wide == 0;
+  return p->format.dtype == GPB_BF16
+             ? launch_format<__bf16>(which, a, narrow, as_stream(stream))
+             : launch_format<_Float16>(which, a, narrow, as_stream(stream));
 }
 
 }  // namespace

@@ -10,6 +10,7 @@
 // its parts in the order of the list, so results do not depend on timing.
 #include <algorithm>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "attend.h"
@@ -17,8 +18,6 @@
 namespace gpb {
 namespace {
 
-// Workgroups the GPU holds at once: 256 CUs, two workgroups each of the
-// 64- and 128-wide heads (64 KiB of LDS), one of the latent rows (153 KiB).
 constexpr int kCus = 256;
 
 struct Block {
@@ -185,22 +184,71 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
                   grouped);
   }
 
-  // Cut long ranges of keys: no part longer than the batch's keys spread over
-  // the workgroups the GPU holds, none shorter than min_keys (a part's sums
-  // are written and read again, and its workgroup has a start).
-  const int64_t slots = which == 2 ? kCus : 2 * kCus, min_keys = 256;
-  int64_t total = 0;
+  // Cut long ranges of keys into parts of at most `most` keys, none shorter
+  // than min_keys.  A workgroup's start and end take as long as `start` keys.
+  bool any_wide = false;
+  int64_t total = 0, uncut = 0, longest_block = 1;
   for (const Segment &g : p.segments)
-    for (size_t k = 0; k < g.n_blocks; ++k)
-      total += hkv * p.tile_of(g.wide) * p.blocks[g.block0 + k].n_tiles;
-  const int64_t most = std::max(min_keys, ceil_div64(total, slots));
+    for (size_t k = 0; k < g.n_blocks; ++k) {
+      const int64_t keys = static_cast<int64_t>(p.tile_of(g.wide)) * p.blocks[g.block0 + k].n_tiles;
+      total += hkv * keys;
+      uncut += hkv;
+      longest_block = std::max(longest_block, keys);
+      any_wide |= g.wide;
+    }
+  const int64_t slots = kCus * blocks_per_cu(which, !any_wide);
+  const int64_t min_keys = any_wide ? 256 : 128, start = which == 2 ? 150 : 300;
+  auto cut = [&](const Segment &g, const Block &b, int64_t most) {
+    const int64_t keys = static_cast<int64_t>(b.n_tiles) * p.tile_of(g.wide);
+    return std::max<int64_t>(1, std::min<int64_t>(b.n_tiles, ceil_div64(keys, most)));
+  };
+  // How long the batch takes if its workgroups start the longest first: the
+  // longest one where all run at once; else all of them spread evenly, and the
+  // longest of those that had to wait, which starts when the rest end.  Sums
+  // written and read again take the whole GPU about a key's time (33 ns) per
+  // 19,000 values.
+  std::vector<std::pair<int64_t, int64_t>> lengths;  // keys, how many
+  auto span = [&](int64_t most) {
+    lengths.clear();
+    int64_t n = 0, sum = 0, longest = 0, rows = 0;
+    for (const Segment &g : p.segments)
+      for (size_t k = 0; k < g.n_blocks; ++k) {
+        const Block &b = p.blocks[g.block0 + k];
+        const int64_t parts = cut(g, b, most);
+        const int64_t keys = static_cast<int64_t>(b.n_tiles) * p.tile_of(g.wide) / parts + start;
+        lengths.emplace_back(keys, hkv * parts);
+        n += hkv * parts;
+        sum += hkv * parts * keys;
+        longest = std::max(longest, keys);
+        if (g.grouped || parts > 1) rows += hkv * parts * b.n_rows;
+      }
+    const int64_t again = rows * f->v_dim / 19000;
+    if (n <= slots) return longest + again;
+    std::sort(lengths.rbegin(), lengths.rend());
+    int64_t before = 0, waits = 0;
+    for (const auto &l : lengths) {
+      waits = l.first;
+      before += l.second;
+      if (before > slots) break;
+    }
+    return std::max(longest, sum / slots + waits) + again;
+  };
+  int64_t most = std::max(min_keys, ceil_div64(total, slots));
+  if (uncut <= 4 * slots) {
+    int64_t best = INT64_MAX;
+    const int64_t even = most;
+    for (int64_t part : {even / 2, even * 2 / 3, even, even * 9 / 8, even * 5 / 4, even * 3 / 2,
+                         even * 2, even * 3, longest_block}) {
+      part = std::max(min_keys, part);
+      const int64_t t = span(part);
+      if (t < best) best = t, most = part;
+    }
+  }
   int64_t n_items = 0, n_partial = 0, n_joins = 0, n_refs = 0;
   for (const Segment &g : p.segments)
     for (size_t k = 0; k < g.n_blocks; ++k) {
       Block &b = p.blocks[g.block0 + k];
-      const int64_t keys = static_cast<int64_t>(b.n_tiles) * p.tile_of(g.wide);
-      b.parts = static_cast<int32_t>(
-          std::max<int64_t>(1, std::min<int64_t>(b.n_tiles, ceil_div64(keys, most))));
+      b.parts = static_cast<int32_t>(cut(g, b, most));
       b.partial = -1;
       if (g.grouped || b.parts > 1) {
         b.partial = n_partial;
@@ -253,6 +301,9 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
   plan->n_tokens = static_cast<int32_t>(tokens);
   plan->max_keys = static_cast<int32_t>(longest);
   plan->n_items = static_cast<int32_t>(n_items);
+  for (const Segment &g : p.segments)
+    for (size_t k = 0; g.wide && k < g.n_blocks; ++k)
+      plan->n_wide += static_cast<int32_t>(hkv * p.blocks[g.block0 + k].parts);
   plan->n_joins = static_cast<int32_t>(n_joins);
   plan->n_refs = static_cast<int32_t>(n_refs);
   plan->n_partial_rows = static_cast<int32_t>(n_partial);

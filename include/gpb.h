@@ -662,7 +662,7 @@ typedef struct gpb_attend_plan {
   int32_t bs, n_heads, window, sinks, page_rows, n_groups;
   int32_t n_tokens;             /* queries of the batch                        */
   int32_t max_keys;             /* longest kv_lens                             */
-  int32_t n_items, n_joins, n_refs, n_partial_rows;
+  int32_t n_items, n_wide, n_joins, n_refs, n_partial_rows;
   int32_t joins_at, refs_at, positions_at;  /* int32 offsets in the list       */
   int32_t list_ints;            /* int32 values of the whole list              */
   int64_t workspace_bytes;
