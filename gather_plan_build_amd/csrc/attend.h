@@ -29,11 +29,14 @@ struct AttendJoin {
 constexpr int kItemInts = sizeof(AttendItem) / 4;
 constexpr int kJoinInts = sizeof(AttendJoin) / 4;
 
-// A wide item's four waves take 32 query rows each of one tile of 64 keys; a
-// narrow item's four waves hold the same 32 rows or fewer, each over tiles of
-// 32 keys of its own.  Over latent rows every item is wide and has 64 rows,
-// two waves to each 32 of them.
-constexpr int kWideRows = 128, kNarrowRows = 32, kLatentRows = 64;
+// Query rows of an item of attention kernel `which` (0: 64-wide heads, 1: 128,
+// 2: latent rows).  A wide item's four waves take a quarter of the rows each of
+// one tile of 64 keys (over latent rows two waves share a half); a narrow
+// item's four waves hold the same rows, each over tiles of 32 keys of its own.
+constexpr int kNarrowRows = 32;
+constexpr int rows_of(int which, bool wide) {
+  return which == 2 ? 64 : !wide ? kNarrowRows : which == 0 ? 256 : 128;
+}
 constexpr int kWideTile = 64, kNarrowTile = 32;
 
 // Which attention kernel a format has, or -1.

@@ -184,7 +184,8 @@ struct Attend {
   static constexpr int BUFS = DK == 64 ? 4 : 2;
   static constexpr int TILES_LDS = NARROW ? 4 * kNarrowTile * ROW : BUFS * kWideTile * ROW;
   static constexpr int WAVE_XCHG = 2048 + 128;                 // latent: a wave's weights, maxima
-  static constexpr int RING = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kWideRows);
+  static constexpr int kRows = rows_of(IN_KEY ? 2 : DK / 128, !NARROW);  // of an item, at most
+  static constexpr int RING = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kRows);
   static constexpr int LDS = RING + 4096;
   static constexpr int NT = DV / 32 / (IN_KEY ? 2 : 1);        // output tiles of a wave
   // chunks among which a row's are moved, and steps of 16 values they make
@@ -406,31 +407,32 @@ struct Attend {
                            (d - D0) / (G1 / 2) * G1 * 16);
   }
 
-  // q.k of the 32 keys in LDS rows row0 .. of a tile of TILE and the lane's
-  // query row; with every EVERY steps one of the next tile's loads goes out,
+  // q.k of the 32 keys in LDS rows row0 .. of a tile of TILE and RH query rows
+  // of the lane; with every EVERY steps one of the next tile's loads goes out,
   // the first FIRST.
-  template <int TILE, int FIRST, int EVERY, typename L>
-  static __device__ __forceinline__ f32x16 products(const x8 *q, const lds_u8 *tile, int row0,
-                                                    const Places &w, const L &next) {
+  template <int TILE, int FIRST, int EVERY, int RH = 1, typename L>
+  static __device__ __forceinline__ void products(const x8 *q, const lds_u8 *tile, int row0,
+                                                  const Places &w, const L &next, f32x16 *s) {
     constexpr int AHEAD = DK / 16 < 6 ? DK / 16 : 6;
     x8 k[AHEAD];
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) k[d] = key_operand<TILE>(tile, row0, w, d);
-    f32x16 s = {};
-    product_steps<TILE, FIRST, EVERY, 0, AHEAD>(q, tile, row0, w, next, k, s);
-    return s;
+#pragma unroll
+    for (int r = 0; r < RH; ++r) s[r] = f32x16{};
+    product_steps<TILE, FIRST, EVERY, RH, 0, AHEAD>(q, tile, row0, w, next, k, s);
   }
-  template <int TILE, int FIRST, int EVERY, int D, int AHEAD, typename L>
+  template <int TILE, int FIRST, int EVERY, int RH, int D, int AHEAD, typename L>
   static __device__ __forceinline__ void product_steps(const x8 *q, const lds_u8 *tile, int row0,
                                                        const Places &w, const L &next, x8 *k,
-                                                       f32x16 &s) {
+                                                       f32x16 *s) {
     if constexpr (D < DK / 16) {
-      s = mma<T>(k[D % AHEAD], q[D], s);
+#pragma unroll
+      for (int r = 0; r < RH; ++r) s[r] = mma<T>(k[D % AHEAD], q[r * (DK / 16) + D], s[r]);
       if constexpr (D + AHEAD < DK / 16)
         k[D % AHEAD] = key_operand<TILE>(tile, row0, w, D + AHEAD);
       if constexpr (D % EVERY == EVERY - 1) next.template issue<FIRST + D / EVERY>();
       in_order();
-      product_steps<TILE, FIRST, EVERY, D + 1, AHEAD>(q, tile, row0, w, next, k, s);
+      product_steps<TILE, FIRST, EVERY, RH, D + 1, AHEAD>(q, tile, row0, w, next, k, s);
     }
   }
 
@@ -498,30 +500,32 @@ struct Attend {
     return (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 
-  // Sums of N output tiles (values 32 t0 ..) += weights of 16 * NP keys (LDS
-  // rows 0 .. of v); with every second step one of the next tile's loads from
-  // FIRST on goes out.
-  template <int NP, int N, int FIRST, typename L>
+  // Sums of N output tiles (values 32 t0 ..) of RH rows += weights p of 16 * NP
+  // keys (LDS rows 0 .. of v); with every second step one of the next tile's
+  // loads from FIRST on goes out.
+  template <int NP, int N, int FIRST, int RH = 1, typename L>
   static __device__ __forceinline__ void add_values(const x8 *p, const lds_u8 *v, const Places &w,
-                                                    int t0, f32x16 *o, const L &next) {
+                                                    int t0, State *st, const L &next) {
     constexpr int AHEAD = 4;
     const lds_u8 *at = v + t0 / (VG / 4) * VG * 16;
     x8 x[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) x[i] = value_operand(at, w, i / N * 16, i % N);
-    value_steps<NP * N, N, FIRST, 0, AHEAD>(p, at, w, o, next, x);
+    value_steps<NP, N, FIRST, RH, 0, AHEAD>(p, at, w, st, next, x);
   }
-  template <int ALL, int N, int FIRST, int I, int AHEAD, typename L>
+  template <int NP, int N, int FIRST, int RH, int I, int AHEAD, typename L>
   static __device__ __forceinline__ void value_steps(const x8 *p, const lds_u8 *at,
-                                                     const Places &w, f32x16 *o, const L &next,
+                                                     const Places &w, State *st, const L &next,
                                                      x8 *x) {
-    if constexpr (I < ALL) {
-      o[I % N] = mma<T>(x[I % AHEAD], p[I / N], o[I % N]);
-      if constexpr (I + AHEAD < ALL)
+    if constexpr (I < NP * N) {
+#pragma unroll
+      for (int r = 0; r < RH; ++r)
+        st[r].o[I % N] = mma<T>(x[I % AHEAD], p[r * NP + I / N], st[r].o[I % N]);
+      if constexpr (I + AHEAD < NP * N)
         x[I % AHEAD] = value_operand(at, w, (I + AHEAD) / N * 16, (I + AHEAD) % N);
       if constexpr (I % 2 == 0) next.template issue<FIRST + I / 2>();
       in_order();
-      value_steps<ALL, N, FIRST, I + 1, AHEAD>(p, at, w, o, next, x);
+      value_steps<NP, N, FIRST, RH, I + 1, AHEAD>(p, at, w, st, next, x);
     }
   }
 
@@ -663,26 +667,29 @@ struct Attend {
   }
 
   // The end of an item whose products left tiles out (see odd_values): the
-  // sums so far go to LDS, and a wave takes a row at a time through the left
+  // sums so far are laid down in LDS, and a wave takes a row at a time through the left
   // tiles, key by key, only those that the row sees.
-  static __device__ void careful(const AttendArgs &a, const AttendItem &it, lds_u8 *lds, int row,
-                                 int half, const State &st, float l, int t0, bool holds) {
+  static __device__ __forceinline__ void lay_down(const AttendItem &it, lds_u8 *lds, int row,
+                                                  int half, const State &st, float l, int t0,
+                                                  bool holds) {
+    typedef __attribute__((address_space(3))) float lds_float;
+    lds_float *sums = (lds_float *)lds, *ml = (lds_float *)(lds + TILES_LDS);
+    if (!holds || row >= it.n_rows) return;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        sums[row * DV + 32 * (t0 + t) + 8 * (i / 4) + 4 * half + i % 4] = st.o[t][i];
+    if (half == 0 && t0 == 0) {
+      ml[2 * row] = st.m;
+      ml[2 * row + 1] = l;
+    }
+  }
+  static __device__ void careful(const AttendArgs &a, const AttendItem &it, lds_u8 *lds) {
     typedef __attribute__((address_space(3))) float lds_float;
     lds_float *sums = (lds_float *)lds, *ml = (lds_float *)(lds + TILES_LDS);
     const int lane = threadIdx.x & 63;
     constexpr int PK = DK / 64, PV = DV / 64;
-    __syncthreads();
-    if (holds && row < it.n_rows) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          sums[row * DV + 32 * (t0 + t) + 8 * (i / 4) + 4 * half + i % 4] = st.o[t][i];
-      if (half == 0 && t0 == 0) {
-        ml[2 * row] = st.m;
-        ml[2 * row + 1] = l;
-      }
-    }
     __syncthreads();
     const int tile = it.wide ? kWideTile : kNarrowTile;
     const Source from(a, it);
@@ -746,27 +753,37 @@ struct Attend {
     }
   }
 
-  // Four waves, 32 rows each, tiles of 64 keys in BUFS LDS buffers.
+  // Four waves, 32 RH rows each, tiles of 64 keys in BUFS LDS buffers.  Of
+  // 64-wide heads a wave has room for 64 rows: every operand read from LDS then
+  // serves two matrix instructions, and a tile's loads and addresses twice the
+  // weights.
   template <bool SCAN>
   static __device__ __forceinline__ bool wide(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
+    constexpr int RH = kRows / 128, BUF = kWideTile * ROW;
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int row = wave * 32 + (lane & 31), half = lane >> 5;
-    constexpr int BUF = kWideTile * ROW;
+    const int row = wave * 32 * RH + (lane & 31), half = lane >> 5;
+    const bool idle = wave * 32 * RH >= it.n_rows;  // a wave without rows only loads
     typedef Loader<kWideTile, 4> Load;
     const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
-    x8 q[DK / 16];
-    int pos;
-    load_queries(a, it, row, half, q, &pos);
-    const Sight see = sight(a, it, pos);
-    Places w;
-    find_places(w, lane);
-    State st;
-    st.clear();
-    bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
 #pragma unroll
       for (int v = 0; v < AHEAD; ++v) rows.ask(v, v);
+    }
+    x8 q[RH * (DK / 16)];
+    Sight see[RH];
+    State st[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      int pos;
+      load_queries(a, it, row + 32 * r, half, q + r * (DK / 16), &pos);
+      see[r] = sight(a, it, pos);
+      st[r].clear();
+    }
+    Places w;
+    find_places(w, lane);
+    bool left = false;  // SCAN: a tile is left to `careful`
+    if (it.n_tiles > 0) {
       loads_done();
 #pragma unroll
       for (int v = 0; v < AHEAD; ++v) {
@@ -782,32 +799,62 @@ struct Attend {
         const bool odd = SCAN && !whole &&
                          __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const Load load(a, it, rows, rows.row(v + AHEAD, v + AHEAD, lane), lds + (v + AHEAD) % BUFS * BUF, wave,
-                        lane);
+        const Load load(a, it, rows, rows.row(v + AHEAD, v + AHEAD, lane),
+                        lds + (v + AHEAD) % BUFS * BUF, wave, lane);
         rows.ask(v + 2 * AHEAD, v + 2 * AHEAD);
-        if (odd) {
+        if (odd || idle) {
           load.all();
           continue;
         }
-        f32x16 s[2] = {products<kWideTile, 0, 2>(q, now, 0, w, load),
-                       products<kWideTile, DK / 32, 2>(q, now, 32, w, load)};
-        x8 p[4];
-        weigh<2>(a, it, s, key0, whole, see, st, half, p);
-        add_values<4, NT, 0>(p, now + kWideTile * R0, w, 0, st.o, NoLoader());
+        if constexpr (RH == 1) {
+          f32x16 s[2];
+          products<kWideTile, 0, 2>(q, now, 0, w, load, s);
+          products<kWideTile, DK / 32, 2>(q, now, 32, w, load, s + 1);
+          x8 p[4];
+          weigh<2>(a, it, s, key0, whole, see[0], st[0], half, p);
+          add_values<4, NT, 0>(p, now + kWideTile * R0, w, 0, st, NoLoader());
+        } else {
+          thirty_two<0, RH>(a, it, q, now, w, key0, whole, see, st, half, load);
+          thirty_two<1, RH>(a, it, q, now, w, key0, whole, see, st, half, load);
+        }
       }
       loads_done();
     }
-    float l = st.l + other_half(st.l, half);
+    float l[RH];
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      l[r] = st[r].l + other_half(st[r].l, half);
+      bad |= row + 32 * r < it.n_rows && odd_sums(st[r].o, l[r]);
+    }
     if constexpr (SCAN) {
       if (__syncthreads_or(left)) {
-        careful(a, it, lds, row, half, st, l, 0, true);
+#pragma unroll
+        for (int r = 0; r < RH; ++r) lay_down(it, lds, row + 32 * r, half, st[r], l[r], 0, true);
+        careful(a, it, lds);
         return true;
       }
-    } else if (__syncthreads_or(row < it.n_rows && odd_sums(st.o, l))) {
+    } else if (__syncthreads_or(bad)) {
       return false;
     }
-    store(a, it, row, half, st, l, 0);
+#pragma unroll
+    for (int r = 0; r < RH; ++r) store(a, it, row + 32 * r, half, st[r], l[r], 0);
     return true;
+  }
+  // Keys 32 B .. + 31 of a wide tile and RH rows of the lane.
+  template <int B, int RH, typename L>
+  static __device__ __forceinline__ void thirty_two(const AttendArgs &a, const AttendItem &it,
+                                                    const x8 *q, const lds_u8 *now,
+                                                    const Places &w, int key0, bool whole,
+                                                    const Sight *see, State *st, int half,
+                                                    const L &load) {
+    f32x16 s[RH];
+    products<kWideTile, B *(DK / 32), 2, RH>(q, now, 32 * B, w, load, s);
+    x8 p[2 * RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r)
+      weigh<1>(a, it, s + r, key0 + 32 * B, whole, see[r], st[r], half, p + 2 * r);
+    add_values<2, NT, 0, RH>(p, now + kWideTile * R0 + 32 * B * VS, w, 0, st, NoLoader());
   }
 
   // Latent rows: 64 query rows, two waves to each 32 of them.  The sums of a
@@ -862,13 +909,14 @@ struct Attend {
           continue;
         }
         x8 p[2];
-        f32x16 s = products<kWideTile, 0, 3>(q, now, 32 * part, w, load);
+        f32x16 s;
+        products<kWideTile, 0, 3>(q, now, 32 * part, w, load, &s);
         weigh<1>(a, it, &s, key0 + 32 * part, whole, see, st, half, p);
         const float m = st.m;
         ((lds8 *)mine)[lane] = p[0];
         ((lds8 *)mine)[64 + lane] = p[1];
         if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
-        add_values<2, NT, DK / 48>(p, now + 32 * part * VS, w, part * NT, st.o, load);
+        add_values<2, NT, DK / 48>(p, now + 32 * part * VS, w, part * NT, &st, load);
         __syncthreads();
         p[0] = ((const lds8 *)theirs)[lane];
         p[1] = ((const lds8 *)theirs)[64 + lane];
@@ -883,7 +931,7 @@ struct Attend {
             for (int j = 0; j < 8; ++j)
               p[b][j] = static_cast<T>(static_cast<float>(p[b][j]) * f2);
         }
-        add_values<2, NT, 0>(p, now + 32 * (1 - part) * VS, w, part * NT, st.o, NoLoader());
+        add_values<2, NT, 0>(p, now + 32 * (1 - part) * VS, w, part * NT, &st, NoLoader());
       }
       loads_done();
     }
@@ -895,7 +943,8 @@ struct Attend {
     l += ((const lds_float *)theirs)[lane];
     if constexpr (SCAN) {
       if (__syncthreads_or(left)) {
-        careful(a, it, lds, row, half, st, l, part * NT, true);
+        lay_down(it, lds, row, half, st, l, part * NT, true);
+        careful(a, it, lds);
         return true;
       }
     } else if (__syncthreads_or(row < it.n_rows && odd_sums(st.o, l))) {
@@ -947,7 +996,8 @@ struct Attend {
           Load(a, it, rows, rows.row(v + 4, n + 1, lane), own, 0, lane).all();
           continue;
         }
-        f32x16 s = products<kNarrowTile, 0, 1>(q, own, 0, w, NoLoader());
+        f32x16 s;
+        products<kNarrowTile, 0, 1>(q, own, 0, w, NoLoader(), &s);
         // the keys have been read: the next ones' loads may overwrite them
         const bool more = v + 4 < it.n_tiles;
         const Load load(a, it, rows, rows.row(v + 4, n + 1, lane), own, 0, lane);
@@ -961,7 +1011,7 @@ struct Attend {
         if (!more) loads_done();
         else if (rows.pages) loads_done<Load::N0 + 1>();
         else loads_done<Load::N0>();
-        add_values<2, NT, 0>(p, own + kNarrowTile * R0, w, 0, st.o, NoLoader());
+        add_values<2, NT, 0>(p, own + kNarrowTile * R0, w, 0, &st, NoLoader());
         lds_reads_done();
         if (more) load.template all<Load::N0, Load::N>();
       }
@@ -999,7 +1049,8 @@ struct Attend {
     }
     if constexpr (SCAN) {
       if (__syncthreads_or(left)) {
-        careful(a, it, lds, row, half, st, l, 0, wave == 0);
+        lay_down(it, lds, row, half, st, l, 0, wave == 0);
+        careful(a, it, lds);
         return true;
       }
     } else if (__syncthreads_or(wave == 0 && row < it.n_rows && odd_sums(st.o, l))) {
@@ -1034,7 +1085,7 @@ __global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128, NARROW
   // out, whatever it holds
   const int64_t all = static_cast<int64_t>(a.n_tokens) * a.G;
   const bool ok = it.req >= 0 && it.req < a.bs && it.row0 >= 0 && it.n_rows >= 1 &&
-                  it.n_rows <= (IN_KEY ? kLatentRows : it.wide ? kWideRows : kNarrowRows) &&
+                  it.n_rows <= rows_of(IN_KEY ? 2 : DK / 128, it.wide) &&
                   !(NARROW && it.wide) &&
                   it.row0 + it.n_rows <= all &&
                   it.kv_head >= 0 && it.kv_head < a.hkv && it.key_lo >= 0 &&

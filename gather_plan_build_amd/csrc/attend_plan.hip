@@ -40,7 +40,7 @@ struct Segment {
 struct Planner {
   const gpb_attend_shape &s;
   int32_t G;  // query heads per KV head
-  bool latent;
+  int which;  // attention kernel
   std::vector<int64_t> q_start;
   std::vector<int32_t> pos;
   std::vector<Segment> segments;
@@ -48,9 +48,7 @@ struct Planner {
   std::vector<int32_t> group_of;  // segment of a request's shared keys, or -1
   std::vector<int32_t> own;       // segment of a request's own keys, or -1
 
-  int rows_of(bool wide) const {
-    return latent ? kLatentRows : wide ? kWideRows : kNarrowRows;
-  }
+  int rows_of(bool wide) const { return gpb::rows_of(which, wide); }
   int tile_of(bool wide) const { return wide ? kWideTile : kNarrowTile; }
 
   // The tiles of a block: those of the first tokens (A) and those from the
@@ -82,7 +80,7 @@ struct Planner {
   void add_segment(int32_t req, int64_t tok0, int64_t n_tok, int32_t lo, int32_t hi,
                    bool grouped) {
     Segment g{req, tok0, n_tok, lo, hi, grouped,
-              latent || n_tok * G > kNarrowRows, blocks.size(), 0};
+              which == 2 || n_tok * G > kNarrowRows, blocks.size(), 0};
     const int64_t M = rows_of(g.wide);
     auto add = [&](int64_t row0, int64_t n) {
       Block b{};
@@ -136,7 +134,7 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
       s->n_groups < 0 || (s->bs > 0 && (!s->h_q_lens || !s->h_kv_lens)) ||
       (s->n_groups > 0 && !s->h_groups))
     return GPB_EINVAL;
-  Planner p{*s, s->n_heads / f->n_kv_heads, which == 2};
+  Planner p{*s, s->n_heads / f->n_kv_heads, which};
   const int64_t hkv = f->n_kv_heads, G = p.G;
   int64_t tokens = 0, longest = 0;
   p.q_start.resize(s->bs);

@@ -183,7 +183,7 @@ def covered(f, hq, q, kv, window, sinks, page, groups):
         (r, row0, n_rows, h, lo, hi, n_tiles, tile0, n_first, tile1, partial, wide, pmin,
          pmax) = it[:14]
         tile = 64 if wide else 32
-        assert 1 <= n_rows <= (64 if latent else 128 if wide else 32)
+        assert 1 <= n_rows <= (64 if latent else 256 if wide else 32)
         assert row0 + n_rows <= T * G
         toks = np.arange(row0, row0 + n_rows) // G
         assert pmin == pos[toks].min() and pmax == pos[toks].max()
