@@ -123,9 +123,13 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *base, uint64_t off, u
                  "v"(lane16), "n"(TO), "n"(X)
                : "s96", "s97", "scc");
 }
-// What the wave asked of LDS has arrived.
+// What the wave asked of LDS has arrived (and what it asked of the scalar
+// cache: as long as such a load may be under way the compiler cannot tell how
+// many LDS reads are, and has each product wait for all of them).  The builtin
+// is the s_waitcnt lgkmcnt(0) that the compiler reckons with.
 __device__ __forceinline__ void lds_reads_done() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("" ::: "memory");
 }
 // All but the newest LEFT of the wave's loads have arrived.
 template <int LEFT = 0>
@@ -211,8 +215,8 @@ struct Attend {
 
     __device__ __forceinline__ Source(const AttendArgs &a, const AttendItem &it)
         : src(a.rows), pages(nullptr), status(a.status), stride(a.row_bytes),
-          page_rows(a.page_rows), page_shift(a.page_shift), lo(it.key_lo), last(it.key_hi - 1),
-          n_pages(0) {
+          page_rows(a.page_rows), page_shift(a.page_shift), lo(it.key_lo),
+          last(it.key_hi - 1), n_pages(0) {
       const int64_t base = uniform<int64_t>(a.base ? a.base[it.req] : it.req * a.pages_stride);
       bool ok;
       if (a.pages) {
@@ -309,6 +313,13 @@ struct Attend {
       src[1] = IN_KEY ? src[0] + VB
                       : from.src + static_cast<int64_t>(a.hkv) * KB +
                             static_cast<int64_t>(it.kv_head) * VB;
+    }
+    // Rows of queries instead: off from q.
+    __device__ __forceinline__ Loader(const uint8_t *q, uint64_t off, lds_u8 *tile, int wave,
+                                      int lane)
+        : to(tile), off(off), wave(wave), lane(lane) {
+      src[0] = q;
+      src[1] = q + VB;
     }
     template <int I>
     __device__ __forceinline__ void issue() const {
@@ -599,6 +610,11 @@ struct Attend {
            (a.window == 0 || it.pos_max - key0 < a.window || key0 + n <= a.sinks);
   }
 
+  static __device__ __forceinline__ int position(const AttendArgs &a, const AttendItem &it,
+                                                 int row) {
+    return row < it.n_rows ? a.list[a.positions_at + (it.row0 + row) / a.G] : -1;
+  }
+
   // The lane's query row: its token, its head, its queries in registers.
   static __device__ __forceinline__ void load_queries(const AttendArgs &a, const AttendItem &it,
                                                       int row, int half, x8 *q, int *pos) {
@@ -613,12 +629,7 @@ struct Attend {
     // arrived before the tiles' loads start: a wait for them later would wait
     // for those too
 #pragma unroll
-    for (int d = 0; d < DK / 16; ++d) {
-      // (a latent's go to accumulation registers, from which a matrix
-      // instruction takes an operand as well: the sums need the others)
-      if (IN_KEY) asm volatile("" : "+a"(q[d]));
-      else asm volatile("" : "+v"(q[d]));
-    }
+    for (int d = 0; d < DK / 16; ++d) asm volatile("" : "+v"(q[d]));
     asm volatile("" : "+v"(*pos));
   }
 
@@ -630,13 +641,27 @@ struct Attend {
                      : (m + __builtin_amdgcn_logf(l) - SHIFT) * 0.69314718055994531f;
   }
 
-  // The row's sums (or results) of output tiles t0 ..; the first also its m
-  // and l (or its log-sum).
-  static __device__ __forceinline__ void store(const AttendArgs &a, const AttendItem &it, int row,
-                                               int half, const State &st, float l, int t0) {
-    if (row >= it.n_rows) return;
+  // Results of the row at `g` (token * G + head of the KV head's group).
+  static __device__ __forceinline__ int64_t out_place(const AttendArgs &a, const AttendItem &it,
+                                                      int g, int64_t *lse_at) {
+    const int token = g / a.G, h = g - token * a.G + it.kv_head * a.G;
+    *lse_at = static_cast<int64_t>(token) * a.n_heads + h;
+    return token * a.o_ts + h * a.o_hs;
+  }
+
+  // The sums (or results) of the wave's 32 rows from row0 on, output tiles t0
+  // ..; t0 = 0 also their m and l (or log-sums).  They go by way of 32 W * 4
+  // bytes of LDS of the wave's own, so that rows are written in whole: a lane
+  // holds 16 bytes of every 64 of one row.
+  static __device__ __forceinline__ void store(const AttendArgs &a, const AttendItem &it,
+                                               lds_u8 *room, int row0, int lane, const State &st,
+                                               float l, int t0) {
+    if (row0 >= it.n_rows) return;
+    constexpr int W = NT * 32;  // values of a row here
+    const int n = lane & 31, half = lane >> 5, row = row0 + n;
+    typedef __attribute__((address_space(3))) u32x4 lds16;
     if (it.partial >= 0) {
-      const int64_t at = static_cast<int64_t>(it.partial) + row;
+      constexpr int C = W / 4, M = C < 32 ? C - 1 : 31;  // 16-byte chunks, four values
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -644,14 +669,25 @@ struct Attend {
           f32x4 x;
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[j] = st.o[t][4 * y + j];
-          *reinterpret_cast<f32x4 *>(a.sums + at * DV + 32 * (t0 + t) + 8 * y + 4 * half) = x;
+          *(lds16 *)(room + (n * C + ((8 * t + 2 * y + half) ^ (n & M))) * 16) =
+              __builtin_bit_cast(u32x4, x);
         }
-      if (half == 0 && t0 == 0) *reinterpret_cast<f32x2 *>(a.ml + 2 * at) = f32x2{st.m, l};
+      lds_reads_done();
+      float *to = a.sums + static_cast<int64_t>(it.partial) * DV + 32 * t0;
+#pragma unroll
+      for (int i = 0; i < 32 * C / 64; ++i) {
+        const int r = i * (64 / C) + lane / C, c = lane % C;
+        const u32x4 x = *(const lds16 *)(room + (r * C + (c ^ (r & M))) * 16);
+        if (row0 + r < it.n_rows)
+          *reinterpret_cast<u32x4 *>(to + static_cast<int64_t>(row0 + r) * DV + c * 4) = x;
+      }
+      if (half == 0 && t0 == 0 && row < it.n_rows)
+        *reinterpret_cast<f32x2 *>(a.ml + 2 * (static_cast<int64_t>(it.partial) + row)) =
+            f32x2{st.m, l};
+      lds_reads_done();
       return;
     }
-    const int g = it.row0 + row;
-    const int token = g / a.G, h = g - token * a.G + it.kv_head * a.G;
-    uint16_t *dst = a.out + token * a.o_ts + h * a.o_hs;
+    constexpr int C = W / 8, M = C < 32 ? C - 1 : 31;  // chunks of eight values
     const float inv = inverse(l);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -660,10 +696,25 @@ struct Attend {
         x4 x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = static_cast<T>(st.o[t][4 * y + j] * inv);
-        *reinterpret_cast<x4 *>(dst + 32 * (t0 + t) + 8 * y + 4 * half) = x;
+        typedef __attribute__((address_space(3))) x4 lds8;
+        *(lds8 *)(room + (n * C + ((4 * t + y) ^ (n & M))) * 16 + half * 8) = x;
       }
-    if (half == 0 && t0 == 0 && a.lse)
-      a.lse[static_cast<int64_t>(token) * a.n_heads + h] = log_sum(st.m, l);
+    lds_reads_done();
+    int64_t lse_at;
+    const uint64_t at = out_place(a, it, it.row0 + min(row, it.n_rows - 1), &lse_at);
+    typedef u32x4 Loose __attribute__((aligned(8)));  // out is 8-byte aligned
+#pragma unroll
+    for (int i = 0; i < 32 * C / 64; ++i) {
+      const int r = i * (64 / C) + lane / C, c = lane % C;
+      const u32x4 x = *(const lds16 *)(room + (r * C + (c ^ (r & M))) * 16);
+      const uint64_t to = __shfl(static_cast<uint32_t>(at), r, 64) |
+                          static_cast<uint64_t>(__shfl(static_cast<uint32_t>(at >> 32), r, 64))
+                              << 32;
+      if (row0 + r < it.n_rows)
+        *reinterpret_cast<Loose *>(a.out + static_cast<int64_t>(to) + 32 * t0 + c * 8) = x;
+    }
+    if (half == 0 && t0 == 0 && a.lse && row < it.n_rows) a.lse[lse_at] = log_sum(st.m, l);
+    lds_reads_done();
   }
 
   // The end of an item whose products left tiles out (see odd_values): the
@@ -790,6 +841,7 @@ struct Attend {
         Load(a, it, rows, rows.row(v, v, lane), lds + v * BUF, wave, lane).all();
         rows.ask(v + AHEAD, v + AHEAD);
       }
+      lds_reads_done();
       for (int v = 0; v < it.n_tiles; ++v) {
         loads_done<(BUFS - 2) * Load::N>();
         __syncthreads();
@@ -838,7 +890,8 @@ struct Attend {
       return false;
     }
 #pragma unroll
-    for (int r = 0; r < RH; ++r) store(a, it, row + 32 * r, half, st[r], l[r], 0);
+    for (int r = 0; r < RH; ++r)
+      store(a, it, lds + wave * 128 * NT * 32, (wave * RH + r) * 32, lane, st[r], l[r], 0);
     return true;
   }
   // Keys 32 B .. + 31 of a wide tile and RH rows of the lane.
@@ -877,21 +930,39 @@ struct Attend {
     const lds_u8 *theirs = lds + TILES_LDS + (wave ^ 1) * WAVE_XCHG;
     typedef __attribute__((address_space(3))) x8 lds8;
     typedef __attribute__((address_space(3))) float lds_float;
-    x8 q[DK / 16];
-    int pos;
-    load_queries(a, it, row, half, q, &pos);
+    x8 q[DK / 16] = {};
     Places w;
     find_places(w, lane);
-    const Sight see = sight(a, it, pos);
+    const Sight see = sight(a, it, position(a, it, row));
     State st;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
       typedef Loader<kWideTile, 4> Load;
       rows.ask(0, 0);
-      loads_done();
+      {
+        // the queries come as a tile of their own, in the second buffer, since
+        // a key's place in LDS is a query's too
+        const int g = it.row0 + min(wave * 16 + (lane & 15), it.n_rows - 1);
+        const int t = g / a.G, h = g - t * a.G + it.kv_head * a.G;
+        Load(reinterpret_cast<const uint8_t *>(a.q),
+             static_cast<uint64_t>(t * a.q_ts + h * a.q_hs) * 2, lds + BUF, wave, lane)
+            .all();
+      }
+      loads_done<Load::N>();
       Load(a, it, rows, rows.row(0, 0, lane), lds, wave, lane).all();
       rows.ask(1, 1);
+      if (rows.pages) loads_done<Load::N + 1>();
+      else loads_done<Load::N>();
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < DK / 16; ++d) {
+        q[d] = key_operand<kWideTile>(lds + BUF, 32 * (wave >> 1), w, d);
+        // to the accumulation registers, from which a matrix instruction takes
+        // an operand as well: the sums need the others
+        asm volatile("" : "+a"(q[d]));
+      }
+      lds_reads_done();
       for (int v = 0; v < it.n_tiles; ++v) {
         loads_done();
         __syncthreads();
@@ -950,7 +1021,7 @@ struct Attend {
     } else if (__syncthreads_or(row < it.n_rows && odd_sums(st.o, l))) {
       return false;
     }
-    store(a, it, row, half, st, l, part * NT);
+    store(a, it, lds + wave * 128 * NT * 32, (wave >> 1) * 32, lane, st, l, part * NT);
     return true;
   }
 
@@ -975,8 +1046,6 @@ struct Attend {
     State st;
     lds_u8 *own = lds + wave * kNarrowTile * ROW;
     typedef __attribute__((address_space(3))) float lds_float;
-    lds_float *slot = (lds_float *)lds;
-    constexpr int SLOT = (NT * 16 + 2) * 64;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
     if (wave < it.n_tiles) {
@@ -984,6 +1053,7 @@ struct Attend {
       loads_done();
       Load(a, it, rows, rows.row(wave, 0, lane), own, 0, lane).all();
       int n = 0;  // tiles of the wave so far
+      lds_reads_done();
       for (int v = wave; v < it.n_tiles; v += 4, ++n) {
         const int key0 = first_key(it, v, kNarrowTile);
         const bool whole = whole_tile(a, it, key0, kNarrowTile);
@@ -1017,51 +1087,88 @@ struct Attend {
       }
       loads_done();
     }
-    float l = st.l + other_half(st.l, half);
+    const float l = st.l + other_half(st.l, half);
 
-    // waves 2 and 3 hand over to 0 and 1, then 1 to 0
+    // The waves lay their sums side by side, and a wave takes a row at a time
+    // of all four.
+    constexpr int C = DV / 4, M = C < 32 ? C - 1 : 31, PER = DV / 64;
+    typedef __attribute__((address_space(3))) u32x4 lds16;
+    typedef float Values __attribute__((ext_vector_type(PER)));
+    typedef __attribute__((address_space(3))) Values lds_values;
+    lds_float *ml = (lds_float *)(lds + TILES_LDS);  // of wave w, row r: w * 32 + r
+    __syncthreads();
+    if (row < it.n_rows) {
 #pragma unroll
-    for (int step = 2; step >= 1; step >>= 1) {
-      __syncthreads();
-      if (wave >= step && wave < 2 * step) {
-        lds_float *to = slot + (wave - step) * SLOT + lane;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int y = 0; y < 4; ++y) {
+          f32x4 x;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) to[(t * 16 + i) * 64] = st.o[t][i];
-        to[NT * 16 * 64] = st.m;
-        to[NT * 16 * 64 + 64] = l;
+          for (int j = 0; j < 4; ++j) x[j] = st.o[t][4 * y + j];
+          *(lds16 *)(lds + ((wave * 32 + row) * C + ((8 * t + 2 * y + half) ^ (row & M))) * 16) =
+              __builtin_bit_cast(u32x4, x);
+        }
+      if (half == 0) {
+        ml[2 * (wave * 32 + row)] = st.m;
+        ml[2 * (wave * 32 + row) + 1] = l;
       }
-      __syncthreads();
-      if (wave < step) {
-        const lds_float *from = slot + wave * SLOT + lane;
-        const float m2 = from[NT * 16 * 64], l2 = from[NT * 16 * 64 + 64];
-        const float m = fmaxf(st.m, m2), ref = finite_m(m);
-        const float f1 = __builtin_amdgcn_exp2f(st.m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
-        l = l * f1 + l2 * f2;
-        st.m = m;
+    }
+    left = __syncthreads_or(left);  // (SCAN)
+    bool odd = false;
+    for (int r = wave; r < it.n_rows; r += 4) {
+      float m[4], sum = 0.0f, top = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            st.o[t][i] = st.o[t][i] * f1 + from[(t * 16 + i) * 64] * f2;
+      for (int x = 0; x < 4; ++x) {
+        m[x] = ml[2 * (x * 32 + r)];
+        top = fmaxf(top, m[x]);
       }
+      Values o = {};
+      const int chunk = lane * PER / 4, rest = lane * PER % 4;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float f = __builtin_amdgcn_exp2f(m[x] - finite_m(top));
+        sum += ml[2 * (x * 32 + r) + 1] * f;
+        o += *(const lds_values *)(lds + ((x * 32 + r) * C + (chunk ^ (r & M))) * 16 + rest * 4) * f;
+      }
+      float zero = sum * 0.0f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) zero = __builtin_fmaf(o[e], 0.0f, zero);
+      odd |= !(zero == 0.0f);
+      if (SCAN && left) {  // where `careful` looks for them: row r of all is in use no more
+        lds_reads_done();
+#pragma unroll
+        for (int e = 0; e < PER; ++e) ((lds_float *)lds)[r * DV + lane * PER + e] = o[e];
+        if (lane == 0) {
+          ml[2 * r] = top;
+          ml[2 * r + 1] = sum;
+        }
+        continue;
+      }
+      if (it.partial >= 0) {
+        const int64_t at = static_cast<int64_t>(it.partial) + r;
+        *reinterpret_cast<Values *>(a.sums + at * DV + lane * PER) = o;
+        if (lane == 0) *reinterpret_cast<f32x2 *>(a.ml + 2 * at) = f32x2{top, sum};
+        continue;
+      }
+      int64_t lse_at;
+      T *to = reinterpret_cast<T *>(a.out + out_place(a, it, it.row0 + r, &lse_at)) + lane * PER;
+      typedef T Out __attribute__((ext_vector_type(PER)));
+      Out x;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) x[e] = static_cast<T>(o[e] * inverse(sum));
+      *reinterpret_cast<Out *>(to) = x;
+      if (lane == 0 && a.lse) a.lse[lse_at] = log_sum(top, sum);
     }
     if constexpr (SCAN) {
-      if (__syncthreads_or(left)) {
-        lay_down(it, lds, row, half, st, l, 0, wave == 0);
-        careful(a, it, lds);
-        return true;
-      }
-    } else if (__syncthreads_or(wave == 0 && row < it.n_rows && odd_sums(st.o, l))) {
-      return false;
+      if (left) careful(a, it, lds);
+      return true;
+    } else {
+      return !__syncthreads_or(odd);  // (what was written is written over)
     }
-    if (wave == 0) store(a, it, row, half, st, l, 0);
-    return true;
   }
 
-  // An item's work.  False: its sums hold an infinity or NaN, nothing has been
-  // written, and the item is to be done again with SCAN.
+  // An item's work.  False: its sums hold an infinity or NaN, and the item is to
+  // be done again with SCAN.
   template <bool SCAN>
   static __device__ __forceinline__ bool item(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
