@@ -88,11 +88,15 @@ def _elf_section(data, name):
     return None
 
 
+_OTHER_KERNELS = (b"k_row_append", b"k_attend")
+
+
 def _kernel_digest(lib=None):
-    """Digest of the machine code of the library's gfx950 kernels: the .text
-    of every gfx950 code object in its offload bundles.  It changes when a
-    kernel's code does and not when only host code or comments do, so the
-    counters stay attached to the kernels they were taken on."""
+    """Digest of the machine code of the library's gfx950 compose kernels: the
+    .text of every gfx950 code object in its offload bundles, but for those of
+    the row append and the attention, which no counter here is taken on.  It
+    changes when a kernel's code does and not when only host code or comments
+    do, so the counters stay attached to the kernels they were taken on."""
     import struct
     with open(lib or LIB, "rb") as f:
         data = f.read()
@@ -106,8 +110,9 @@ def _kernel_digest(lib=None):
             off, size, tlen = struct.unpack_from("<QQQ", fatbin, q)
             triple = fatbin[q + 24:q + 24 + tlen].decode()
             q += 24 + tlen
-            if triple.endswith("gfx950"):
-                h.update(_elf_section(fatbin[at + off:at + off + size], ".text") or b"")
+            code = fatbin[at + off:at + off + size]
+            if triple.endswith("gfx950") and not any(k in code for k in _OTHER_KERNELS):
+                h.update(_elf_section(code, ".text") or b"")
         at = fatbin.find(_BUNDLE_MAGIC, at + len(_BUNDLE_MAGIC))
     return h.hexdigest()[:16]
 
