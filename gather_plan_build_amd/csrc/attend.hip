@@ -300,45 +300,52 @@ struct Attend {
   struct Loader {
     static constexpr int N0 = TILE * R0 / 1024 / WAVES, N1 = TILE * R1 / 1024 / WAVES;
     static constexpr int N = N0 + N1;
+    // Rows of 1 KiB are loaded one at a time, from where a lane says; shorter
+    // ones several at a time, a lane taking its chunk of its own row, the same
+    // of keys and values.
+    static constexpr bool LONG = R0 == 1024;
+    static constexpr int C = (LONG ? R1 : R0) / 16, SHORT = LONG ? N1 : N0;
+    static_assert(LONG || R0 == R1, "keys and values of one width, or a latent");
     const uint8_t *src[2];  // of the rows of R0 and of R1 bytes
-    lds_u8 *to;             // of the wave's first load
+    lds_u8 *to;
     uint64_t off;           // of the lane's row
+    uint64_t chunk[SHORT];
     int wave, lane;
 
     __device__ __forceinline__ Loader(const AttendArgs &a, const AttendItem &it,
                                       const Source &from, uint64_t off, lds_u8 *tile, int wave,
                                       int lane)
-        : to(tile), off(off), wave(wave), lane(lane) {
-      src[0] = uniform(from.src + static_cast<int64_t>(it.kv_head) * KB);
-      src[1] = IN_KEY ? src[0] + VB
-                      : from.src + static_cast<int64_t>(a.hkv) * KB +
-                            static_cast<int64_t>(it.kv_head) * VB;
+        : Loader(from.src + static_cast<int64_t>(it.kv_head) * KB, off, tile, wave, lane) {
+      if (!IN_KEY)
+        src[1] = from.src + static_cast<int64_t>(a.hkv) * KB +
+                 static_cast<int64_t>(it.kv_head) * VB;
     }
-    // Rows of queries instead: off from q.
-    __device__ __forceinline__ Loader(const uint8_t *q, uint64_t off, lds_u8 *tile, int wave,
+    // Latent rows, or queries of their form, at off from `first`.
+    __device__ __forceinline__ Loader(const uint8_t *first, uint64_t off, lds_u8 *tile, int wave,
                                       int lane)
         : to(tile), off(off), wave(wave), lane(lane) {
-      src[0] = q;
-      src[1] = q + VB;
+      src[0] = uniform(first);
+      src[1] = src[0] + VB;
+#pragma unroll
+      for (int j = 0; j < SHORT; ++j) {
+        const int r = j * (64 / C) + lane / C;  // its low bits are those of its LDS row
+        const uint32_t lo = __shfl(static_cast<uint32_t>(off), r, 64);
+        const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), r, 64);
+        chunk[j] = (lo | static_cast<uint64_t>(hi) << 32) + chunk_at<C * 16>(r, lane % C) * 16;
+      }
     }
     template <int I>
     __device__ __forceinline__ void issue() const {
       if constexpr (I < N) {
-        constexpr int B = I < N0 ? R0 : R1, C = B / 16, J = I < N0 ? I : I - N0;
-        const int first = wave * (I < N0 ? N0 : N1);  // instruction of the tile
-        lds_u8 *at = to + (I < N0 ? 0 : TILE * R0) + first * 1024;
-        if constexpr (C == 64) {  // a row each, 16 a wave: its swizzle is that of J
+        constexpr int J = I < N0 ? I : I - N0;
+        lds_u8 *at = to + (I < N0 ? wave * N0 : TILE * R0 / 1024 + wave * N1) * 1024;
+        if constexpr (LONG && I < N0) {  // (16 a wave: a row's swizzle is that of J)
           const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(off), J);
           const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(off >> 32), J);
-          load_to_lds<turned_back<B>(row_bits<B>(J)) * 16, J * 1024>(
-              src[0], lo | static_cast<uint64_t>(hi) << 32, turned_back<B>(lane) * 16, at);
+          load_to_lds<turned_back<R0>(row_bits<R0>(J)) * 16, J * 1024>(
+              src[0], lo | static_cast<uint64_t>(hi) << 32, turned_back<R0>(lane) * 16, at);
         } else {
-          const int r = J * (64 / C) + lane / C;  // and so is the swizzle of key r
-          const uint32_t lo = __shfl(static_cast<uint32_t>(off), r, 64);
-          const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), r, 64);
-          load_to_lds(src[I < N0 ? 0 : 1] + (lo | static_cast<uint64_t>(hi) << 32) +
-                          chunk_at<B>(r, lane % C) * 16,
-                      at + J * 1024);
+          load_to_lds(src[I < N0 ? 0 : 1] + chunk[J], at + J * 1024);
         }
       }
     }
