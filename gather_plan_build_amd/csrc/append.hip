@@ -154,9 +154,11 @@ int row_append(const gpb_row_format *f, const gpb_append *p, int32_t *d_status, 
   if (rc != GPB_OK) return rc;
   if (!p || p->n_rows < 0 || p->n_q_heads < 0 || p->n_q_heads > 65536 ||
       p->n_pool_rows < 0) return GPB_EINVAL;
-  if (p->n_pool_rows > INT32_MAX) return GPB_ERANGE;
+  // (a launch has fewer than 2^32 threads)
+  if (p->n_pool_rows > INT32_MAX || p->n_rows > static_cast<int64_t>(UINT32_MAX / kBlock))
+    return GPB_ERANGE;
   if (p->rot_dim < 0 || p->rot_dim > 2 * kMaxPairs || p->rot_dim % 16 || p->rot_start < 0 ||
-      p->rot_start % 8 || p->rot_start + p->rot_dim > f->k_dim ||
+      p->rot_start % 8 || p->rot_start > f->k_dim - p->rot_dim ||
       (p->interleaved != 0 && p->interleaved != 1))
     return GPB_EINVAL;
   if (p->rot_dim > 0) {
@@ -189,6 +191,8 @@ int row_append(const gpb_row_format *f, const gpb_append *p, int32_t *d_status, 
       (has_q && (!whole_chunks(p->q_token_stride) || !whole_chunks(p->q_head_stride) ||
                  !whole_chunks(p->qo_token_stride) || !whole_chunks(p->qo_head_stride))))
     return GPB_EALIGN;
+  if (has_q && !apart(p->n_rows, p->n_q_heads, f->k_dim, p->qo_token_stride, p->qo_head_stride))
+    return GPB_EINVAL;
 
   AppendArgs a = {};
   a.k = static_cast<const uint16_t *>(p->d_k);

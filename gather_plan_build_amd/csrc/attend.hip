@@ -211,16 +211,22 @@ struct Attend {
     int32_t *status;
     uint32_t stride;
     int page_rows, page_shift, lo, last;
+    int sunk, near, behind;  // keys [sunk, near) are read as `behind`
     uint32_t n_pages;
 
     __device__ __forceinline__ Source(const AttendArgs &a, const AttendItem &it)
         : src(a.rows), pages(nullptr), status(a.status), stride(a.row_bytes),
           page_rows(a.page_rows), page_shift(a.page_shift), lo(it.key_lo),
-          last(it.key_hi - 1), n_pages(0) {
+          last(max(min(it.key_hi - 1, it.pos_max), lo)), sunk(0), near(0), behind(0), n_pages(0) {
+      if (a.window > 0) {
+        sunk = a.sinks;
+        near = max(lo, it.pos_min + 1 - a.window);
+        behind = near <= last ? near : max(sunk - 1, lo);
+      }
       const int64_t base = uniform<int64_t>(a.base ? a.base[it.req] : it.req * a.pages_stride);
       bool ok;
       if (a.pages) {
-        ok = base >= 0 && base + page_of(max(last, 0)) < a.n_listed;
+        ok = base >= 0 && base + page_of(last) < a.n_listed;
         if (ok) pages = a.pages + base;
         n_pages = a.n_pages;
       } else {
@@ -229,10 +235,16 @@ struct Attend {
       }
       if (!ok) {
         stride = 0;
-        if (status && lo <= last) atomicOr(status, GPB_STATUS_BAD_DESCRIPTOR);
+        if (status && it.n_tiles > 0) atomicOr(status, GPB_STATUS_BAD_DESCRIPTOR);
       }
     }
-    __device__ __forceinline__ int in_range(int key) const { return min(max(key, lo), last); }
+    // The key, or if no row sees it one that some row sees: the pages behind a
+    // window and past the last query may no longer, or not yet, be the
+    // request's.
+    __device__ __forceinline__ int in_range(int key) const {
+      key = max(key, lo);
+      return min(key >= sunk && key < near ? behind : key, last);
+    }
     __device__ __forceinline__ uint32_t page_of(uint32_t key) const {
       return page_shift >= 0 ? key >> page_shift : key / static_cast<uint32_t>(page_rows);
     }
@@ -1201,7 +1213,7 @@ __global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128, NARROW
   const bool ok = it.req >= 0 && it.req < a.bs && it.row0 >= 0 && it.n_rows >= 1 &&
                   it.n_rows <= rows_of(IN_KEY ? 2 : DK / 128, it.wide) &&
                   !(NARROW && it.wide) &&
-                  it.row0 + it.n_rows <= all &&
+                  static_cast<int64_t>(it.row0) + it.n_rows <= all &&
                   it.kv_head >= 0 && it.kv_head < a.hkv && it.key_lo >= 0 &&
                   it.key_lo <= it.key_hi && it.key_hi <= a.max_keys &&
                   (it.n_tiles == 0 || it.key_lo < it.key_hi) && it.n_tiles >= 0 &&
@@ -1355,6 +1367,8 @@ int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io 
       io->q_token_stride % 8 || io->q_head_stride % 8 || io->out_token_stride % 4 ||
       io->out_head_stride % 4)
     return GPB_EALIGN;
+  if (!apart(p->n_tokens, p->n_heads, p->format.v_dim, io->out_token_stride, io->out_head_stride))
+    return GPB_EINVAL;
 
   AttendArgs a = {};
   a.list = d_list;

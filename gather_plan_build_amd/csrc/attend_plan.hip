@@ -143,6 +143,7 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
     if (q < 0 || n < 0) return GPB_EINVAL;
     p.q_start[r] = tokens;
     tokens += q;
+    if (tokens > INT32_MAX) return GPB_ERANGE;
     longest = std::max(longest, n);
   }
   // rows of a KV head, positions and keys are int32 in the list
@@ -254,7 +255,8 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
       }
       n_items += hkv * b.parts;
     }
-  if (n_items > INT32_MAX / kItemInts || n_partial > INT32_MAX) return GPB_ERANGE;
+  // (a launch has fewer than 2^32 threads)
+  if (n_items > UINT32_MAX / 256 || n_partial > INT32_MAX) return GPB_ERANGE;
 
   // joins: every token's rows of a KV head in runs of at most 32 (which no
   // block cuts), where the token has more than one part
@@ -283,7 +285,7 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
           }
           j.n_refs = static_cast<int32_t>(refs.size()) - j.ref0;
           joins.push_back(j);
-          if (refs.size() > INT32_MAX / 4u || joins.size() > INT32_MAX / 64u) return GPB_ERANGE;
+          if (refs.size() > INT32_MAX / 4u || joins.size() > UINT32_MAX / 256) return GPB_ERANGE;
         }
       }
   }

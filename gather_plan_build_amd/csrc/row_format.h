@@ -42,4 +42,16 @@ inline int check_format(const gpb_row_format *f) {
   return f->row_bytes % 16 ? GPB_EALIGN : GPB_OK;
 }
 
+// Whether results [tokens][heads] of `dim` values have a place each: heads
+// within tokens, or tokens within heads.
+inline bool apart(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride,
+                  int64_t head_stride) {
+  const auto within = [dim](int64_t n, int64_t stride, int64_t others, int64_t outer) {
+    return (n <= 1 || stride >= dim) &&
+           (others <= 1 || (outer >= dim && (n <= 1 || stride <= (outer - dim) / (n - 1))));
+  };
+  return within(heads, head_stride, tokens, token_stride) ||
+         within(tokens, token_stride, heads, head_stride);
+}
+
 }  // namespace gpb

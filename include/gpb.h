@@ -610,9 +610,11 @@ typedef struct gpb_row_format {
  * 64 bits, so far positions keep their fraction.  rot_dim = 0 rotates
  * nothing.  rot_start is a multiple of 8, rot_dim a multiple of 16, at most
  * 512.  Strides are in elements and multiples of 8, pointers to row data
- * 16-byte aligned. */
+ * 16-byte aligned; the heads of d_q_out have a place each (heads within
+ * tokens or tokens within heads).  Nothing else that is written overlaps what
+ * is read. */
 typedef struct gpb_append {
-  int32_t n_rows, n_q_heads;
+  int32_t n_rows, n_q_heads;    /* n_q_heads at most 65536                     */
   const void *d_k, *d_v;
   int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
   void *d_pool;
@@ -630,7 +632,7 @@ typedef struct gpb_append {
 } gpb_append;
 
 /* Append the rows in one launch.  Errors: GPB_EINVAL, GPB_EALIGN, GPB_ERANGE
- * (n_pool_rows beyond INT32_MAX), GPB_EHIP. */
+ * (n_pool_rows beyond INT32_MAX, n_rows of 2^24 or more), GPB_EHIP. */
 int gpb_row_append(const gpb_row_format *format, const gpb_append *append,
                    int32_t *d_status, void *stream);
 
@@ -648,7 +650,7 @@ int gpb_row_append(const gpb_row_format *format, const gpb_append *append,
  * least 1, a multiple of page_rows, and no more than kv_lens - q_lens of any
  * member (a query is never among the shared keys). */
 typedef struct gpb_attend_shape {
-  int32_t bs, n_heads;          /* n_heads a multiple of n_kv_heads            */
+  int32_t bs, n_heads;          /* n_heads a multiple of n_kv_heads, <= 65536  */
   int32_t window, sinks;        /* window 0: every earlier key                 */
   int32_t page_rows;            /* keys per page; any >= 1 for the dense call  */
   const int32_t *h_q_lens, *h_kv_lens;  /* host [bs]                           */
@@ -682,8 +684,9 @@ int gpb_attend_plan_build(const gpb_row_format *format, const gpb_attend_shape *
 
 /* Queries and results of one layer.  q: n_tokens tokens of n_heads heads of
  * k_dim values of the format's type; out: the same of v_dim; element strides,
- * multiples of 8 (out: of 4), pointers 16-byte aligned (out: 8).  Rows behind
- * the last query are neither read nor written.  lse (optional): float,
+ * multiples of 8 (out: of 4), pointers 16-byte aligned (out: 8); the heads of
+ * out have a place each (heads within tokens or tokens within heads).  Rows
+ * behind the last query are neither read nor written.  lse (optional): float,
  * natural log of the sum of exp(score), [n_tokens][n_heads] contiguous.
  * scale > 0 multiplies q.k.  out must not overlap any input. */
 typedef struct gpb_attend_io {
@@ -700,10 +703,11 @@ typedef struct gpb_attend_io {
  * k_bases).  d_list is the device copy of the plan's list; d_workspace holds
  * plan->workspace_bytes bytes, 16-byte aligned, and may be NULL when that is
  * 0; calls that may overlap need a workspace each.  A plan with groups is
- * refused (the dense buffer holds each request's keys apart).  A base that
- * leads outside the buffer reads row 0 instead and ORs
- * GPB_STATUS_BAD_DESCRIPTOR into *d_status; a list that is not the plan's
- * ORs GPB_STATUS_BAD_PLAN_INPUT and its item is left out.  Errors: GPB_EINVAL,
+ * refused (the dense buffer holds each request's keys apart).  Keys that no
+ * query sees are not read.  Where a request's base leads outside the buffer
+ * every key of its work item is row 0 and GPB_STATUS_BAD_DESCRIPTOR is ORed
+ * into *d_status; an item of d_list that is not the plan's is left out, its
+ * results as they were, and GPB_STATUS_BAD_PLAN_INPUT ORed.  Errors: GPB_EINVAL,
  * GPB_EALIGN, GPB_ERANGE, GPB_EHIP. */
 int gpb_attend_dense(const gpb_attend_plan *plan, const int32_t *d_list,
                      const gpb_attend_io *io, const void *d_dense, int64_t n_dense_rows,
@@ -716,8 +720,10 @@ int gpb_attend_dense(const gpb_attend_plan *plan, const int32_t *d_list,
  * d_pages[d_page_base[r]], or at d_pages[r * pages_stride] when d_page_base is
  * NULL; d_pages holds n_pages_listed entries (with d_page_base NULL, at least
  * bs * pages_stride, and pages_stride covers the longest request).  The plan's
- * slot_pages with slot_base are such a list.  A page outside the pool's whole
- * pages, or an entry outside d_pages, reads page 0 instead and ORs
+ * slot_pages with slot_base are such a list.  Entries of pages that no query
+ * sees (behind the window and the first tokens) may hold anything.  The keys of
+ * a page outside the pool's whole pages are those of page 0; where a list ends
+ * outside d_pages every key of the work item is row 0; both OR
  * GPB_STATUS_BAD_DESCRIPTOR into *d_status.  Errors as gpb_attend_dense. */
 int gpb_attend_paged(const gpb_attend_plan *plan, const int32_t *d_list,
                      const gpb_attend_io *io, const void *d_pool, int64_t n_pool_rows,

@@ -401,6 +401,56 @@ def test_pages_outside_the_pool_are_reported_and_touch_one_request():
     assert int(status) == gpb.STATUS_BAD_DESCRIPTOR
 
 
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 16), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("q,kv,page,window,sinks", [
+    ([1, 1], [2000, 700], 16, 100, 0),
+    ([1, 2], [2000, 700], 16, 100, 4),
+    ([40, 33], [1500, 400], 16, 70, 0),
+    ([300], [900], 8, 33, 17),
+    ([1], [3000], 256, 1000, 1),
+])
+def test_pages_that_no_query_sees_are_not_read(which, hkv, hq, q, kv, page, window, sinks):
+    """The pages behind a window are no longer the request's: their entries are
+    not asked for, whatever tile the window's first keys share."""
+    b = Batch(fmt(which, "bf16", hkv), hq, q, kv, page=page)
+    for r, (n, m) in enumerate(zip(q, kv)):
+        first, sunk = max(0, m - n + 1 - window) // page, -(-sinks // page)
+        b.table[r, sunk:max(first, sunk)] = -1
+    b.check(window, sinks, dense=False)
+
+
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 16), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 30, 2 ** 31 - 1),
+                                          (5, 2 ** 31 - 1), (1, 0)])
+def test_largest_windows_and_queries_before_any_key(which, hkv, hq, window, sinks):
+    Batch(fmt(which, "bf16", hkv), hq, [150, 1], [100, 64]).check(window, sinks)
+
+
+@pytest.mark.parametrize("which", ["64", "128", "latent"])
+def test_results_with_heads_outermost(which):
+    b = Batch(fmt(which, "fp16", 1), 8, [70, 1], [200, 900])
+    f, want = b.f, b.want(0, 0, 0.1)
+    out = torch.zeros(8, 71, f.v_dim, dtype=f.dtype, device="cuda").transpose(0, 1)
+    q = b.q.transpose(0, 1).contiguous().transpose(0, 1)
+    got, lse = gpb.attend_paged(b.plan(), q, b.pool, b.table, 0.1, out=out)
+    assert got.data_ptr() == out.data_ptr()
+    check(out, lse, want)
+    with pytest.raises(gpb.GpbError):
+        gpb.attend_paged(b.plan(), q, b.pool, b.table, 0.1,
+                         out=out[:1].expand(71, 8, f.v_dim))
+
+
+def test_an_item_whose_rows_end_past_int32_is_reported():
+    b = Batch(fmt("64", "bf16", 1), 2, [1, 1], [90, 20], stale=0.0)
+    plan = b.plan()
+    host = plan.list_host.copy()
+    host[1] = 2 ** 31 - 1                       # the first item's first row
+    plan.list.copy_(torch.from_numpy(host))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1, status=status)
+    assert int(status) == 4          # GPB_STATUS_BAD_PLAN_INPUT
+
+
 def test_a_list_that_is_not_the_plans_is_reported():
     f = fmt("64", "bf16", 1)
     b = Batch(f, 2, [1, 1], [900, 2000], stale=0.0)

@@ -357,3 +357,35 @@ def test_binding_refuses_before_the_library():
     with pytest.raises(ValueError):                       # host memory
         gpb.row_append(f, k, k, torch.zeros(64, 512, dtype=torch.bfloat16),
                        torch.zeros(3, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rot_start=2 ** 31 - 8),
+    dict(d_q=A, d_q_out=2 * A, qo_head_stride=64),       # heads of 128 values on each other
+    dict(d_q=A, d_q_out=2 * A, qo_token_stride=0),
+    dict(d_q=A, d_q_out=2 * A, qo_token_stride=256),
+    dict(q_token_stride=0, qo_token_stride=0),           # in place on one token's queries
+    dict(d_q=A, d_q_out=2 * A, qo_token_stride=-512),
+])
+def test_append_refuses_results_that_share_a_place(kw):
+    a = append_args(fmt(), **kw)
+    assert B.lib.gpb_row_append(ctypes.byref(fmt().c), ctypes.byref(a), None, None) == B.EINVAL
+
+
+def test_append_refuses_more_rows_than_a_launch_holds():
+    a = append_args(fmt(), n_rows=1 << 24)
+    assert B.lib.gpb_row_append(ctypes.byref(fmt().c), ctypes.byref(a), None, None) == B.ERANGE
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("kw", [dict(out_head_stride=64), dict(out_token_stride=0),
+                                dict(out_token_stride=508), dict(out_token_stride=-512),
+                                dict(out_head_stride=1 << 62, out_token_stride=64)])
+def test_attend_refuses_results_that_share_a_place(paged, kw):
+    assert attend_args(paged, **kw) == B.EINVAL
+
+
+def test_work_list_of_more_queries_than_a_list_holds_is_refused():
+    n = 2 ** 31 - 1
+    assert build(fmt(), 4, [n] * 5, [n] * 5)[0] == B.ERANGE
+    assert build(fmt(), 65536, [n], [5])[0] == B.ERANGE
