@@ -9,6 +9,7 @@
 // their results; the others write sums, and a join per token and KV head adds
 // its parts in the order of the list, so results do not depend on timing.
 #include <algorithm>
+#include <functional>
 #include <new>
 #include <utility>
 #include <vector>
@@ -18,7 +19,7 @@
 namespace gpb {
 namespace {
 
-constexpr int kCus = 256;
+constexpr int kCus = 256, kXcds = 8;
 
 struct Block {
   int64_t row0;
@@ -123,6 +124,73 @@ struct Planner {
   }
 };
 
+// Workgroups on CUs in the order of the list, `parts` of them, the longest
+// first.  A CU holds per_cu; the next one starts where the first ends.
+struct Rounds {
+  int cus, per_cu;
+  std::vector<int64_t> parts;
+  struct Cu {
+    double last, left[2];  // time of the last event; keys that its workgroups still have to do
+    int n;
+  };
+  std::vector<Cu> at;
+  std::vector<std::pair<double, int>> next;  // heap: the next end, of which CU
+
+  Rounds(int cus, int per_cu) : cus(cus), per_cu(per_cu) {}
+
+  int64_t time() {
+    next.clear();
+    const std::greater<std::pair<double, int>> later;
+    const size_t n = parts.size();
+    double end = 0;
+    if (per_cu != 2) {  // one that does not share, or more that do so evenly
+      for (size_t i = 0; i < n; ++i) {
+        double from = 0;
+        if (next.size() >= static_cast<size_t>(cus) * per_cu) {
+          std::pop_heap(next.begin(), next.end(), later);
+          from = next.back().first;
+          next.pop_back();
+        }
+        next.emplace_back(from + parts[i], 0);
+        std::push_heap(next.begin(), next.end(), later);
+        end = std::max(end, from + parts[i]);
+      }
+      return static_cast<int64_t>(end);
+    }
+    // Of two workgroups the older one's instructions go first: it does 1.17
+    // keys and the other 0.83 in the time that each would do one, and one alone
+    // 1.6 (measured on wide items: 2.5 and 3.55 us a tile).
+    size_t i = 0;
+    at.assign(cus, Cu{});
+    for (int w = 0; w < 2; ++w)
+      for (Cu &c : at)
+        if (i < n) c.left[c.n++] = static_cast<double>(parts[i++]);
+    const auto push = [&](int k) {
+      const Cu &c = at[k];
+      if (c.n == 0) return;
+      const double t = c.n == 1 ? c.left[0] / 1.6 : std::min(c.left[0] / 1.17, c.left[1] / 0.83);
+      next.emplace_back(c.last + t, k);
+      std::push_heap(next.begin(), next.end(), later);
+    };
+    for (int k = 0; k < cus; ++k) push(k);
+    while (!next.empty()) {
+      std::pop_heap(next.begin(), next.end(), later);
+      const auto e = next.back();
+      next.pop_back();
+      Cu &c = at[e.second];
+      const double t = e.first - c.last;
+      c.left[0] -= t * (c.n == 1 ? 1.6 : 1.17);
+      c.left[1] -= t * 0.83;
+      if (c.n == 1 || c.left[0] <= c.left[1]) c.left[0] = c.left[1];
+      --c.n;
+      c.last = end = e.first;
+      if (i < n) c.left[c.n++] = static_cast<double>(parts[i++]);
+      push(e.second);
+    }
+    return static_cast<int64_t>(end);
+  }
+};
+
 int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_plan *plan,
                int32_t *h_list, int64_t list_ints) {
   int rc = check_format(f);
@@ -201,13 +269,17 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
     const int64_t keys = static_cast<int64_t>(b.n_tiles) * p.tile_of(g.wide);
     return std::max<int64_t>(1, std::min<int64_t>(b.n_tiles, ceil_div64(keys, most)));
   };
-  // How long the batch takes if its workgroups start the longest first: the
-  // longest one where all run at once; else all of them spread evenly, and the
-  // longest of those that had to wait, which starts when the rest end.  Sums
-  // written and read again take the whole GPU about a key's time (33 ns) per
-  // 19,000 values.
+  // How long the batch takes, in keys: the longest part where all of them run
+  // at once, else what Rounds finds.  A join costs a launch (160 keys' time of
+  // 33 ns: two requests of 292 and 357 latent rows, 16 heads, take 21.3 us
+  // whole and 22.9 us in parts), and sums written and read again take the whole
+  // GPU about a key's time per 19,000 values.  Where KV heads divide the CUs,
+  // all heads do the same on their share of them.
+  const int per_cu = blocks_per_cu(which, !any_wide);
+  const int64_t like = kCus % hkv ? 1 : hkv;
   std::vector<std::pair<int64_t, int64_t>> lengths;  // keys, how many
-  auto span = [&](int64_t most) {
+  Rounds rounds(static_cast<int>(kCus / like), per_cu);
+  auto span = [&](int64_t most, int64_t to_beat) {
     lengths.clear();
     int64_t n = 0, sum = 0, longest = 0, rows = 0;
     for (const Segment &g : p.segments)
@@ -215,32 +287,31 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
         const Block &b = p.blocks[g.block0 + k];
         const int64_t parts = cut(g, b, most);
         const int64_t keys = static_cast<int64_t>(b.n_tiles) * p.tile_of(g.wide) / parts + start;
-        lengths.emplace_back(keys, hkv * parts);
+        lengths.emplace_back(keys, hkv / like * parts);
         n += hkv * parts;
         sum += hkv * parts * keys;
         longest = std::max(longest, keys);
         if (g.grouped || parts > 1) rows += hkv * parts * b.n_rows;
       }
-    const int64_t again = rows * f->v_dim / 19000;
+    const int64_t again = rows > 0 ? 160 + rows * f->v_dim / 19000 : 0;
     if (n <= slots) return longest + again;
+    if (sum / slots + again >= to_beat) return to_beat;  // even if nothing waited
     std::sort(lengths.rbegin(), lengths.rend());
-    int64_t before = 0, waits = 0;
-    for (const auto &l : lengths) {
-      waits = l.first;
-      before += l.second;
-      if (before > slots) break;
-    }
-    return std::max(longest, sum / slots + waits) + again;
+    rounds.parts.clear();
+    for (const auto &l : lengths) rounds.parts.insert(rounds.parts.end(), l.second, l.first);
+    return rounds.time() + again;
   };
   int64_t most = std::max(min_keys, ceil_div64(total, slots));
   if (uncut <= 4 * slots) {
-    int64_t best = INT64_MAX;
+    int64_t best = INT64_MAX / 2, last = 0;
     const int64_t even = most;
-    for (int64_t part : {even / 2, even * 2 / 3, even, even * 9 / 8, even * 5 / 4, even * 3 / 2,
-                         even * 2, even * 3, longest_block}) {
+    for (int64_t part : {longest_block, even * 2, even * 3 / 2, even * 5 / 4, even * 9 / 8, even,
+                         even * 4 / 5, even * 2 / 3, even / 2}) {
       part = std::max(min_keys, part);
-      const int64_t t = span(part);
-      if (t < best) best = t, most = part;
+      if (part == last) continue;
+      last = part;
+      const int64_t t = span(part, best - best / 32);
+      if (t < best - best / 32) best = t, most = part;  // (the estimate is worth no less)
     }
   }
   int64_t n_items = 0, n_partial = 0, n_joins = 0, n_refs = 0;
@@ -315,18 +386,39 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
   if (!h_list) return GPB_OK;
   if (list_ints < ints) return GPB_ERANGE;
 
-  // Items, the longest first (the last workgroups to start are then short),
-  // the KV heads of a part next to each other.
-  struct Part { int64_t keys; const Segment *g; const Block *b; int32_t x; };
+  // Items, the longest first (the last workgroups to start are then short), the
+  // KV heads of a part next to each other.
+  struct Part { int64_t keys; const Segment *g; const Block *b; int32_t x, v; };
   std::vector<Part> parts;
   for (const Segment &g : p.segments)
     for (size_t k = 0; k < g.n_blocks; ++k) {
       const Block &b = p.blocks[g.block0 + k];
       for (int32_t x = 0; x < b.parts; ++x)
-        parts.push_back({static_cast<int64_t>(b.n_tiles / b.parts) * p.tile_of(g.wide), &g, &b, x});
+        for (int32_t v = 0; v < hkv; ++v)
+          parts.push_back({static_cast<int64_t>(b.n_tiles / b.parts) * p.tile_of(g.wide), &g, &b,
+                           x, v});
     }
   std::stable_sort(parts.begin(), parts.end(),
                    [](const Part &x, const Part &y) { return x.keys > y.keys; });
+  // Item i runs on XCD i % 8, each with an L2 of its own.  The blocks of a group
+  // read the same keys at one time, so those that read the same heads and keys
+  // are dealt to as few XCDs as may be: 20 blocks of 64 rows over 32,768 shared
+  // latent rows in 9 parts, 160 us so and 184 us with the blocks of a part on
+  // any XCD.  (Other items: the heads, next to each other, find their own.)
+  for (size_t first = 0, end; first < parts.size(); first = end) {
+    for (end = first + 1; end < parts.size() && parts[end].keys == parts[first].keys &&
+                          parts[end].g == parts[first].g;)
+      ++end;
+    if (!parts[first].g->grouped) continue;
+    std::vector<Part> run(parts.begin() + first, parts.begin() + end);
+    std::stable_sort(run.begin(), run.end(), [](const Part &x, const Part &y) {
+      return x.v != y.v ? x.v < y.v : x.x < y.x;
+    });
+    size_t from = 0;
+    for (size_t xcd = 0; xcd < kXcds; ++xcd)
+      for (size_t i = first + (xcd + kXcds - first % kXcds) % kXcds; i < end; i += kXcds)
+        parts[i] = run[from++];
+  }
   AttendItem *out = reinterpret_cast<AttendItem *>(h_list);
   for (const Part &q : parts) {
     const Block &b = *q.b;
@@ -334,6 +426,7 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
     const int64_t v1 = static_cast<int64_t>(b.n_tiles) * (q.x + 1) / b.parts;
     AttendItem it{};
     it.req = q.g->req; it.row0 = static_cast<int32_t>(b.row0); it.n_rows = b.n_rows;
+    it.kv_head = q.v;
     it.key_lo = q.g->key_lo; it.key_hi = q.g->key_hi;
     it.n_tiles = static_cast<int32_t>(v1 - v0);
     if (v0 < b.n_first) {
@@ -346,13 +439,11 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
     }
     it.wide = q.g->wide;
     it.pos_min = b.pos_min; it.pos_max = b.pos_max;
-    for (int64_t v = 0; v < hkv; ++v) {
-      it.kv_head = static_cast<int32_t>(v);
-      it.partial = b.partial < 0
-                       ? -1
-                       : static_cast<int32_t>(b.partial + (v * b.parts + q.x) * b.n_rows);
-      *out++ = it;
-    }
+    it.partial = b.partial < 0
+                     ? -1
+                     : static_cast<int32_t>(b.partial + (static_cast<int64_t>(q.v) * b.parts + q.x) *
+                                                            b.n_rows);
+    *out++ = it;
   }
   std::copy(joins.begin(), joins.end(),
             reinterpret_cast<AttendJoin *>(h_list + plan->joins_at));
