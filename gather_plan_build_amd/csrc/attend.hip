@@ -16,8 +16,17 @@
 // transposing LDS reads (ds_read_b64_tr_b16) of four keys each.
 //
 // Keys and values go to LDS by direct loads, 16 bytes a lane, a row's 16-byte
-// chunks permuted within the row (swizzle) so that reads do not meet in a bank: the
-// direct load fixes the LDS place of a lane, so the lane picks its source.
+// chunks permuted within the row so that reads do not meet in a bank: the
+// direct load fixes the LDS place of a lane, so the lane picks its source.  A
+// wait then is for LDS alone, and the next tile's loads go out one by one
+// between the matrix instructions of this one.
+//
+// Three kernels, by what bounds them (each beside its function): `wide`, many
+// query rows over one tile, by the matrix and vector units; `narrow`, few rows
+// (decoding), by the latency of rows from HBM; `latent`, whose 512-value sums
+// fill the registers of a CU, by LDS reads and matrix instructions in turn.
+// Long ranges of keys are cut into parts, joined by their log-sums in a second
+// launch in the order of the work list.
 //
 // Scores, m, l and the sums are fp32; P is rounded to the row's type for the
 // second product (its errors, at most half a step each, average out; l sums
@@ -183,12 +192,11 @@ struct Attend {
   // latent), then n rows of R1 bytes (a value, or the rest of a latent).
   static constexpr int R0 = IN_KEY ? VB : KB, R1 = IN_KEY ? KB - VB : VB;
   static constexpr int ROW = R0 + R1;                          // LDS bytes per key
-  // wide tiles under way or in use: a 64-wide head's are over too soon for one
-  // to arrive meanwhile
-  static constexpr int BUFS = DK == 64 ? 4 : 2;
-  static constexpr int TILES_LDS = NARROW ? 4 * kNarrowTile * ROW : BUFS * kWideTile * ROW;
-  static constexpr int WAVE_XCHG = 2048 + 128;                 // latent: a wave's weights, maxima
   static constexpr int kRows = rows_of(IN_KEY ? 2 : DK / 128, !NARROW);  // of an item, at most
+  // the tile in use and the one under way, or in the end a row's sums
+  static constexpr int TILES_LDS =
+      NARROW ? 4 * kNarrowTile * ROW : std::max(2 * kWideTile * ROW, kRows * DV * 4);
+  static constexpr int WAVE_XCHG = 2048 + 128;                 // latent: a wave's weights, maxima
   static constexpr int RING = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kRows);
   static constexpr int LDS = RING + 4096;
   static constexpr int NT = DV / 32 / (IN_KEY ? 2 : 1);        // output tiles of a wave
@@ -276,7 +284,6 @@ struct Attend {
   // numbers come through LDS as the rows do, some tiles before those are asked
   // for, so that no wait for a page number is a wait for the loads of rows
   // behind it.  A wave has room for four tiles' numbers.
-  static constexpr int AHEAD = BUFS - 1;  // wide tiles asked for before their turn
   template <int TILE, int KEYS>
   struct Rows : Source {
     const AttendItem &it;
@@ -823,10 +830,17 @@ struct Attend {
     }
   }
 
-  // Four waves, 32 RH rows each, tiles of 64 keys in BUFS LDS buffers.  Of
+  // Four waves, 32 RH rows each, tiles of 64 keys in two LDS buffers.  Of
   // 64-wide heads a wave has room for 64 rows: every operand read from LDS then
   // serves two matrix instructions, and a tile's loads and addresses twice the
   // weights.
+  //
+  // 128-wide heads, 2,723 queries over 3,481 to 8,153 keys, 32 heads over 8: 345
+  // us, 0.78 PFLOP/s; the matrix unit is busy 45% of the time that a CU has
+  // work, the vector unit 54%, and CUs have none for a fifth of it (some
+  // 900 items on 512 places).  64-wide heads have half the products per weight:
+  // 17,337 queries, 64 heads over 8, window 1024: 450 us, 0.62 PFLOP/s, the
+  // vector unit busy 74% of the time with maxima, exponentials and sums.
   template <bool SCAN>
   static __device__ __forceinline__ bool wide(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
@@ -836,10 +850,7 @@ struct Attend {
     const bool idle = wave * 32 * RH >= it.n_rows;  // a wave without rows only loads
     typedef Loader<kWideTile, 4> Load;
     const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
-    if (it.n_tiles > 0) {
-#pragma unroll
-      for (int v = 0; v < AHEAD; ++v) rows.ask(v, v);
-    }
+    if (it.n_tiles > 0) rows.ask(0, 0);
     x8 q[RH * (DK / 16)];
     Sight see[RH];
     State st[RH];
@@ -855,24 +866,20 @@ struct Attend {
     bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
       loads_done();
-#pragma unroll
-      for (int v = 0; v < AHEAD; ++v) {
-        Load(a, it, rows, rows.row(v, v, lane), lds + v * BUF, wave, lane).all();
-        rows.ask(v + AHEAD, v + AHEAD);
-      }
+      Load(a, it, rows, rows.row(0, 0, lane), lds, wave, lane).all();
+      rows.ask(1, 1);
       lds_reads_done();
       for (int v = 0; v < it.n_tiles; ++v) {
-        loads_done<(BUFS - 2) * Load::N>();
+        loads_done();
         __syncthreads();
-        lds_u8 *now = lds + v % BUFS * BUF;
+        lds_u8 *now = lds + (v & 1) * BUF;
         const int key0 = first_key(it, v, kWideTile);
         const bool whole = whole_tile(a, it, key0, kWideTile);
         const bool odd = SCAN && !whole &&
                          __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const Load load(a, it, rows, rows.row(v + AHEAD, v + AHEAD, lane),
-                        lds + (v + AHEAD) % BUFS * BUF, wave, lane);
-        rows.ask(v + 2 * AHEAD, v + 2 * AHEAD);
+        const Load load(a, it, rows, rows.row(v + 1, v + 1, lane), lds + (~v & 1) * BUF, wave, lane);
+        rows.ask(v + 2, v + 2);
         if (odd || idle) {
           load.all();
           continue;
@@ -1202,7 +1209,7 @@ struct Attend {
 };
 
 template <typename T, int DK, int DV, bool IN_KEY, bool NARROW>
-__global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128, NARROW)) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128)) void k_attend(AttendArgs a) {
   typedef Attend<T, DK, DV, IN_KEY, NARROW> A;
   __shared__ __attribute__((aligned(1024))) uint8_t memory[A::LDS];
   lds_u8 *lds = (lds_u8 *)memory;

@@ -9,7 +9,6 @@
 // their results; the others write sums, and a join per token and KV head adds
 // its parts in the order of the list, so results do not depend on timing.
 #include <algorithm>
-#include <functional>
 #include <new>
 #include <utility>
 #include <vector>
@@ -124,73 +123,6 @@ struct Planner {
   }
 };
 
-// Workgroups on CUs in the order of the list, `parts` of them, the longest
-// first.  A CU holds per_cu; the next one starts where the first ends.
-struct Rounds {
-  int cus, per_cu;
-  std::vector<int64_t> parts;
-  struct Cu {
-    double last, left[2];  // time of the last event; keys that its workgroups still have to do
-    int n;
-  };
-  std::vector<Cu> at;
-  std::vector<std::pair<double, int>> next;  // heap: the next end, of which CU
-
-  Rounds(int cus, int per_cu) : cus(cus), per_cu(per_cu) {}
-
-  int64_t time() {
-    next.clear();
-    const std::greater<std::pair<double, int>> later;
-    const size_t n = parts.size();
-    double end = 0;
-    if (per_cu != 2) {  // one that does not share, or more that do so evenly
-      for (size_t i = 0; i < n; ++i) {
-        double from = 0;
-        if (next.size() >= static_cast<size_t>(cus) * per_cu) {
-          std::pop_heap(next.begin(), next.end(), later);
-          from = next.back().first;
-          next.pop_back();
-        }
-        next.emplace_back(from + parts[i], 0);
-        std::push_heap(next.begin(), next.end(), later);
-        end = std::max(end, from + parts[i]);
-      }
-      return static_cast<int64_t>(end);
-    }
-    // Of two workgroups the older one's instructions go first: it does 1.17
-    // keys and the other 0.83 in the time that each would do one, and one alone
-    // 1.6 (measured on wide items: 2.5 and 3.55 us a tile).
-    size_t i = 0;
-    at.assign(cus, Cu{});
-    for (int w = 0; w < 2; ++w)
-      for (Cu &c : at)
-        if (i < n) c.left[c.n++] = static_cast<double>(parts[i++]);
-    const auto push = [&](int k) {
-      const Cu &c = at[k];
-      if (c.n == 0) return;
-      const double t = c.n == 1 ? c.left[0] / 1.6 : std::min(c.left[0] / 1.17, c.left[1] / 0.83);
-      next.emplace_back(c.last + t, k);
-      std::push_heap(next.begin(), next.end(), later);
-    };
-    for (int k = 0; k < cus; ++k) push(k);
-    while (!next.empty()) {
-      std::pop_heap(next.begin(), next.end(), later);
-      const auto e = next.back();
-      next.pop_back();
-      Cu &c = at[e.second];
-      const double t = e.first - c.last;
-      c.left[0] -= t * (c.n == 1 ? 1.6 : 1.17);
-      c.left[1] -= t * 0.83;
-      if (c.n == 1 || c.left[0] <= c.left[1]) c.left[0] = c.left[1];
-      --c.n;
-      c.last = end = e.first;
-      if (i < n) c.left[c.n++] = static_cast<double>(parts[i++]);
-      push(e.second);
-    }
-    return static_cast<int64_t>(end);
-  }
-};
-
 int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_plan *plan,
                int32_t *h_list, int64_t list_ints) {
   int rc = check_format(f);
@@ -252,8 +184,9 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
   }
 
   // Cut long ranges of keys into parts of at most `most` keys, none shorter
-  // than min_keys.  A workgroup's start and end take as long as `start` keys.
-  bool any_wide = false;
+  // than min_keys (one query of 737 keys, 32 heads over 8: 13.4 us with parts of
+  // 256 keys, 13.7 of 128, 15.7 of 64).  A workgroup's start and end take as
+  // long as `start` keys.
   int64_t total = 0, uncut = 0, longest_block = 1;
   for (const Segment &g : p.segments)
     for (size_t k = 0; k < g.n_blocks; ++k) {
@@ -261,25 +194,22 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
       total += hkv * keys;
       uncut += hkv;
       longest_block = std::max(longest_block, keys);
-      any_wide |= g.wide;
     }
-  const int64_t slots = kCus * blocks_per_cu(which, !any_wide);
-  const int64_t min_keys = any_wide ? 256 : 128, start = which == 2 ? 150 : 300;
+  const int64_t slots = kCus * blocks_per_cu(which);
+  const int64_t min_keys = 256, start = which == 2 ? 150 : 300;
   auto cut = [&](const Segment &g, const Block &b, int64_t most) {
     const int64_t keys = static_cast<int64_t>(b.n_tiles) * p.tile_of(g.wide);
     return std::max<int64_t>(1, std::min<int64_t>(b.n_tiles, ceil_div64(keys, most)));
   };
-  // How long the batch takes, in keys: the longest part where all of them run
-  // at once, else what Rounds finds.  A join costs a launch (160 keys' time of
-  // 33 ns: two requests of 292 and 357 latent rows, 16 heads, take 21.3 us
-  // whole and 22.9 us in parts), and sums written and read again take the whole
-  // GPU about a key's time per 19,000 values.  Where KV heads divide the CUs,
-  // all heads do the same on their share of them.
-  const int per_cu = blocks_per_cu(which, !any_wide);
-  const int64_t like = kCus % hkv ? 1 : hkv;
+  // How long the batch takes, in keys, if its workgroups start the longest
+  // first: the longest one where all run at once; else all of them spread
+  // evenly, and the longest of those that had to wait, which starts when the
+  // rest end.  A join costs a launch (160 keys' time of 33 ns: two requests of
+  // 292 and 357 latent rows, 16 heads, take 21.3 us whole and 22.9 us in
+  // parts), and sums written and read again take the whole GPU about a key's
+  // time per 19,000 values.
   std::vector<std::pair<int64_t, int64_t>> lengths;  // keys, how many
-  Rounds rounds(static_cast<int>(kCus / like), per_cu);
-  auto span = [&](int64_t most, int64_t to_beat) {
+  auto span = [&](int64_t most) {
     lengths.clear();
     int64_t n = 0, sum = 0, longest = 0, rows = 0;
     for (const Segment &g : p.segments)
@@ -287,7 +217,7 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
         const Block &b = p.blocks[g.block0 + k];
         const int64_t parts = cut(g, b, most);
         const int64_t keys = static_cast<int64_t>(b.n_tiles) * p.tile_of(g.wide) / parts + start;
-        lengths.emplace_back(keys, hkv / like * parts);
+        lengths.emplace_back(keys, hkv * parts);
         n += hkv * parts;
         sum += hkv * parts * keys;
         longest = std::max(longest, keys);
@@ -295,23 +225,24 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
       }
     const int64_t again = rows > 0 ? 160 + rows * f->v_dim / 19000 : 0;
     if (n <= slots) return longest + again;
-    if (sum / slots + again >= to_beat) return to_beat;  // even if nothing waited
     std::sort(lengths.rbegin(), lengths.rend());
-    rounds.parts.clear();
-    for (const auto &l : lengths) rounds.parts.insert(rounds.parts.end(), l.second, l.first);
-    return rounds.time() + again;
+    int64_t before = 0, waits = 0;
+    for (const auto &l : lengths) {
+      waits = l.first;
+      before += l.second;
+      if (before > slots) break;
+    }
+    return std::max(longest, sum / slots + waits) + again;
   };
   int64_t most = std::max(min_keys, ceil_div64(total, slots));
   if (uncut <= 4 * slots) {
-    int64_t best = INT64_MAX / 2, last = 0;
+    int64_t best = INT64_MAX;
     const int64_t even = most;
-    for (int64_t part : {longest_block, even * 2, even * 3 / 2, even * 5 / 4, even * 9 / 8, even,
-                         even * 4 / 5, even * 2 / 3, even / 2}) {
+    for (int64_t part : {longest_block, even * 3, even * 2, even * 3 / 2, even * 5 / 4,
+                         even * 9 / 8, even, even * 2 / 3, even / 2}) {
       part = std::max(min_keys, part);
-      if (part == last) continue;
-      last = part;
-      const int64_t t = span(part, best - best / 32);
-      if (t < best - best / 32) best = t, most = part;  // (the estimate is worth no less)
+      const int64_t t = span(part);
+      if (t < best) best = t, most = part;
     }
   }
   int64_t n_items = 0, n_partial = 0, n_joins = 0, n_refs = 0;
