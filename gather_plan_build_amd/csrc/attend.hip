@@ -835,10 +835,10 @@ struct Attend {
   // serves two matrix instructions, and a tile's loads and addresses twice the
   // weights.
   //
-  // 128-wide heads, 2,723 queries over 3,481 to 8,153 keys, 32 heads over 8: 345
-  // us, 0.78 PFLOP/s; the matrix unit is busy 45% of the time that a CU has
-  // work, the vector unit 54%, and CUs have none for a fifth of it (some
-  // 900 items on 512 places).  64-wide heads have half the products per weight:
+  // 128-wide heads, 2,723 queries over 3,481 to 8,153 keys, 32 heads over 8: 323
+  // us and a join of 9, 0.78 PFLOP/s; the matrix unit is busy 45% of the time that
+  // a CU has work, the vector unit 54%, and CUs have none for a fifth of it (776
+  // items on 512 places).  64-wide heads have half the products per weight:
   // 17,337 queries, 64 heads over 8, window 1024: 450 us, 0.62 PFLOP/s, the
   // vector unit busy 74% of the time with maxima, exponentials and sums.
   template <bool SCAN>
@@ -1052,7 +1052,13 @@ struct Attend {
   }
 
   // Four waves over the same rows, each with tiles of 32 keys of its own;
-  // their sums meet in LDS at the end, the waves in order.
+  // their sums meet in LDS at the end, the waves in order.  A wave waits for no
+  // other before that, so eight waves of a CU have their loads under way at
+  // different times, and a tile's loads are out before its predecessor's
+  // products.  Eight queries over windows of 4096 keys, 64 heads over 8, 64
+  // wide: 17.5 us and a join of 4 for 67 MB, 3.8 TB/s with the start (item, page
+  // numbers, first rows: three trips to HBM).  One query over 737 keys is start
+  // and join alone: 13.4 us.
   template <bool SCAN>
   static __device__ __forceinline__ bool narrow(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
@@ -1237,7 +1243,9 @@ __global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128)) void 
 
 // The rows of one token and KV head: parts weighted by 2^(m - max m), in the
 // order of the list.  A wave a row; a lane first takes a part's m and l, then
-// DV / 64 values of every part.
+// DV / 64 values of every part, four parts' under way at once.  Bound by latency
+// (the reference, m and l, sums: 4 us for 64 rows of 8 parts) and, with many
+// rows, by the sums: 8.8 us for 22 MB.
 template <typename T, int DV>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   typedef Attend<T, 64, 64, false, false> A;  // for what depends on T alone
