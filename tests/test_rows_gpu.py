@@ -312,6 +312,24 @@ def test_latent_rows_that_are_not_finite(bad):
     assert not torch.isfinite(out[30:, :, 7]).any()
 
 
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 16), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 3)])
+def test_values_that_are_not_finite_behind_a_shared_prefix(which, hkv, hq, window, sinks):
+    """The last key of each request, which its last query alone sees, and a
+    shared key that a window hides from all."""
+    f = fmt(which, "bf16", hkv)
+    b = Batch(f, hq, [2, 40, 1, 3], [200, 290, 300, 260], groups=[(0, 4, 128)], stale=0.0)
+    at = 0 if f.values_in_key else hkv * f.k_dim     # a value
+    for r, n in ((0, 200), (1, 290), (3, 260)):
+        b.rows[r][n - 1, at] = float("inf")
+        b.pool[b.lists[r][(n - 1) // 64] * 64 + (n - 1) % 64, at] = float("inf")
+    if window:
+        for r in range(4):
+            b.rows[r][5, at] = float("nan")
+        b.pool[b.lists[0][0] * 64 + 5, at] = float("nan")
+    b.check(window, sinks, dense=False)
+
+
 def test_large_scores_and_a_growing_maximum():
     """Keys that grow along the sequence move the running maximum in every
     tile; scores of some hundreds stay in range."""
@@ -562,6 +580,85 @@ def test_two_captured_graphs_of_a_decode_step():
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(bufs[0], eager[0]) and torch.equal(bufs[1], eager[1])
+
+
+@pytest.mark.parametrize("which", ["64", "128", "latent"])
+def test_batches_without_queries_or_without_keys(which):
+    f = fmt(which, "bf16", 1)
+    none = gpb.AttendPlan(f, 4, [], [])
+    out, lse = gpb.attend_paged(none, normal(1, 0, 4, f.k_dim), normal(2, 64, f.row_bytes // 2),
+                                torch.zeros(0, 3, dtype=torch.int32, device="cuda"), 0.1)
+    assert out.shape == (0, 4, f.v_dim) and lse.shape == (0, 4)
+    bare = gpb.AttendPlan(f, 4, [3, 0, 70], [0, 5, 0])
+    q, pool = normal(3, 73, 4, f.k_dim), normal(4, 64, f.row_bytes // 2)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = gpb.attend_paged(bare, q, pool, ints([[-1], [0], [-1]]), 0.1, status=status)
+    o2, l2 = gpb.attend_dense(bare, q, pool, ints([99, 0, -7]), 0.1, status=status)
+    for o, l in ((out, lse), (o2, l2)):
+        assert not o.any() and (l == -math.inf).all()
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("which,hkv,hq", [("64", 1, 8), ("128", 2, 8), ("latent", 1, 16)])
+def test_prefill_captured_and_replayed_on_new_rows(which, hkv, hq):
+    """Wide items with parts and joins, in a graph: every replay reads what the
+    buffers hold then, an odd value in one of them included."""
+    b = Batch(fmt(which, "bf16", hkv), hq, [70, 5], [1900, 1100], stale=0.0)
+    plan = b.plan()
+    assert plan.c.n_joins > 0
+    out = torch.empty(75, hq, b.f.v_dim, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(75, hq, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gpb.attend_dense(plan, b.q, b.dense, b.k_bases, 0.1, out=out, lse=lse)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gpb.attend_dense(plan, b.q, b.dense, b.k_bases, 0.1, out=out, lse=lse)
+    for turn in range(4):
+        b.dense.copy_(normal(50 + turn, *b.dense.shape))
+        if turn == 2:
+            b.dense[1890, :8] = float("nan")      # seen by the last ten queries of request 0
+        eager = gpb.attend_dense(plan, b.q, b.dense, b.k_bases, 0.1)
+        torch.cuda.synchronize()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), eager[0].view(torch.int16))
+        assert torch.equal(lse.view(torch.int32), eager[1].view(torch.int32))
+        odd = ~torch.isfinite(out).flatten(1).all(1)
+        want = torch.zeros(75, dtype=torch.bool, device="cuda")
+        if turn == 2:
+            want[60:70] = True
+        assert torch.equal(odd, want)
+
+
+def test_two_threads_on_two_streams():
+    import threading
+    parts = [Batch(fmt("128", "bf16", 2), 8, [1, 90], [1500, 1800], seed=7 + i) for i in range(2)]
+    plans = [b.plan() for b in parts]
+    want = [gpb.attend_paged(p, b.q, b.pool, b.table, 0.1) for p, b in zip(plans, parts)]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got[i].append(gpb.attend_paged(plans[i], parts[i].q, parts[i].pool,
+                                               parts[i].table, 0.1))
+            stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for o, l in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
 
 
 # ------------------------------------------------------------------ together
