@@ -15,8 +15,8 @@
 // heads, then every lane moves 16-byte chunks, two chunks where the pair's
 // halves lie rot_dim / 2 apart, so that a head can be rotated in place.
 // 44,600 tokens of latent rows and 16 query heads of 576 values to the pool and
-// token-packed: 331 us for 1.80 GB, 5.4 TB/s, where a large copy reaches 4.9;
-// 4,099 tokens of 28 query and 4 + 4 other heads of 128: 16.3 us for 75.6 MB (4.7
+// token-packed: 316 us for 1.80 GB, 5.7 TB/s, where large copies reach 4.9 to 6.7;
+// 4,099 tokens of 28 query and 4 + 4 other heads of 128: 15.7 us for 75.6 MB (4.8
 // TB/s); 8 tokens: 4 us, the launch and two trips to HBM.
 #include "row_format.h"
 
@@ -50,11 +50,15 @@ __device__ __forceinline__ u32x4 narrow(f32x8 v) {
   return __builtin_bit_cast(u32x4, __builtin_convertvector(v, typename Vec<T>::x8));
 }
 
+// Both past the caches: nothing is touched twice here, and rows that fill whole
+// lines need not be fetched first.  44,600 latent rows: 316 us so, 333 with plain
+// stores, 328 with plain loads and stores; 4,099 tokens of 36 heads: 14.8, 17.0
+// and 14.5.
 __device__ __forceinline__ u32x4 load16(const uint16_t *p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
 }
 __device__ __forceinline__ void store16(uint8_t *p, u32x4 v) {
-  *reinterpret_cast<u32x4 *>(p) = v;
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
 }
 
 template <typename T>
