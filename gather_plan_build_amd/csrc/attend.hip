@@ -736,8 +736,9 @@ struct Attend {
       const uint64_t to = __shfl(static_cast<uint32_t>(at), r, 64) |
                           static_cast<uint64_t>(__shfl(static_cast<uint32_t>(at >> 32), r, 64))
                               << 32;
-      if (row0 + r < it.n_rows)
-        *reinterpret_cast<Loose *>(a.out + static_cast<int64_t>(to) + 32 * t0 + c * 8) = x;
+      if (row0 + r < it.n_rows)  // past the caches: 3% of the windowed prefill's time
+        __builtin_nontemporal_store(
+            x, reinterpret_cast<Loose *>(a.out + static_cast<int64_t>(to) + 32 * t0 + c * 8));
     }
     if (half == 0 && t0 == 0 && a.lse && row < it.n_rows) a.lse[lse_at] = log_sum(st.m, l);
     lds_reads_done();
