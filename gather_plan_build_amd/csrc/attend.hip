@@ -39,26 +39,6 @@
 namespace gpb {
 namespace {
 
-struct AttendArgs {
-  const int32_t *list;
-  const uint16_t *q;
-  int64_t q_ts, q_hs;
-  const uint8_t *rows;      // dense buffer or pool
-  int64_t n_rows;           // rows of it; paged: of its whole pages
-  const int32_t *pages;     // NULL: dense
-  const int32_t *base;      // k_bases (dense), page_base or NULL (paged)
-  int64_t n_listed, pages_stride;
-  uint16_t *out;
-  int64_t o_ts, o_hs;
-  float *lse;
-  float *sums, *ml;         // workspace: sums [partial rows][DV], (m, l) pairs
-  int32_t *status;
-  float c;                  // scale * log2(e)
-  int32_t row_bytes, page_rows, page_shift, n_pages, window, sinks;
-  int32_t G, hkv, n_heads, n_tokens, bs, max_keys;
-  int32_t n_items, n_joins, n_refs, n_partial_rows, joins_at, refs_at, positions_at;
-};
-
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -213,24 +193,17 @@ struct Attend {
   // its page's number (paged).  A base that leads outside the rows, or outside
   // the page list, is reported and all the item's keys read row 0; so is a page
   // outside the pool, and its keys read page 0.
-  struct Source {
+  struct Source : AttendKeys {
     const uint8_t *src;
     const int32_t *pages;  // of the request's first page
     int32_t *status;
     uint32_t stride;
-    int page_rows, page_shift, lo, last;
-    int sunk, near, behind;  // keys [sunk, near) are read as `behind`
+    int page_rows, page_shift;
     uint32_t n_pages;
 
     __device__ __forceinline__ Source(const AttendArgs &a, const AttendItem &it)
-        : src(a.rows), pages(nullptr), status(a.status), stride(a.row_bytes),
-          page_rows(a.page_rows), page_shift(a.page_shift), lo(it.key_lo),
-          last(max(min(it.key_hi - 1, it.pos_max), lo)), sunk(0), near(0), behind(0), n_pages(0) {
-      if (a.window > 0) {
-        sunk = a.sinks;
-        near = max(lo, it.pos_min + 1 - a.window);
-        behind = near <= last ? near : max(sunk - 1, lo);
-      }
+        : AttendKeys(a, it), src(a.rows), pages(nullptr), status(a.status), stride(a.row_bytes),
+          page_rows(a.page_rows), page_shift(a.page_shift), n_pages(0) {
       const int64_t base = uniform<int64_t>(a.base ? a.base[it.req] : it.req * a.pages_stride);
       bool ok;
       if (a.pages) {
@@ -245,13 +218,6 @@ struct Attend {
         stride = 0;
         if (status && it.n_tiles > 0) atomicOr(status, GPB_STATUS_BAD_DESCRIPTOR);
       }
-    }
-    // The key, or if no row sees it one that some row sees: the pages behind a
-    // window and past the last query may no longer, or not yet, be the
-    // request's.
-    __device__ __forceinline__ int in_range(int key) const {
-      key = max(key, lo);
-      return min(key >= sunk && key < near ? behind : key, last);
     }
     __device__ __forceinline__ uint32_t page_of(uint32_t key) const {
       return page_shift >= 0 ? key >> page_shift : key / static_cast<uint32_t>(page_rows);
@@ -1221,21 +1187,7 @@ __global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128)) void 
   __shared__ __attribute__((aligned(1024))) uint8_t memory[A::LDS];
   lds_u8 *lds = (lds_u8 *)memory;
   const AttendItem it = reinterpret_cast<const AttendItem *>(a.list)[blockIdx.x];
-  // the list is the caller's device memory: an item outside the batch is left
-  // out, whatever it holds
-  const int64_t all = static_cast<int64_t>(a.n_tokens) * a.G;
-  const bool ok = it.req >= 0 && it.req < a.bs && it.row0 >= 0 && it.n_rows >= 1 &&
-                  it.n_rows <= rows_of(IN_KEY ? 2 : DK / 128, it.wide) &&
-                  !(NARROW && it.wide) &&
-                  static_cast<int64_t>(it.row0) + it.n_rows <= all &&
-                  it.kv_head >= 0 && it.kv_head < a.hkv && it.key_lo >= 0 &&
-                  it.key_lo <= it.key_hi && it.key_hi <= a.max_keys &&
-                  (it.n_tiles == 0 || it.key_lo < it.key_hi) && it.n_tiles >= 0 &&
-                  it.n_tiles <= a.max_keys / kNarrowTile + 1 && it.n_first >= 0 &&
-                  it.tile0 >= 0 && it.tile1 >= 0 && it.tile0 <= a.max_keys / kNarrowTile &&
-                  it.tile1 <= a.max_keys / kNarrowTile && it.partial >= -1 &&
-                  it.partial <= a.n_partial_rows - (it.partial < 0 ? 0 : it.n_rows);
-  if (!ok) {
+  if (!item_fits(a, it, IN_KEY ? 2 : DK / 128, NARROW)) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, GPB_STATUS_BAD_PLAN_INPUT);
     return;
   }
@@ -1401,16 +1353,8 @@ int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io 
   a.ml = a.sums + static_cast<int64_t>(p->n_partial_rows) * p->format.v_dim;
   a.status = d_status;
   a.c = io->scale * 1.44269504088896341f;
-  a.row_bytes = p->format.row_bytes; a.page_rows = p->page_rows;
-  a.page_shift = p->page_rows & (p->page_rows - 1) ? -1 : __builtin_ctz(p->page_rows);
+  plan_args(*p, &a);
   a.n_pages = static_cast<int32_t>(usable / p->page_rows);
-  // (no position reaches 2^30, so a larger window is no window)
-  a.window = std::min(p->window, 1 << 30); a.sinks = std::min(p->sinks, 1 << 30);
-  a.hkv = p->format.n_kv_heads; a.n_heads = p->n_heads; a.G = p->n_heads / a.hkv;
-  a.n_tokens = p->n_tokens; a.bs = p->bs; a.max_keys = p->max_keys;
-  a.n_items = p->n_items; a.n_joins = p->n_joins; a.n_refs = p->n_refs;
-  a.n_partial_rows = p->n_partial_rows;
-  a.joins_at = p->joins_at; a.refs_at = p->refs_at; a.positions_at = p->positions_at;
   const bool narrow = p->n_wide == 0;
   return p->format.dtype == GPB_BF16
              ? launch_format<__bf16>(which, a, narrow, as_stream(stream))

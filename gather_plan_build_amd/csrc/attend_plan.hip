@@ -68,7 +68,8 @@ struct Planner {
     const int64_t b0 = near < hi ? near / tn : end;
     if (a1 > a0 && a1 < b0) {
       b->n_first = static_cast<int32_t>(a1 - a0);
-      b->tile1 = static_cast<int32_t>(b0);
+      // (shared keys may all lie behind the window of the group's queries)
+      b->tile1 = b0 < end ? static_cast<int32_t>(b0) : 0;
       b->n_tiles = static_cast<int32_t>(b->n_first + (end - b0));
     } else {
       const int64_t from = a1 > a0 ? a0 : b0;

@@ -661,6 +661,26 @@ def test_two_threads_on_two_streams():
             assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
 
 
+@pytest.mark.parametrize("which,hkv,hq", [("64", 1, 4), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("q,kv,page,groups,window,sinks", [
+    ([1, 1], [60, 60], 16, [(0, 2, 48)], 12, 4),
+    ([1, 1], [1020, 1018], 16, [(0, 2, 1008)], 8, 4),
+    ([1, 2, 1], [57, 60, 58], 1, [(0, 3, 56)], 1, 3),
+    ([1, 1], [60, 60], 16, [(0, 2, 48)], 12, 0),
+])
+def test_shared_keys_behind_the_window(which, hkv, hq, q, kv, page, groups, window, sinks):
+    """The window hides the shared keys but for the first tokens, and the batch
+    ends in the tile they end in; the workspace holds what was there before."""
+    b = Batch(fmt(which, "bf16", hkv), hq, q, kv, page=page, groups=groups)
+    plan = b.plan(window, sinks)
+    assert plan.c.n_joins > 0
+    ws = plan.workspace().fill_(255)        # NaN
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1, workspace=ws, status=status)
+    check(out, lse, b.want(window, sinks, 0.1))
+    assert int(status) == 0
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():

@@ -8,6 +8,7 @@ import torch
 
 import gather_plan_build_amd as gpb
 from gather_plan_build_amd import binding as B
+import rows_list
 
 A = 0x100000  # an address that is never dereferenced
 
@@ -389,3 +390,57 @@ def test_work_list_of_more_queries_than_a_list_holds_is_refused():
     n = 2 ** 31 - 1
     assert build(fmt(), 4, [n] * 5, [n] * 5)[0] == B.ERANGE
     assert build(fmt(), 65536, [n], [5])[0] == B.ERANGE
+
+
+# ------------------------------------------------------------------ what the kernels make of a list
+
+@pytest.fixture(scope="module")
+def check_lists(tmp_path_factory):
+    return rows_list.library(tmp_path_factory.mktemp("lists"))
+
+
+def grouped_batches(seed, n):
+    """Random batches whose first requests share keys, with windows and first
+    tokens and pages that end anywhere in a tile."""
+    rng = np.random.default_rng(seed)
+    for _ in range(n):
+        bs = int(rng.integers(1, 6))
+        q = rng.integers(0, rng.choice([3, 12, 60]), bs)
+        kv = rng.integers(0, rng.choice([80, 400, 1500]), bs)
+        page = int(rng.choice([1, 3, 8, 16, 32, 50, 64]))
+        groups = []
+        if bs > 1 and rng.random() < 0.8:
+            n_g = int(rng.integers(2, bs + 1))
+            shared = page * int(rng.integers(1, 2 + rng.choice([40, 300]) // page))
+            kv[:n_g] = shared + q[:n_g] + rng.integers(0, rng.choice([2, 20, 100]), n_g)
+            groups = [(0, n_g, shared)]
+        window = int(rng.choice([0, 1, 5, 12, 33, 200]))
+        sinks = int(rng.choice([0, 1, 4, 17, 40, 1000]))
+        which = str(rng.choice(["64", "128", "latent"]))
+        hkv = 1 if which == "latent" else int(rng.integers(1, 3))
+        yield (fmt(which, hkv=hkv), hkv * int(rng.choice([1, 4, 7, 16, 40])), list(q), list(kv),
+               window, sinks, page, groups)
+
+
+BEHIND_THE_WINDOW = [       # shared keys that the window hides but for the first tokens
+    (("128", 1), 4, [1, 1], [60, 60], 12, 4, 16, [(0, 2, 48)]),
+    (("64", 1), 4, [1, 1], [1020, 1018], 8, 4, 16, [(0, 2, 1008)]),
+]
+
+
+@pytest.mark.parametrize("f,hq,q,kv,window,sinks,page,groups", BEHIND_THE_WINDOW)
+def test_items_of_shared_keys_behind_the_window_are_taken(check_lists, f, hq, q, kv, window,
+                                                          sinks, page, groups):
+    rc, plan, lst = build(fmt(f[0], hkv=f[1]), hq, q, kv, window, sinks, page, groups)
+    assert rc == B.OK
+    assert rows_list.outcome(check_lists.list_items_fit, plan, lst) == (0, -1)
+    covered(fmt(f[0], hkv=f[1]), hq, q, kv, window, sinks, page, groups)
+
+
+def test_every_item_of_random_batches_is_taken(check_lists):
+    for case in grouped_batches(5, 4000):
+        rc, plan, lst = build(*case)
+        assert rc == B.OK
+        assert rows_list.outcome(check_lists.list_items_fit, plan, lst) == (0, -1), case[1:]
+    for case in grouped_batches(6, 60):
+        covered(*case)
