@@ -119,12 +119,14 @@ struct AttendKeys {
     if (a.window > 0) {
       sunk = a.sinks;
       near = std::max(lo, it.pos_min + 1 - a.window);
-      behind = near <= last ? near : std::max(sunk - 1, lo);
+      // (shared keys may all lie behind the window but for the first tokens)
+      if (near > last) last = std::max(std::min(last, sunk - 1), lo);
+      behind = near;
     }
   }
-  // The key, or if no row sees it one that some row sees: the pages behind a
-  // window and past the last query may no longer, or not yet, be the
-  // request's.
+  // The key, or if no row sees it one that some row sees (an item that has
+  // tiles has such a one): the pages behind a window and past the last query
+  // may no longer, or not yet, be the request's.
   __host__ __device__ int in_range(int key) const {
     key = std::max(key, lo);
     return std::min(key >= sunk && key < near ? behind : key, last);

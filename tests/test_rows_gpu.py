@@ -681,6 +681,22 @@ def test_shared_keys_behind_the_window(which, hkv, hq, q, kv, page, groups, wind
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 16), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("q,kv,page,shared,window,sinks", [
+    ([1, 1], [20, 20], 8, 16, 3, 4),
+    ([1, 2, 1], [600, 611, 602], 3, 594, 5, 7),
+    ([40, 33], [500, 480], 16, 432, 8, 17),
+])
+def test_shared_pages_that_no_query_sees_are_not_read(which, hkv, hq, q, kv, page, shared, window,
+                                                      sinks):
+    b = Batch(fmt(which, "bf16", hkv), hq, q, kv, page=page, groups=[(0, len(q), shared)])
+    for r, (n, m) in enumerate(zip(q, kv)):
+        first = (m - n + 1 - window) // page
+        assert min(kv) - max(q) + 1 - window > shared - page
+        b.table[r, -(-sinks // page):min(first, shared // page)] = -1
+    b.check(window, sinks, dense=False)
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():

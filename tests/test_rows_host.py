@@ -444,3 +444,17 @@ def test_every_item_of_random_batches_is_taken(check_lists):
         assert rows_list.outcome(check_lists.list_items_fit, plan, lst) == (0, -1), case[1:]
     for case in grouped_batches(6, 60):
         covered(*case)
+
+
+def test_keys_of_items_behind_the_window_are_seen(check_lists):
+    # keys 17 .. 31 of the one tile are past the shared keys, 4 .. 15 seen by no query
+    rc, plan, lst = build(fmt("64", hkv=1), 4, [1, 1], [20, 20], 3, 4, 8, [(0, 2, 16)])
+    assert rc == B.OK
+    assert rows_list.outcome(check_lists.list_keys_seen, plan, lst) == (0, -1)
+
+
+def test_only_keys_that_a_query_sees_are_read(check_lists):
+    for case in grouped_batches(7, 4000):
+        rc, plan, lst = build(*case)
+        assert rc == B.OK
+        assert rows_list.outcome(check_lists.list_keys_seen, plan, lst) == (0, -1), case[1:]
