@@ -702,19 +702,20 @@ class _on:
         import torch
         self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
         self.other = None   # a stream that is not the device's current one
+        self.used = torch.cuda.current_stream(index)   # the one the kernels run on
         if stream is None:
-            self.raw = torch.cuda.current_stream(index).cuda_stream
+            self.raw = self.used.cuda_stream
         elif isinstance(stream, int):
             self.raw = stream
-            if stream != torch.cuda.current_stream(index).cuda_stream:
-                self.other = torch.cuda.ExternalStream(stream, device=index) if stream else \
-                    torch.cuda.default_stream(index)
+            if stream != self.used.cuda_stream:
+                self.other = self.used = torch.cuda.ExternalStream(stream, device=index) \
+                    if stream else torch.cuda.default_stream(index)
         else:
             if stream.device.index != index:
                 raise ValueError("the stream is on %s, the tensors on GPU %d"
                                  % (stream.device, index))
             self.raw = stream.cuda_stream
-            self.other = stream
+            self.other = self.used = stream
 
     def __enter__(self):
         if self.guard is not None:
@@ -800,7 +801,8 @@ class AttendPlan:
     and the first ``sinks`` of the sequence.  ``groups`` lists (first request,
     number of requests, shared keys): consecutive requests that begin with the same
     whole pages, read once for all of them (paged attention only).  One plan serves
-    every layer of the batch."""
+    every layer of the batch, on any stream, and may be dropped while calls with it
+    are under way; a captured graph needs it for as long as it is replayed."""
 
     def __init__(self, fmt, n_heads, q_lens, kv_lens, window=0, sinks=0, page_size=64,
                  groups=(), device="cuda"):
@@ -829,7 +831,14 @@ class AttendPlan:
         self.device = torch.device("cuda", torch.cuda.current_device()) \
             if dev.index is None else dev
         self.list = torch.from_numpy(self.list_host).to(self.device)
+        self.list_stream = torch.cuda.current_stream(self.device).cuda_stream
         self.list_ptr, self.ref = self.list.data_ptr(), ctypes.byref(self.c)
+
+    def read_on(self, on):
+        """The list is read by kernels on the stream of ``on``: should the plan go
+        before they end, its memory is not handed out until they have."""
+        if on.raw != self.list_stream:
+            self.list.record_stream(on.used)
 
     def room(self, out, lse, own_lse, workspace):
         """Results and workspace of one call, where the caller has none."""
@@ -860,6 +869,7 @@ def _attend(plan, q, scale, out, lse, workspace, status, stream, call, what, **t
     q_ts, q_hs = _heads(q, T, plan.n_heads, fmt.k_dim, fmt.dtype, "q")
     on = _on(dev.index, stream)
     with on as st:
+        plan.read_on(on)
         if out is None or own_lse or (workspace is None and plan.workspace_bytes):
             if on.other is None:
                 out, lse, workspace = plan.room(out, lse, own_lse, workspace)

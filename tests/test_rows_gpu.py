@@ -697,6 +697,34 @@ def test_shared_pages_that_no_query_sees_are_not_read(which, hkv, hq, q, kv, pag
     b.check(window, sinks, dense=False)
 
 
+@pytest.mark.parametrize("given", ["stream", "raw", "current"])
+def test_a_plan_dropped_while_another_stream_reads_its_list(given):
+    """The list's memory is not handed out again before the call that waits on
+    the other stream has ended."""
+    b = Batch(fmt("128", "bf16", 2), 8, [1, 40], [1500, 1800])
+    plan = b.plan()
+    want = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1)
+    torch.cuda.synchronize()
+    place, size = plan.list.data_ptr(), plan.list.numel()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1 << 26)                     # some tens of milliseconds
+        if given == "current":
+            got = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1)
+    if given != "current":
+        got = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1,
+                               stream=side if given == "stream" else side.cuda_stream)
+    ended = torch.cuda.Event()
+    ended.record(side)
+    del plan
+    others = [torch.full((size,), -1, dtype=torch.int32, device="cuda") for _ in range(8)]
+    waiting = not ended.query()
+    torch.cuda.synchronize()
+    assert waiting, "the other stream was done too soon to tell"
+    assert place not in [x.data_ptr() for x in others]
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():

@@ -458,3 +458,31 @@ def test_only_keys_that_a_query_sees_are_read(check_lists):
         rc, plan, lst = build(*case)
         assert rc == B.OK
         assert rows_list.outcome(check_lists.list_keys_seen, plan, lst) == (0, -1), case[1:]
+
+
+def test_a_plans_list_is_recorded_on_the_stream_that_reads_it(monkeypatch):
+    """The allocator must not hand the list's memory out while a stream other
+    than the one it was made on may still read it."""
+    import contextlib
+    from types import SimpleNamespace
+
+    seen = []
+    f = fmt()
+    plan = gpb.AttendPlan.__new__(gpb.AttendPlan)
+    plan.fmt, plan.n_heads, plan.n_tokens, plan.workspace_bytes = f, 4, 3, 0
+    plan.device = torch.device("cuda", 0)
+    plan.list, plan.list_stream = SimpleNamespace(record_stream=seen.append), 77
+
+    def on(index, stream):
+        c = contextlib.nullcontext(stream.cuda_stream)
+        c.raw, c.used, c.other = stream.cuda_stream, stream, stream
+        return c
+
+    monkeypatch.setattr(B, "_on", on)
+    monkeypatch.setattr(B, "_same_device", lambda *a, **kw: None)
+    q, out = (torch.zeros(3, 4, 128, dtype=torch.bfloat16) for _ in range(2))
+    for raw in (5, 77):
+        stream = SimpleNamespace(cuda_stream=raw)
+        B._attend(plan, q, 0.1, out, None, None, None, stream, lambda *a: B.OK, "attend")
+        assert seen == ([stream] if raw == 5 else []), raw
+        seen.clear()
