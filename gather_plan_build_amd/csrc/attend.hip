@@ -1314,6 +1314,7 @@ int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io 
   if (n_rows < 0 || n_listed < 0 || pages_stride < 0 || workspace_bytes < 0) return GPB_EINVAL;
   if (n_rows > INT32_MAX) return GPB_ERANGE;
   if (p->n_tokens == 0) return GPB_OK;
+  if (p->bs == 0) return GPB_EINVAL;
   if (!d_list || !io->d_q || !io->d_out) return GPB_EINVAL;
   if (workspace_bytes < p->workspace_bytes || (p->workspace_bytes > 0 && !d_workspace))
     return GPB_EINVAL;

@@ -486,3 +486,9 @@ def test_a_plans_list_is_recorded_on_the_stream_that_reads_it(monkeypatch):
         B._attend(plan, q, 0.1, out, None, None, None, stream, lambda *a: B.OK, "attend")
         assert seen == ([stream] if raw == 5 else []), raw
         seen.clear()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_plan_with_queries_and_no_requests_is_refused(paged):
+    for kw in (dict(), dict(base=None, stride=2)):
+        assert attend_args(paged, bs=0, **kw) == B.EINVAL
