@@ -81,21 +81,27 @@ __device__ __forceinline__ int wave_id() {
 // Direct loads of 16 bytes a lane into 1 KiB of LDS.  Written out because the
 // compiler, which cannot tell the two buffers of a tile apart, lets every LDS
 // read wait for all such loads; `loads_done` waits for them where the tile is
-// needed, and it and the barriers keep the LDS reads on their side.  The loads
-// have no register to write, so nothing of the compiler's can be overtaken.
+// needed.  The loads have no register to write, so nothing of the compiler's can
+// be overtaken, and are memory to it, so LDS reads stay on their side of each.
+// m0 is not named among what they write: the compiler keeps nothing of its own
+// there (a register it has reserved, and refuses in that list), it sets it right
+// before an instruction that needs it.  No other instruction here does, which
+// tests/test_rows_code.py looks for in the machine code.
 __device__ __forceinline__ uint32_t lds_at(lds_u8 *p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
 }
 __device__ __forceinline__ void load_to_lds(const uint8_t *from, lds_u8 *to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
-               : "s"(lds_at(to)), "v"(from));
+               : "s"(lds_at(to)), "v"(from)
+               : "memory");
 }
 // Four bytes a lane, 256 bytes in all.
 __device__ __forceinline__ void load4_to_lds(const int32_t *from, lds_u8 *to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :
-               : "s"(lds_at(to)), "v"(from));
+               : "s"(lds_at(to)), "v"(from)
+               : "memory");
 }
 // The lane's place is `lane16` ^ X bytes from base + off, which all lanes
 // share; the LDS place is `to` + TO.
@@ -110,7 +116,7 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *base, uint64_t off, u
                : "s"(lds_at(to)), "s"(static_cast<uint32_t>(b)), "s"(static_cast<uint32_t>(off)),
                  "s"(static_cast<uint32_t>(b >> 32)), "s"(static_cast<uint32_t>(off >> 32)),
                  "v"(lane16), "n"(TO), "n"(X)
-               : "s96", "s97", "scc");
+               : "s96", "s97", "scc", "memory");
 }
 // What the wave asked of LDS has arrived (and what it asked of the scalar
 // cache: as long as such a load may be under way the compiler cannot tell how
