@@ -28,9 +28,12 @@
 // Long ranges of keys are cut into parts, joined by their log-sums in a second
 // launch in the order of the work list.
 //
-// Scores, m, l and the sums are fp32; P is rounded to the row's type for the
-// second product (its errors, at most half a step each, average out; l sums
-// the unrounded ones).
+// Scores, m, l and the sums are fp32.  P is rounded to the row's type for the
+// second product, once, because the matrix instruction's operands have one type;
+// l sums the unrounded weights.  Results are then off by 2.3e-3 of their norm in
+// bf16 and 2.9e-4 in fp16 (normal keys and values), where their own rounding
+// alone makes 1.7e-3 and 2.1e-4: the rest would take a second operand for what P
+// loses, and with it twice the second product's instructions.
 #include <algorithm>
 #include <cmath>
 
@@ -492,9 +495,11 @@ struct Attend {
 
   // The m to weigh by, given the largest score of new keys: m stays until it is
   // passed by more than 8, so that the sums are rescaled now and then and not
-  // with every new maximum.  Weights then reach 2^8 (fp16: 2^14).
+  // with every new maximum.  Weights then reach 2^8 (fp16: 2^14).  m is a whole
+  // number, the next above the score: what is brought from one m to another is
+  // then multiplied by a power of two, which rounds nothing.
   static __device__ __forceinline__ float next_m(float m, float top) {
-    return top > m + 8.0f ? top : m;
+    return top > m + 8.0f ? __builtin_ceilf(top) : m;
   }
   static __device__ __forceinline__ float finite_m(float m) {
     return m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 0
@@ -921,7 +926,9 @@ struct Attend {
   // weights to the other through LDS, and both add all 64 keys to their half
   // of the values, their own keys first.  A pair ends every tile with one m;
   // where their keys move it apart, each brings its sums, and the weights it
-  // was handed, to the larger.
+  // was handed, to the larger: by a power of two, so a weight is still rounded
+  // once (fp16 weights below 2^-20 of the largest, whose last places are lost, a
+  // second time).
   template <bool SCAN>
   static __device__ __forceinline__ bool latent(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {

@@ -725,6 +725,40 @@ def test_a_plan_dropped_while_another_stream_reads_its_list(given):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("which,hq", [("64", 32), ("128", 64), ("latent", 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_weights_are_rounded_once(which, hq, dtype):
+    """One key alone has a value, and its scores are single products, exact in
+    fp32.  Its weight is then off by one rounding to the row's type and, with
+    the scaling of the score (below 2^5), the exponential, the sum and the
+    division, by 2^-18; the result is rounded once more.  The maxima of the two
+    halves of a tile lie apart by no whole power of two."""
+    f = fmt(which, dtype, 1)
+    n = 64
+    b = Batch(f, hq, [1] * 60, [n] * 60, stale=0.0)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    rand = lambda *shape: torch.rand(shape, generator=g, device="cuda")
+    b.q.zero_()
+    b.q[..., f.k_dim - 1] = (1 + rand(*b.q.shape[:2])).to(f.dtype)
+    for r, x in enumerate(b.rows):
+        x.zero_()
+        x[:, f.k_dim - 1] = -8
+        x[3, f.k_dim - 1] = 1 + 2 * rand(1).item()       # the largest, in the first half
+        x[40, f.k_dim - 1] = 0.5 * rand(1).item()        # the largest of the second
+        x[50, f.k_dim - 1] = -rand(1).item()
+        at = 0 if f.values_in_key else f.k_dim
+        x[50, at:at + f.v_dim - 64 * f.values_in_key] = (1 + rand(
+            f.v_dim - 64 * f.values_in_key)).to(f.dtype)
+        b.dense[r * n:(r + 1) * n] = x
+    out, lse = gpb.attend_dense(b.plan(), b.q, b.dense, b.k_bases, 1.0)
+    want, _, _, _ = b.want(0, 0, 1.0)
+    half = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[f.dtype]
+    off = (out.double() - want).abs() - (2 * half + half ** 2 + 2.0 ** -18) * want.abs()
+    worst = float((off / want.abs().clamp_min(1e-30)).max())
+    assert worst <= 0
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():
