@@ -759,6 +759,83 @@ def test_weights_are_rounded_once(which, hq, dtype):
     assert worst <= 0
 
 
+def put_rows(b):
+    """The batch's rows to the dense buffer and the pool again."""
+    base = b.k_bases.tolist()
+    for r, x in enumerate(b.rows):
+        b.dense[base[r]:base[r] + len(x)] = x
+        for i, p in enumerate(b.lists[r]):
+            part = x[i * b.page:(i + 1) * b.page]
+            b.pool[p * b.page:p * b.page + len(part)] = part
+
+
+def check_kinds(out, want):
+    """NaN where NaN is due, and each infinity where it is."""
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(kind(out.double()), kind(want)), kind.__name__
+
+
+@pytest.mark.parametrize("which", ["64", "128"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("q,kv,window,sinks,at", [
+    ([100], [230], 0, 0, [140, 229, 180]),       # wide items, results at once
+    ([20], [500], 40, 2, [1, 445, 470, 499]),    # values that left some windows
+    ([1, 3], [70, 40], 0, 0, [39, 38]),          # narrow items
+    ([2, 1], [2500, 3000], 0, 0, [7, 2499]),     # narrow items in parts
+    ([150, 2], [3000, 700], 0, 0, [9, 2900, 2999]),   # wide items in parts
+    ([150], [3000], 200, 3, [2, 2700, 2999]),
+])
+def test_odd_values_of_both_types(which, dtype, bad, q, kv, window, sinks, at):
+    """Each result has the infinities and NaN of the formula and no others, the
+    rows beside them their values."""
+    f = fmt(which, dtype, 1)
+    b = Batch(f, 4, q, kv)
+    for x in b.rows:
+        for n, i in enumerate(i for i in at if i < len(x)):
+            x[i, f.k_dim + 5 + 9 * n] = bad
+    put_rows(b)
+    out, _ = b.check(window, sinks)
+    want = b.want(window, sinks, 1.0 / math.sqrt(f.k_dim))[0]
+    assert not torch.isfinite(want).all()
+    check_kinds(out, want)
+
+
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 16), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 3)])
+def test_odd_values_behind_a_shared_prefix_in_half_precision(which, hkv, hq, window, sinks):
+    f = fmt(which, "fp16", hkv)
+    b = Batch(f, hq, [2, 40, 1, 3], [200, 290, 300, 260], groups=[(0, 4, 128)], stale=0.0)
+    at = 0 if f.values_in_key else hkv * f.k_dim     # a value
+    for r, n in ((0, 200), (1, 290), (3, 260)):
+        b.rows[r][n - 1, at] = float("inf")
+    if window:
+        for r in range(4):
+            b.rows[r][5, at] = float("nan")
+    put_rows(b)
+    b.check(window, sinks, dense=False)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q,kv", [(60, 200), (60, 3000), (3, 2000)])
+def test_odd_latent_rows_in_half_precision(bad, q, kv):
+    """Queries before the odd row keep their values, those that see it have none."""
+    f = fmt("latent", "fp16")
+    b = Batch(f, 4, [q], [kv])
+    at = kv - q // 2
+    b.rows[0][at, 7] = bad
+    put_rows(b)
+    out, lse = gpb.attend_dense(b.plan(), b.q, b.dense, b.k_bases, 0.05)
+    clean = b.rows[0].clone()
+    clean[at] = 0
+    k, v = split(f, clean)
+    pos = torch.arange(kv - q, kv, device="cuda")
+    want = attention(b.q[:q], k, v, pos, 0, 0, 0.05)
+    n = at - (kv - q)
+    check(out[:n], lse[:n], [w[:n] for w in want])
+    assert not torch.isfinite(out[n:, :, 7]).any()
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():
