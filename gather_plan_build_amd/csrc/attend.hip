@@ -199,9 +199,11 @@ struct Attend {
   static constexpr int G0 = R0 % 256 ? 8 : 16, G1 = R1 % 256 ? 8 : 16;
   typedef typename Vec<T>::x8 x8;
   typedef typename Vec<T>::x4 x4;
-  // P of fp16 is held times 2^6 (at most 2^6, l with it): weights down to
-  // 2^-31 of the largest keep a value, where fp16 alone ends at 2^-25
-  static constexpr float SHIFT = sizeof(T) == 2 && __is_same(T, _Float16) ? 6.0f : 0.0f;
+  // P is held times 2^SHIFT, l with it.  fp16: weights down to 2^-31 of the
+  // largest keep a value, where fp16 alone ends at 2^-25.  bf16: an m that stays
+  // (see next_m) lets weights grow by 2^8; so held they are at most 1, and sums
+  // of the largest values do not pass fp32 before the result does.
+  static constexpr float SHIFT = __is_same(T, _Float16) ? 6.0f : -8.0f;
 
   // Where an item's keys are: key x is `offset` bytes from src, found through
   // its page's number (paged).  A base that leads outside the rows, or outside
@@ -495,7 +497,7 @@ struct Attend {
 
   // The m to weigh by, given the largest score of new keys: m stays until it is
   // passed by more than 8, so that the sums are rescaled now and then and not
-  // with every new maximum.  Weights then reach 2^8 (fp16: 2^14).  m is a whole
+  // with every new maximum.  Weights then reach 1 (fp16: 2^14).  m is a whole
   // number, the next above the score: what is brought from one m to another is
   // then multiplied by a power of two, which rounds nothing.
   static __device__ __forceinline__ float next_m(float m, float top) {

@@ -836,6 +836,29 @@ def test_odd_latent_rows_in_half_precision(bad, q, kv):
     assert not torch.isfinite(out[n:, :, 7]).any()
 
 
+@pytest.mark.parametrize("which,hq,nq", [("64", 2, 1), ("64", 4, 20), ("128", 2, 1), ("128", 4, 20),
+                                         ("latent", 2, 1)])
+def test_large_values_and_a_maximum_that_grows(which, hq, nq):
+    """Scores grow by 5 from tile to tile, less than what moves the running
+    maximum, and values are as large as weights of at most 1 allow: 60 of 5e36
+    make 3e38, below the largest float."""
+    f = fmt(which, "bf16", 1)
+    n = 160
+    b = Batch(f, hq, [nq], [n], stale=0.0)
+    x = b.rows[0]
+    x.zero_()
+    b.q.zero_()
+    b.q[..., f.k_dim - 1] = 1
+    x[n - 40 - nq:, f.k_dim - 1] = 5
+    at = 0 if f.values_in_key else f.k_dim
+    x[:, at:at + 64] = 5e36
+    put_rows(b)
+    out, lse = gpb.attend_dense(b.plan(), b.q, b.dense, b.k_bases, 1.0)
+    want = b.want(0, 0, 1.0)[0]
+    assert torch.isfinite(out).all()
+    assert ((out.double() - want).abs() <= 2.0 ** -6 * want.abs()).all()
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():
