@@ -187,7 +187,10 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
   // Cut long ranges of keys into parts of at most `most` keys, none shorter
   // than min_keys (one query of 737 keys, 32 heads over 8: 13.4 us with parts of
   // 256 keys, 13.7 of 128, 15.7 of 64).  A workgroup's start and end take as
-  // long as `start` keys.
+  // long as `start` keys: 2,723 queries over 3,481 to 8,153 keys, 32 heads over
+  // 8, 128 wide, 326 us so, 347 with none and 326 with twice as many; 48 queries
+  // behind 16,384 shared keys 58, 56 and 65.  A key counts the same in a wide, a
+  // narrow and a half-empty item, which it is not: their lists are a compromise.
   int64_t total = 0, uncut = 0, longest_block = 1;
   for (const Segment &g : p.segments)
     for (size_t k = 0; k < g.n_blocks; ++k) {
@@ -206,8 +209,9 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
   // first: the longest one where all run at once; else all of them spread
   // evenly, and the longest of those that had to wait, which starts when the
   // rest end.  A join costs a launch (160 keys' time of 33 ns: two requests of
-  // 292 and 357 latent rows, 16 heads, take 21.3 us whole and 22.9 us in
-  // parts), and sums written and read again take the whole GPU about a key's
+  // 292 and 357 latent rows, 16 heads, take 21.0 us whole and 23.2 us in
+  // parts; with half of it 4,200 queries of 128-wide heads take 281 us instead of
+  // 263, twice as much changes nothing measured), and sums written and read again take the whole GPU about a key's
   // time per 19,000 values.
   std::vector<std::pair<int64_t, int64_t>> lengths;  // keys, how many
   auto span = [&](int64_t most) {
@@ -235,6 +239,14 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
     }
     return std::max(longest, sum / slots + waits) + again;
   };
+  // Parts of an even share of the work, or of the length among some multiples of
+  // it, or uncut, that `span` finds best: 32 queries over 613 to 8,084 latent
+  // rows 42 us so, 51 with three lengths to choose from and 59 with the even
+  // share; 120 behind shared latent rows 148, 207 and 188; 2,500 queries of
+  // 64-wide heads 205, 205 and 222; nothing measured is more than 3% slower.
+  // With more than four blocks to a place the uncut ones fill the GPU evenly, and
+  // the lists are the same either way, but the search takes its time on the host:
+  // 44,600 queries over latent rows 0.7 ms without it, 2.5 with it.
   int64_t most = std::max(min_keys, ceil_div64(total, slots));
   if (uncut <= 4 * slots) {
     int64_t best = INT64_MAX;
