@@ -859,6 +859,52 @@ def test_large_values_and_a_maximum_that_grows(which, hq, nq):
     assert ((out.double() - want).abs() <= 2.0 ** -6 * want.abs()).all()
 
 
+@pytest.mark.parametrize("seed", range(60))
+def test_random_batches(seed):
+    """Groups, windows, first tokens, pages that end anywhere; the entries of
+    pages that no query sees, and the workspace, hold anything."""
+    rng = np.random.default_rng(seed)
+    which = str(rng.choice(["64", "128", "latent"]))
+    hkv = 1 if which == "latent" else int(rng.integers(1, 4))
+    f = fmt(which, str(rng.choice(["bf16", "fp16"])), hkv)
+    hq = hkv * int(rng.choice([1, 3, 4, 8, 16, 40]))
+    bs = int(rng.integers(1, 7))
+    q = rng.integers(0, rng.choice([3, 12, 90]), bs)
+    kv = rng.integers(0, rng.choice([80, 400, 2500]), bs)
+    page = int(rng.choice([1, 3, 8, 16, 50, 64]))
+    window = int(rng.choice([0, 0, 1, 12, 33, 200]))
+    sinks = int(rng.choice([0, 4, 17, 40]))
+    groups = []
+    if bs > 1 and rng.random() < 0.6:
+        n = int(rng.integers(2, bs + 1))
+        shared = page * int(rng.integers(1, 2 + rng.choice([40, 300, 1500]) // page))
+        kv[:n] = shared + q[:n] + rng.integers(0, rng.choice([2, 20, 600]), n)
+        groups = [(0, n, shared)]
+    b = Batch(f, hq, q.tolist(), kv.tolist(), page=page, groups=groups, seed=seed)
+    seen = np.zeros(b.table.shape, bool)           # pages that a query sees
+    for r in range(bs):
+        home = next((g for g in groups if g[0] < r < g[0] + g[1]), None)
+        for x in range(max(0, kv[r] - q[r]), kv[r]):
+            keys = np.arange(x + 1)
+            if window:
+                keys = keys[(x - keys < window) | (keys < sinks)]
+            pages = np.unique(keys // page)
+            seen[r, pages] = True
+            if home:
+                seen[home[0], pages[pages < home[2] // page]] = True
+    for first, n, shared in groups:                # read through the first request's list
+        seen[first + 1:first + n, :shared // page] = False
+    b.table[torch.from_numpy(~seen).cuda()] = int(rng.choice([-1, 10 ** 9]))
+    plan = b.plan(window, sinks)
+    ws = plan.workspace().fill_(255) if plan.workspace_bytes else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    scale = 1.0 / math.sqrt(f.k_dim)
+    out, lse = gpb.attend_paged(plan, b.q, b.pool, b.table, scale, workspace=ws, status=status)
+    assert int(status) == 0
+    if sum(q):
+        check(out, lse, b.want(window, sinks, scale))
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():
