@@ -802,7 +802,10 @@ class AttendPlan:
     number of requests, shared keys): consecutive requests that begin with the same
     whole pages, read once for all of them (paged attention only).  One plan serves
     every layer of the batch, on any stream, and may be dropped while calls with it
-    are under way; a captured graph needs it for as long as it is replayed."""
+    are under way; a captured graph needs it for as long as it is replayed, and
+    serves its lengths alone.  Making one takes 40 to 90 us for a decode batch, which
+    needs a new one every step, to 0.7 ms for 44,600 queries, and waits for the
+    current stream (the list is copied to the device from ordinary memory)."""
 
     def __init__(self, fmt, n_heads, q_lens, kv_lens, window=0, sinks=0, page_size=64,
                  groups=(), device="cuda"):

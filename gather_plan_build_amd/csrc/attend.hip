@@ -820,12 +820,12 @@ struct Attend {
   // serves two matrix instructions, and a tile's loads and addresses twice the
   // weights.
   //
-  // 128-wide heads, 2,723 queries over 3,481 to 8,153 keys, 32 heads over 8: 318
+  // 128-wide heads, 2,723 queries over 3,481 to 8,153 keys, 32 heads over 8: 320
   // us and a join of 9, 0.78 PFLOP/s; the matrix unit is busy 45% of the time that
   // a CU has work, the vector unit 54%, and CUs have none for a fifth of it (776
   // items on 512 places).  64-wide heads have half the products per weight:
-  // 17,337 queries, 64 heads over 8, window 1024: 440 us, 0.62 PFLOP/s, the
-  // vector unit busy 74% of the time with maxima, exponentials and sums.
+  // 17,337 queries, 64 heads over 8, window 1024: 438 us, 0.63 PFLOP/s, the
+  // vector unit busy 77% of the time with maxima, exponentials and sums.
   template <bool SCAN>
   static __device__ __forceinline__ bool wide(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {

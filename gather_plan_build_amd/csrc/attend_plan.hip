@@ -243,7 +243,7 @@ int plan_build(const gpb_row_format *f, const gpb_attend_shape *s, gpb_attend_pl
   // it, or uncut, that `span` finds best: 32 queries over 613 to 8,084 latent
   // rows 42 us so, 51 with three lengths to choose from and 59 with the even
   // share; 120 behind shared latent rows 148, 207 and 188; 2,500 queries of
-  // 64-wide heads 205, 205 and 222; nothing measured is more than 3% slower.
+  // 64-wide heads 205, 205 and 222; nothing measured is more than 4% slower.
   // With more than four blocks to a place the uncut ones fill the GPU evenly, and
   // the lists are the same either way, but the search takes its time on the host:
   // 44,600 queries over latent rows 0.7 ms without it, 2.5 with it.
