@@ -794,6 +794,11 @@ def row_append(fmt, k, v, pool, pool_locs, rotation=None, positions=None, rows=N
         _check(rc, "gpb_row_append")
 
 
+# Lists of dropped plans that streams made elsewhere may still read, each with the
+# events that say when they have been.
+_lists_in_use = []
+
+
 class AttendPlan:
     """The work list of an attention over one batch, on the device: request r has
     ``q_lens[r]`` queries, the last of its ``kv_lens[r]`` keys.  A query sees the
@@ -819,7 +824,8 @@ class AttendPlan:
                                  int(page_size), h_q.ctypes.data if h_q.size else None,
                                  h_kv.ctypes.data if h_q.size else None, h_g.size // 3,
                                  h_g.ctypes.data if h_g.size else None)
-        self.fmt, self.n_heads = fmt, int(n_heads)
+        _lists_in_use[:] = [x for x in _lists_in_use if any(not e.query() for e in x[1].values())]
+        self.fmt, self.n_heads, self.readers = fmt, int(n_heads), {}
         self.c = gpb_attend_plan()
         _check(lib.gpb_attend_plan_build(ctypes.byref(fmt.c), ctypes.byref(shape),
                                          ctypes.byref(self.c), None, 0),
@@ -838,10 +844,26 @@ class AttendPlan:
         self.list_ptr, self.ref = self.list.data_ptr(), ctypes.byref(self.c)
 
     def read_on(self, on):
-        """The list is read by kernels on the stream of ``on``: should the plan go
-        before they end, its memory is not handed out until they have."""
-        if on.raw != self.list_stream:
+        """Kernels on the stream of ``on`` read the list: should the plan go before
+        they end, its memory is not handed out until they have.  The allocator sees
+        to that on streams of torch.  It would do so by an event on the stream when
+        the list goes, and a stream made elsewhere may be gone by then, so there the
+        event is recorded now (not into a capture: a graph needs its plan anyway)."""
+        if on.raw == self.list_stream:
+            return
+        if on.raw == 0 or on.used.stream_id != on.raw:
             self.list.record_stream(on.used)
+            return
+        import torch
+        with torch.cuda.stream(on.used):
+            if not torch.cuda.is_current_stream_capturing():
+                self.readers.setdefault(on.raw, torch.cuda.Event()).record()
+
+    readers = {}   # events of streams made elsewhere, by handle
+
+    def __del__(self):
+        if self.readers and _lists_in_use is not None:   # (at exit it may be gone)
+            _lists_in_use.append((self.list, self.readers))
 
     def room(self, out, lse, own_lse, workspace):
         """Results and workspace of one call, where the caller has none."""
@@ -872,7 +894,6 @@ def _attend(plan, q, scale, out, lse, workspace, status, stream, call, what, **t
     q_ts, q_hs = _heads(q, T, plan.n_heads, fmt.k_dim, fmt.dtype, "q")
     on = _on(dev.index, stream)
     with on as st:
-        plan.read_on(on)
         if out is None or own_lse or (workspace is None and plan.workspace_bytes):
             if on.other is None:
                 out, lse, workspace = plan.room(out, lse, own_lse, workspace)
@@ -892,6 +913,7 @@ def _attend(plan, q, scale, out, lse, workspace, status, stream, call, what, **t
                            0 if lse is None else lse.data_ptr(), scale)
         rc = call(ctypes.byref(io), workspace.data_ptr() if n else None, n,
                   None if status is None else status.data_ptr(), st)
+        plan.read_on(on)
     if rc != OK:
         _check(rc, what)
     return out, lse

@@ -905,6 +905,33 @@ def test_random_batches(seed):
         check(out, lse, b.want(window, sinks, scale))
 
 
+def test_a_stream_that_goes_before_the_plan_does():
+    """A stream made elsewhere, and gone when the plan's list is handed back."""
+    import ctypes
+    runtime, = gpb.binding._hip_runtimes()        # the one in use
+    hip = ctypes.CDLL(runtime)
+    b = Batch(fmt("128", "bf16", 2), 8, [1, 40], [1500, 1800])
+    want = gpb.attend_paged(b.plan(), b.q, b.pool, b.table, 0.1)
+    torch.cuda.synchronize()
+    plan = b.plan()
+    handle = ctypes.c_void_p()
+    assert hip.hipStreamCreate(ctypes.byref(handle)) == 0
+    got = gpb.attend_paged(plan, b.q, b.pool, b.table, 0.1, out=torch.empty_like(want[0]),
+                           lse=torch.empty_like(want[1]), workspace=plan.workspace(),
+                           stream=handle.value)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert list(plan.readers) == [handle.value]
+    assert hip.hipStreamDestroy(handle) == 0
+    place, size = plan.list.data_ptr(), plan.list.numel()
+    del plan
+    others = [torch.full((size,), -1, dtype=torch.int32, device="cuda") for _ in range(8)]
+    assert place not in [x.data_ptr() for x in others]     # kept until a next plan is made
+    again = gpb.attend_paged(b.plan(), b.q, b.pool, b.table, 0.1)
+    assert torch.equal(again[0], want[0])
+    assert not gpb.binding._lists_in_use
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():

@@ -482,7 +482,7 @@ def test_a_plans_list_is_recorded_on_the_stream_that_reads_it(monkeypatch):
     monkeypatch.setattr(B, "_same_device", lambda *a, **kw: None)
     q, out = (torch.zeros(3, 4, 128, dtype=torch.bfloat16) for _ in range(2))
     for raw in (5, 77):
-        stream = SimpleNamespace(cuda_stream=raw)
+        stream = SimpleNamespace(cuda_stream=raw, stream_id=3)
         B._attend(plan, q, 0.1, out, None, None, None, stream, lambda *a: B.OK, "attend")
         assert seen == ([stream] if raw == 5 else []), raw
         seen.clear()
