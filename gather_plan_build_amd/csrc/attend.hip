@@ -190,7 +190,7 @@ struct Attend {
   // the tile in use and the one under way, or in the end a row's sums
   static constexpr int TILES_LDS =
       NARROW ? 4 * kNarrowTile * ROW : std::max(2 * kWideTile * ROW, kRows * DV * 4);
-  static constexpr int WAVE_XCHG = 2048 + 128;                 // latent: a wave's weights, maxima
+  static constexpr int WAVE_XCHG = 2048 + 2 * 128;             // latent: a wave's weights, m, maxima
   static constexpr int RING = TILES_LDS + (IN_KEY ? 4 * WAVE_XCHG : 8 * kRows);
   static constexpr int LDS = RING + 4096;
   static constexpr int NT = DV / 32 / (IN_KEY ? 2 : 1);        // output tiles of a wave
@@ -201,7 +201,7 @@ struct Attend {
   typedef typename Vec<T>::x4 x4;
   // P is held times 2^SHIFT, l with it.  fp16: weights down to 2^-31 of the
   // largest keep a value, where fp16 alone ends at 2^-25.  bf16: an m that stays
-  // (see next_m) lets weights grow by 2^8; so held they are at most 1, and sums
+  // (see take_top) lets weights grow by 2^8; so held they are at most 1, and sums
   // of the largest values do not pass fp32 before the result does.
   static constexpr float SHIFT = __is_same(T, _Float16) ? 6.0f : -8.0f;
 
@@ -495,14 +495,6 @@ struct Attend {
     return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   }
 
-  // The m to weigh by, given the largest score of new keys: m stays until it is
-  // passed by more than 8, so that the sums are rescaled now and then and not
-  // with every new maximum.  Weights then reach 1 (fp16: 2^14).  m is a whole
-  // number, the next above the score: what is brought from one m to another is
-  // then multiplied by a power of two, which rounds nothing.
-  static __device__ __forceinline__ float next_m(float m, float top) {
-    return top > m + 8.0f ? __builtin_ceilf(top) : m;
-  }
   static __device__ __forceinline__ float finite_m(float m) {
     return m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 0
   }
@@ -592,12 +584,12 @@ struct Attend {
       for (int i = 0; i < 16; ++i) o[t][i] *= f;
   }
 
-  // The weights of 32 * NB keys from their products, the first at position
-  // key0, as operands p; the sums so far brought to their m.
+  // The largest score of 32 * NB keys from their products, the first at position
+  // key0, those that the row does not see masked.
   template <int NB>
-  static __device__ __forceinline__ void weigh(const AttendArgs &a, const AttendItem &it,
-                                               f32x16 *s, int key0, bool whole, const Sight &see,
-                                               State &st, int half, x8 *p) {
+  static __device__ __forceinline__ float masked_top(const AttendArgs &a, const AttendItem &it,
+                                                     f32x16 *s, int key0, bool whole,
+                                                     const Sight &see, int half) {
     if (!whole) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) mask(a, it, see, key0 + 32 * b, half, s[b]);
@@ -605,13 +597,32 @@ struct Attend {
     float top = largest(s[0]);
     if constexpr (NB == 2) top = fmaxf(top, largest(s[1]));
     top *= a.c;
-    const float m = next_m(st.m, fmaxf(top, other_half(top, half)));
-    if (__any(m > st.m)) {
+    return fmaxf(top, other_half(top, half));
+  }
+  // The m to weigh by, given the largest score of new keys, and the sums so far
+  // brought to it: m stays until it is passed by more than 8, so that the sums are
+  // rescaled now and then and not with every new maximum.  Weights then reach 1
+  // (fp16: 2^14).  m grows to the new maximum, whose weight then is a power of two
+  // (a row of one key has its value exactly), or by whole steps: weights rounded
+  // for one m are brought to another by a power of two, which rounds nothing.
+  static __device__ __forceinline__ void take_top(State &st, float top, bool by_steps) {
+    const bool more = top > st.m + 8.0f;
+    if (__any(more)) {
+      const float from = finite_m(st.m);
+      float m = by_steps ? from + __builtin_ceilf(top - from) : top;
+      m = more ? m : st.m;
       rescale<NT>(st.o, &st.l, __builtin_amdgcn_exp2f(st.m - finite_m(m)));
       st.m = m;
     }
+  }
+  // The weights of the keys, as operands p; the sums so far brought to their m.
+  template <int NB>
+  static __device__ __forceinline__ void weigh(const AttendArgs &a, const AttendItem &it,
+                                               f32x16 *s, int key0, bool whole, const Sight &see,
+                                               State &st, int half, x8 *p) {
+    take_top(st, masked_top<NB>(a, it, s, key0, whole, see, half), false);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) st.l += weights(s[b], a.c, m, p + 2 * b);
+    for (int b = 0; b < NB; ++b) st.l += weights(s[b], a.c, st.m, p + 2 * b);
   }
 
   static __device__ __forceinline__ bool whole_tile(const AttendArgs &a, const AttendItem &it,
@@ -926,11 +937,14 @@ struct Attend {
   // row are 512 values, too many registers beside its 576 of query for one
   // wave, so of a tile's 64 keys each wave of a pair scores 32, hands its
   // weights to the other through LDS, and both add all 64 keys to their half
-  // of the values, their own keys first.  A pair ends every tile with one m;
-  // where their keys move it apart, each brings its sums, and the weights it
-  // was handed, to the larger: by a power of two, so a weight is still rounded
-  // once (fp16 weights below 2^-20 of the largest, whose last places are lost, a
-  // second time).
+  // of the values, their own keys first.  A pair ends every tile with one m.  In
+  // an item's first tile and in those that some row sees in part, where rows see
+  // their first keys, the two exchange their maxima first and take the same m; in
+  // the others, where the exchange would be a wait, m grows by whole steps, and
+  // where it grows apart each wave brings its sums, and the weights it was handed,
+  // to the larger: by a power of two, so a weight is still rounded once (fp16
+  // weights below 2^-20 of the largest, whose last places are lost, a second
+  // time).
   template <bool SCAN>
   static __device__ __forceinline__ bool latent(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
@@ -984,6 +998,7 @@ struct Attend {
         lds_u8 *now = lds + (v & 1) * BUF;
         const int key0 = first_key(it, v, kWideTile);
         const bool whole = whole_tile(a, it, key0, kWideTile);
+        const bool agree = v == 0 || !whole;
         const bool odd =
             SCAN && !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
@@ -991,13 +1006,21 @@ struct Attend {
         rows.ask(v + 2, v + 2);
         if (odd || idle) {
           load.all();
+          if (!odd && agree) __syncthreads();
           if (!odd) __syncthreads();
           continue;
         }
         x8 p[2];
         f32x16 s;
         products<kWideTile, 0, 3>(q, now, 32 * part, w, load, &s);
-        weigh<1>(a, it, &s, key0 + 32 * part, whole, see, st, half, p);
+        float top = masked_top<1>(a, it, &s, key0 + 32 * part, whole, see, half);
+        if (agree) {
+          if (half == 0) ((lds_float *)(mine + 2048 + 128))[lane] = top;
+          __syncthreads();
+          top = fmaxf(top, ((const lds_float *)(theirs + 2048 + 128))[lane & 31]);
+        }
+        take_top(st, top, !agree);
+        st.l += weights(s, a.c, st.m, p);
         const float m = st.m;
         ((lds8 *)mine)[lane] = p[0];
         ((lds8 *)mine)[64 + lane] = p[1];

@@ -932,6 +932,21 @@ def test_a_stream_that_goes_before_the_plan_does():
     assert not gpb.binding._lists_in_use
 
 
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 8), ("128", 1, 4), ("latent", 1, 16)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("q,kv", [([1], [1]), ([1, 1], [70, 300]), ([200, 40], [200, 1000])])
+def test_a_row_that_sees_one_key_has_its_value(which, hkv, hq, dtype, q, kv):
+    """Its weight is the whole sum, and both are a power of two."""
+    f = fmt(which, dtype, hkv)
+    b = Batch(f, hq, q, kv)
+    out, lse = gpb.attend_paged(b.plan(window=1), b.q, b.pool, b.table, 0.1)
+    at = 0
+    for r, (n, m) in enumerate(zip(q, kv)):
+        _, v = split(f, b.rows[r][m - n:])
+        assert torch.equal(out[at:at + n], v.repeat_interleave(hq // v.shape[1], 1))
+        at += n
+
+
 # ------------------------------------------------------------------ together
 
 def test_append_compose_attend_and_decode():
