@@ -836,7 +836,7 @@ struct Attend {
   // a CU has work, the vector unit 54%, and CUs have none for a fifth of it (776
   // items on 512 places).  64-wide heads have half the products per weight:
   // 17,337 queries, 64 heads over 8, window 1024: 438 us, 0.63 PFLOP/s, the
-  // vector unit busy 77% of the time with maxima, exponentials and sums.
+  // vector unit busy 76% of the time with maxima, exponentials and sums.
   template <bool SCAN>
   static __device__ __forceinline__ bool wide(const AttendArgs &a, const AttendItem &it,
                                               lds_u8 *lds) {
