@@ -191,7 +191,7 @@ def _held(case, x):
     share, power = torch.frexp(x.abs().amax(-1))
     # amax = share 2^power; the least e with amax <= 448 2^e, 448 being 0.875 2^9
     e = power - torch.where(share <= 0.875, 9, 8)
-    e = e.clamp(LEAST[name], MOST[name])
+    e = torch.where(share > 0, e, LEAST[name]).clamp(LEAST[name], MOST[name])
     codes = torch.ldexp(x, -e[..., None]).to(torch.float8_e4m3fn)
     return codes, (e + 127).to(torch.uint8)
 
