@@ -15,5 +15,5 @@ from .binding import (BatchMeta, GpbError, Plan, Sources, compose_gather,  # noq
                       strerror, LIB_PATH, PLAN_FIELDS, STATUS_BAD_DESCRIPTOR,
                       STATUS_BAD_STAGING_ROW, STATUS_BAD_PLAN_INPUT,
                       STATUS_LAYER_MISMATCH, RowFormat, Rotation, row_append,
-                      AttendPlan, attend_dense, attend_paged)
+                      rows_read, AttendPlan, attend_dense, attend_paged)
 from .runner import ComposeRunner, layer_groups, layer_groups_two_launch  # noqa: F401

@@ -79,7 +79,7 @@ class gpb_layer_group(ctypes.Structure):
 
 
 MAX_AXES = 4
-BF16, FP16 = 1, 2
+BF16, FP16, HELD_E4M3 = 1, 2, 16
 
 
 class gpb_row_format(ctypes.Structure):
@@ -191,6 +191,9 @@ def _load(path):
                                              vp, vp]
     lib.gpb_row_append.argtypes = [ctypes.POINTER(gpb_row_format), ctypes.POINTER(gpb_append),
                                    vp, vp]
+    lib.gpb_rows_read.argtypes = [ctypes.POINTER(gpb_row_format), vp, i64, vp, i32, vp, i32, vp,
+                                  vp]
+    lib.gpb_rows_read.restype = i32
     lib.gpb_attend_plan_build.argtypes = [ctypes.POINTER(gpb_row_format),
                                           ctypes.POINTER(gpb_attend_shape),
                                           ctypes.POINTER(gpb_attend_plan), vp, i64]
@@ -216,7 +219,7 @@ EXPORTS = ("gpb_plan_sizes", "gpb_plan_build", "gpb_plan_build_clear",
            "gpb_compose_consume_fill", "gpb_compose_layer_ahead_fill",
            "gpb_current_row_fill", "gpb_current_row_scatter_groups",
            "gpb_compose_gather_groups", "gpb_compose_layer_groups", "gpb_row_append",
-           "gpb_attend_plan_build", "gpb_attend_dense", "gpb_attend_paged", "gpb_strerror")
+           "gpb_rows_read", "gpb_attend_plan_build", "gpb_attend_dense", "gpb_attend_paged", "gpb_strerror")
 
 lib = _load(LIB_PATH)
 
@@ -615,9 +618,15 @@ class RowFormat:
     """What a token row holds: ``n_kv_heads`` key heads of ``k_dim`` values, then
     as many value heads of ``v_dim``; with ``values_in_key`` one key head whose
     first ``v_dim`` values are the value (a latent row).  ``dtype`` is "bf16" or
-    "fp16" (or the torch dtype), ``row_bytes`` the distance between rows."""
+    "fp16" (or the torch dtype), ``row_bytes`` the distance between rows.  With
+    ``held="e4m3"`` a row holds a byte for a value and a scale for a head (of a
+    latent row, the value; the rest of its key stays in 16 bits): half the memory,
+    and values off by up to 1/16.  Keys, values and queries are given, and results
+    come, in ``dtype``; the rows' tensors are of any type, uint8 [rows, row_bytes]
+    say."""
 
-    def __init__(self, dtype, n_kv_heads, k_dim, v_dim, values_in_key=False, row_bytes=None):
+    def __init__(self, dtype, n_kv_heads, k_dim, v_dim, values_in_key=False, row_bytes=None,
+                 held=None):
         import torch
         codes = {"bf16": BF16, "fp16": FP16, torch.bfloat16: BF16, torch.float16: FP16}
         if dtype not in codes:
@@ -625,10 +634,20 @@ class RowFormat:
         self.dtype = torch.bfloat16 if codes[dtype] == BF16 else torch.float16
         self.n_kv_heads, self.k_dim, self.v_dim = int(n_kv_heads), int(k_dim), int(v_dim)
         self.values_in_key = bool(values_in_key)
-        payload = 2 * self.n_kv_heads * (self.k_dim + (0 if values_in_key else self.v_dim))
-        self.row_bytes = payload if row_bytes is None else int(row_bytes)
-        self.c = gpb_row_format(codes[dtype], self.n_kv_heads, self.k_dim, self.v_dim,
-                                int(self.values_in_key), self.row_bytes)
+        if held not in (None, "e4m3"):
+            raise ValueError("rows are held in their type (None) or in e4m3, not in %r" % (held,))
+        self.held = held
+        # values of a row, and bytes of the row without padding
+        self.values = self.n_kv_heads * (self.k_dim + (0 if values_in_key else self.v_dim))
+        if held is None:
+            payload = 2 * self.values
+        elif self.values_in_key:
+            payload = self.v_dim + 2 * (self.k_dim - self.v_dim) + 1
+        else:
+            payload = self.values + 2 * self.n_kv_heads
+        self.row_bytes = (payload + 15) // 16 * 16 if row_bytes is None else int(row_bytes)
+        self.c = gpb_row_format(codes[dtype] | (HELD_E4M3 if held else 0), self.n_kv_heads,
+                                self.k_dim, self.v_dim, int(self.values_in_key), self.row_bytes)
         self.ref = ctypes.byref(self.c)
 
 
@@ -734,7 +753,8 @@ def row_append(fmt, k, v, pool, pool_locs, rotation=None, positions=None, rows=N
     and store row t at pool row ``pool_locs[t]`` (int32 [T]; -1 stores none) and, with
     ``rows``, at row t there.  ``pool`` may be None (then pool_locs too).  Queries
     ``q`` [T, heads, k_dim] are rotated into ``q_out`` (``q`` itself by default).
-    One launch.  T is the length of ``pool_locs`` (of ``k`` without a pool)."""
+    A held format quantises the rows as it writes them.  One launch.  T is the length
+    of ``pool_locs`` (of ``k`` without a pool)."""
     T = k.shape[0] if pool_locs is None else pool_locs.numel()
     dev = _device_index(k, "k")
     if q is not None and q_out is None:
@@ -792,6 +812,40 @@ def row_append(fmt, k, v, pool, pool_locs, rotation=None, positions=None, rows=N
                                 None if status is None else status.data_ptr(), st)
     if rc != OK:
         _check(rc, "gpb_row_append")
+
+
+def rows_read(fmt, rows, locs=None, n_rows=None, out=None, status=None, stream=None):
+    """Rows held in 8 bits back as rows of ``fmt.dtype``: row i of ``out`` [n, values]
+    is what row ``locs[i]`` of ``rows`` (a pool, a dense buffer, packed rows) stands
+    for, a row of zeros where ``locs[i]`` is -1; without ``locs`` (int32) row i of
+    ``rows``, all of them or the first ``n_rows``.  Exact.  ``out``'s rows may lie
+    apart; without ``out`` one is allocated.  One launch.  Returns ``out``."""
+    import torch
+    if fmt.held is None:
+        raise ValueError("rows of 16 bits a value need no reading back")
+    dev = _device_index(rows, "rows")
+    _same_device(dev, locs=locs, out=out, status=status)
+    n_src = _rows_of(rows, fmt.row_bytes, "rows")
+    n = (n_src if locs is None else locs.numel()) if n_rows is None else int(n_rows)
+    if n < 0 or (locs is None and n > n_src):
+        raise ValueError("%d rows of %d" % (n, n_src))
+    locs_ptr = None if locs is None else _int32(locs, n, "locs")
+    on = _on(dev, stream)
+    with on as st:
+        if out is None:
+            with torch.cuda.stream(on.used):   # it belongs to the stream the kernel runs on
+                out = torch.empty(n, fmt.values, dtype=fmt.dtype, device=rows.device)
+        if out.dim() != 2 or out.dtype != fmt.dtype or out.shape[0] < n or \
+                out.shape[1] != fmt.values or out.stride(1) != 1:
+            raise ValueError("out: need %s [>= %d, %d] with its last dimension contiguous, got "
+                             "%s %s, strides %s" % (fmt.dtype, n, fmt.values, out.dtype,
+                                                    tuple(out.shape), out.stride()))
+        apart = 2 * (out.stride(0) if out.shape[0] > 1 else fmt.values)
+        rc = lib.gpb_rows_read(fmt.ref, rows.data_ptr(), n_src, locs_ptr, n, out.data_ptr(), apart,
+                               None if status is None else status.data_ptr(), st)
+    if rc != OK:
+        _check(rc, "gpb_rows_read")
+    return out
 
 
 # Lists of dropped plans that streams made elsewhere may still read, each with the

@@ -18,66 +18,16 @@
 // token-packed: 316 us for 1.80 GB, 5.7 TB/s, where large copies reach 4.9 to 6.7;
 // 4,099 tokens of 28 query and 4 + 4 other heads of 128: 15.7 us for 75.6 MB (4.8
 // TB/s); 8 tokens: 4 us, the launch and two trips to HBM.
-#include "row_format.h"
+#include "append.h"
 
 namespace gpb {
 namespace {
-
-constexpr int kMaxPairs = 256;
-
-struct AppendArgs {
-  const uint16_t *k, *v, *q;
-  uint16_t *q_out;
-  uint8_t *pool, *rows;
-  const int32_t *locs, *positions;
-  const float *inv_freq;
-  int64_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs, qo_ts, qo_hs, positions_stride;
-  int64_t n_pool_rows;
-  int32_t row_bytes, hkv, hq, kd, vd, has_v;
-  int32_t rot_start, pairs, interleaved;
-  int32_t axis_end[GPB_MAX_AXES];
-  int32_t head_units;   // units of one key or query head
-  int32_t pair_units;   // of them, units of two chunks (halves apart)
-  int32_t *status;
-};
-
-template <typename T>
-__device__ __forceinline__ f32x8 widen(u32x4 v) {
-  return __builtin_convertvector(__builtin_bit_cast(typename Vec<T>::x8, v), f32x8);
-}
-template <typename T>
-__device__ __forceinline__ u32x4 narrow(f32x8 v) {
-  return __builtin_bit_cast(u32x4, __builtin_convertvector(v, typename Vec<T>::x8));
-}
-
-// Both past the caches: nothing is touched twice here, and rows that fill whole
-// lines need not be fetched first.  44,600 latent rows: 316 us so, 333 with plain
-// stores, 328 with plain loads and stores; 4,099 tokens of 36 heads: 14.8, 17.0
-// and 14.5, which plain ones win by 2%: one form, the large case's.
-__device__ __forceinline__ u32x4 load16(const uint16_t *p) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-}
-__device__ __forceinline__ void store16(uint8_t *p, u32x4 v) {
-  __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
-}
 
 template <typename T>
 __global__ __launch_bounds__(kBlock) void k_row_append(AppendArgs a) {
   __shared__ __attribute__((aligned(16))) float s_cos[kMaxPairs], s_sin[kMaxPairs];
   const int64_t t = blockIdx.x;
-  for (int i = threadIdx.x; i < a.pairs; i += kBlock) {
-    int axis = 0;
-#pragma unroll
-    for (int x = 0; x < GPB_MAX_AXES - 1; ++x) axis += i >= a.axis_end[x];
-    const double pos = a.positions[axis * a.positions_stride + t];
-    double turns = pos * (static_cast<double>(a.inv_freq[i]) * 0.15915494309189533577);
-    turns -= __builtin_rint(turns);
-    float sn, cs;
-    sincospif(static_cast<float>(2.0 * turns), &sn, &cs);
-    s_cos[i] = cs;
-    s_sin[i] = sn;
-  }
-  __syncthreads();
+  find_turns(a, t, s_cos, s_sin);
   const int64_t loc = a.locs ? a.locs[t] : -1;
   const bool stored = loc >= 0 && loc < a.n_pool_rows;
   if (a.locs && !stored && loc != -1 && threadIdx.x == 0 && a.status)
@@ -102,41 +52,9 @@ __global__ __launch_bounds__(kBlock) void k_row_append(AppendArgs a) {
     const int x = key ? u : u - n_k;
     const int h = x / a.head_units, j = x - h * a.head_units;
     const uint16_t *src = key ? a.k + t * a.k_ts + h * a.k_hs : a.q + t * a.q_ts + h * a.q_hs;
-    // unit j of a head: two chunks of pairs whose halves lie apart, or one
-    // chunk (pairs side by side, or not rotated)
-    int e0, e1 = -1;
-    if (j < a.pair_units) {
-      e0 = a.rot_start + 8 * j;
-      e1 = e0 + a.pairs;
-    } else {
-      e0 = 8 * (j - a.pair_units);
-      if (a.pair_units && e0 >= a.rot_start) e0 += 2 * a.pairs;
-    }
-    u32x4 lo = load16(src + e0), hi = {};
-    if (e1 >= 0) {
-      hi = load16(src + e1);
-      const f32x8 p = widen<T>(lo), q = widen<T>(hi);
-      f32x8 y0, y1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float cs = s_cos[8 * j + i], sn = s_sin[8 * j + i];
-        y0[i] = p[i] * cs - q[i] * sn;
-        y1[i] = q[i] * cs + p[i] * sn;
-      }
-      lo = narrow<T>(y0);
-      hi = narrow<T>(y1);
-    } else if (a.interleaved && e0 >= a.rot_start && e0 < a.rot_start + 2 * a.pairs) {
-      const f32x8 p = widen<T>(lo);
-      const int i0 = (e0 - a.rot_start) / 2;
-      f32x8 y;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float cs = s_cos[i0 + i], sn = s_sin[i0 + i];
-        y[2 * i] = p[2 * i] * cs - p[2 * i + 1] * sn;
-        y[2 * i + 1] = p[2 * i + 1] * cs + p[2 * i] * sn;
-      }
-      lo = narrow<T>(y);
-    }
+    int e0, e1;
+    u32x4 lo, hi;
+    rotate_unit<T>(a, src, j, s_cos, s_sin, &e0, &e1, &lo, &hi);
     if (key) {
       const int64_t off = 2ll * (h * a.kd + e0), off1 = 2ll * (h * a.kd + e1);
       if (to_pool) {
@@ -227,6 +145,7 @@ int row_append(const gpb_row_format *f, const gpb_append *p, int32_t *d_status, 
   a.pair_units = p->interleaved ? 0 : p->rot_dim / 16;
   a.head_units = f->k_dim / 8 - a.pair_units;
   a.status = d_status;
+  if (held(f)) return launch_append_held(*f, a, p->n_rows, as_stream(stream));
   const dim3 grid(static_cast<uint32_t>(p->n_rows));
   return f->dtype == GPB_BF16
              ? launch(k_row_append<__bf16>, grid, dim3(kBlock), as_stream(stream), a)

@@ -108,6 +108,10 @@ __host__ __device__ inline bool item_fits(const AttendArgs &a, const AttendItem 
          it.partial <= a.n_partial_rows - (it.partial < 0 ? 0 : it.n_rows);
 }
 
+// attend_held.hip: the launches of rows held in 8 bits, of queries of `type`.
+int launch_attend_held(int type, int which, const AttendArgs &a, bool narrow,
+                       hipStream_t stream);
+
 // Which keys of an item are read.
 struct AttendKeys {
   int lo, last;

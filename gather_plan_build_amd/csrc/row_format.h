@@ -19,19 +19,38 @@ struct Vec<_Float16> {
   typedef _Float16 x8 __attribute__((ext_vector_type(8)));
   typedef _Float16 x4 __attribute__((ext_vector_type(4)));
 };
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// A row's type, and whether its values are held in 8 bits.
+inline int type_of(const gpb_row_format *f) { return f->dtype & ~GPB_HELD_E4M3; }
+inline bool held(const gpb_row_format *f) { return (f->dtype & GPB_HELD_E4M3) != 0; }
+
+// Bytes of a held row: codes, values in the row's type, scales.
+struct HeldRow {
+  int64_t codes, plain, scales;
+  explicit HeldRow(const gpb_row_format &f)
+      : codes(static_cast<int64_t>(f.n_kv_heads) *
+              (f.values_in_key ? f.v_dim : f.k_dim + f.v_dim)),
+        plain(f.values_in_key ? 2ll * (f.k_dim - f.v_dim) : 0),
+        scales(f.values_in_key ? 1 : 2ll * f.n_kv_heads) {}
+};
+
 // Bytes of a row's keys and values, or 0 where the format is not valid.
 inline int64_t payload_bytes(const gpb_row_format *f) {
-  if (f->dtype != GPB_BF16 && f->dtype != GPB_FP16) return 0;
+  if (type_of(f) != GPB_BF16 && type_of(f) != GPB_FP16) return 0;
   if (f->n_kv_heads < 1 || f->n_kv_heads > 1024 || f->k_dim < 8 || f->k_dim > 1024 ||
       f->k_dim % 8 || f->v_dim < 8 || f->v_dim > 1024 || f->v_dim % 8)
     return 0;
   if (f->values_in_key != 0 && f->values_in_key != 1) return 0;
   if (f->values_in_key && (f->n_kv_heads != 1 || f->v_dim > f->k_dim)) return 0;
+  if (held(f)) {
+    const HeldRow row(*f);
+    return row.codes + row.plain + row.scales;
+  }
   return 2ll * f->n_kv_heads * (f->k_dim + (f->values_in_key ? 0 : f->v_dim));
 }
 

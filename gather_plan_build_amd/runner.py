@@ -281,6 +281,13 @@ class ComposeRunner:
                      rotation, positions, rows=self.curs[layer % len(self.curs)], q=q,
                      q_out=q_out, status=self.status, stream=stream)
 
+    def read(self, layer, fmt, out=None, stream=None):
+        """The layer's dense half, whose rows are held in 8 bits, as rows of
+        ``fmt.dtype`` [S * page_size, values]."""
+        self._check_format(fmt)
+        return B.rows_read(fmt, self.dense_of(layer), n_rows=self.S * self.ps, out=out,
+                           status=self.status, stream=stream)
+
     def attend_plan(self, fmt, n_heads, window=0, sinks=0):
         """The attention work list of the batch: every current token a query
         over its request's prefix and the current tokens up to itself."""

@@ -563,9 +563,12 @@ int gpb_compose_layer_noalloc(void *d_dense, const gpb_sources *pools, int32_t n
  * their positions and stores the rows in the paged pool (and token-packed, as
  * the compose takes its current rows); gpb_attend_dense is the attention over
  * the dense buffer the compose fills; gpb_attend_paged reads the pool itself
- * through page tables, as a decode step does. */
+ * through page tables, as a decode step does.  Rows may be held in 8 bits
+ * (GPB_HELD_E4M3): the same calls make and attend them, and gpb_rows_read
+ * gives them back in 16. */
 #define GPB_BF16 1
 #define GPB_FP16 2
+#define GPB_HELD_E4M3 16        /* added to one of them                        */
 
 /* What a token row holds: n_kv_heads key heads of k_dim values one after
  * another from the row's first byte, then n_kv_heads value heads of v_dim
@@ -573,9 +576,24 @@ int gpb_compose_layer_noalloc(void *d_dense, const gpb_sources *pools, int32_t n
  * whose first v_dim values are the value (a latent row).  row_bytes is the
  * distance between rows, a multiple of 16, at least the payload; bytes past
  * the payload belong to the caller and are neither read nor written.  k_dim
- * and v_dim are multiples of 8, at most 1024. */
+ * and v_dim are multiples of 8, at most 1024.
+ *
+ * With GPB_HELD_E4M3 the row holds a byte for a value: the codes of the key
+ * heads, then those of the value heads, then one scale byte for each key head
+ * and one for each value head.  With values_in_key it holds the codes of the
+ * value (the key's first v_dim values), then the key's other k_dim - v_dim
+ * values in the row's type, then one scale byte.  A code is an e4m3 number c (a
+ * sign, four bits of exponent with bias 7, three of fraction; no infinity, NaN
+ * 0x7f and 0xff) and stands for c * 2^(scale - 127).  The scale of a head's values x is
+ * the least power of two with which no |x| passes 448, but at least 2^-100
+ * (bf16) or 2^-15 (fp16), and the codes are x / scale rounded to nearest, ties
+ * to even; |x| beyond 240 * 2^120 or 240 * 2^8, infinity among them, is held as
+ * that, and NaN as NaN, which does not count for the scale.  A value so held
+ * stands for a number of the row's type, is off by at most 2^-4 of itself or
+ * 2^-10 scales, and is exactly what every reader takes it for; what bytes stand
+ * for whose scale no append makes is not specified. */
 typedef struct gpb_row_format {
-  int32_t dtype;                /* GPB_BF16 or GPB_FP16                        */
+  int32_t dtype;                /* GPB_BF16 or GPB_FP16, + GPB_HELD_E4M3       */
   int32_t n_kv_heads;           /* 1 .. 1024                                   */
   int32_t k_dim, v_dim;
   int32_t values_in_key;        /* 0 or 1                                      */
@@ -636,6 +654,22 @@ typedef struct gpb_append {
 int gpb_row_append(const gpb_row_format *format, const gpb_append *append,
                    int32_t *d_status, void *stream);
 
+/* Read rows held in 8 bits back in one launch: row i < n_rows of d_out (rows of
+ * out_row_bytes: the payload of the same heads without GPB_HELD_E4M3, and what
+ * the caller leaves behind it, which is not written) is what row d_locs[i] of
+ * d_rows stands for, or row i where d_locs is NULL (then n_rows <= n_src_rows).
+ * d_locs[i] = -1 gives a row of zeros (a padded entry of a batch); any other
+ * value outside [0, n_src_rows) does too, and GPB_STATUS_BAD_DESCRIPTOR is ORed
+ * into *d_status.  Rows may be named more than once.  d_rows is a pool, a dense
+ * buffer or packed rows, n_src_rows rows of format->row_bytes; d_out does not
+ * overlap it.  Errors: GPB_EINVAL (a format without GPB_HELD_E4M3,
+ * out_row_bytes short of the payload), GPB_EALIGN (out_row_bytes no multiple of
+ * 16, pointers to rows not 16-byte aligned), GPB_ERANGE (n_src_rows beyond
+ * INT32_MAX, rows past a launch), GPB_EHIP. */
+int gpb_rows_read(const gpb_row_format *format, const void *d_rows, int64_t n_src_rows,
+                  const int32_t *d_locs, int32_t n_rows, void *d_out, int32_t out_row_bytes,
+                  int32_t *d_status, void *stream);
+
 /* A batch to attend.  Request r has q_lens[r] queries, the last ones of its
  * kv_lens[r] keys: query j of r is at position kv_lens[r] - q_lens[r] + j and
  * sees key x if x <= its position and (window == 0, or position - x < window,
@@ -681,13 +715,14 @@ typedef struct gpb_attend_plan {
  * of host time for a decode batch, 2 ms for 44,600 queries).  Launch sizes come
  * from the plan: a captured graph serves the lengths it was captured with.
  * Formats attended: k_dim = v_dim = 64 or 128, or k_dim 576 with
- * v_dim 512 in the key.  Errors: GPB_EINVAL, GPB_EALIGN, GPB_ERANGE (sizes
+ * v_dim 512 in the key, of 16 bits a value or held in 8.  Errors: GPB_EINVAL, GPB_EALIGN, GPB_ERANGE (sizes
  * past int32, or a list_ints smaller than the list), GPB_ENOMEM. */
 int gpb_attend_plan_build(const gpb_row_format *format, const gpb_attend_shape *shape,
                           gpb_attend_plan *plan, int32_t *h_list, int64_t list_ints);
 
 /* Queries and results of one layer.  q: n_tokens tokens of n_heads heads of
- * k_dim values of the format's type; out: the same of v_dim; element strides,
+ * k_dim values of the format's type (16 bits, also where the rows are held in
+ * 8); out: the same of v_dim; element strides,
  * multiples of 8 (out: of 4), pointers 16-byte aligned (out: 8); the heads of
  * out have a place each (heads within tokens or tokens within heads).  Rows
  * behind the last query are neither read nor written.  lse (optional): float,
