@@ -77,8 +77,8 @@ int attend(const gpb_attend_plan *p, const int32_t *d_list, const gpb_attend_io 
   if (held(&p->format))
     return launch_attend_held(type_of(&p->format), which, a, narrow, as_stream(stream));
   return p->format.dtype == GPB_BF16
-             ? launch_format<__bf16, false>(which, a, narrow, as_stream(stream))
-             : launch_format<_Float16, false>(which, a, narrow, as_stream(stream));
+             ? launch_format<__bf16, Attend>(which, a, narrow, as_stream(stream))
+             : launch_format<_Float16, Attend>(which, a, narrow, as_stream(stream));
 }
 
 }  // namespace

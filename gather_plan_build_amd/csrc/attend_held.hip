@@ -1,12 +1,793 @@
 // attend_held.hip -- the attention kernels of rows held in 8 bits (gfx950).
+//
+// The kernels of attend_kernel.h with other ways for a row from HBM to the matrix
+// instruction, whose operands stay of 16 bits: a code times its scale is a number
+// of the row's type, so nothing is rounded on that way, and results are off by what
+// they would be off over the rows read back.
+//
+// Latent rows and narrow items keep the codes in LDS and turn eight of them into an
+// operand when it is read: four conversions, which fit into the 32 clocks of the
+// matrix instruction before (35.5 clocks for both).  LDS then holds and gives half
+// the bytes, by which the latent kernel of 16-bit rows is bound.  Wide items of
+// 64- and 128-wide heads are bound by the vector unit, and their four waves read
+// each key: there a wave turns its share of a tile on its way to LDS, once.
+//
+// A key's scale goes with the conversion, since a lane has one key of an operand.
+// A value operand holds eight keys to a lane, so there codes are taken at scale 1
+// and the scale goes to the key's weight.  bf16 has the exponents for that.  fp16
+// does not: its m is the maximum of s + log2 scale, the weight 2^(s + log2 scale -
+// m) at most 1 again, and l sums it over the scale.  Powers of two throughout: the
+// weight is rounded as it would be without.
 #include "attend_kernel.h"
+#include "held.h"
 
 namespace gpb {
+namespace {
+
+// The same load with OFF bytes added to the lane's place.  The instruction adds them
+// to the LDS place as well.
+template <int OFF>
+__device__ __forceinline__ void load_to_lds(const uint8_t *from, lds_u8 *to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
+               :
+               : "s"(lds_at(to) - OFF), "v"(from), "n"(OFF)
+               : "memory");
+}
+__device__ __forceinline__ void load4_to_lds(const uint8_t *from, lds_u8 *to) {
+  load4_to_lds(reinterpret_cast<const int32_t *>(from), to);
+}
+
+template <typename T, int DK, int DV, bool IN_KEY, bool NARROW>
+struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
+  typedef Attend<T, DK, DV, IN_KEY, NARROW> Plain;
+  typedef typename Plain::State State;
+  typedef typename Plain::Source Source;
+  typedef typename Plain::Sight Sight;
+  typedef typename Plain::NoLoader NoLoader;
+  typedef typename Plain::x8 x8;
+  using Plain::NT;
+  using Plain::R0;
+  using Plain::R1;
+  using Plain::ROW;
+  using Plain::RING;
+  using Plain::TILES_LDS;
+  using Plain::WAVE_XCHG;
+  using Plain::SHIFT;
+  using Plain::kRows;
+  static constexpr bool kHalf = __is_same(T, _Float16);
+  // Behind the plain kernel's LDS, a KiB a wave: scales as they come (two tiles of
+  // 256 bytes), and by key (three times 32 floats).  A latent's tiles leave room.
+  static constexpr int SCALES = IN_KEY ? 3 * kWideTile * 640 : Plain::LDS;
+  static constexpr int LDS = IN_KEY ? Plain::LDS : Plain::LDS + 4096;
+
+  // Bytes from a held row's start: of a key head, of a value head, of its scales.
+  static __device__ __forceinline__ int64_t key_at(const AttendItem &it) {
+    return IN_KEY ? 0 : static_cast<int64_t>(it.kv_head) * DK;
+  }
+  static __device__ __forceinline__ int64_t value_at(const AttendArgs &a, const AttendItem &it) {
+    return IN_KEY ? 0
+                  : static_cast<int64_t>(a.hkv) * DK + static_cast<int64_t>(it.kv_head) * DV;
+  }
+  static __device__ __forceinline__ int64_t key_scale_at(const AttendArgs &a,
+                                                         const AttendItem &it) {
+    return IN_KEY ? DV + 2 * (DK - DV)
+                  : static_cast<int64_t>(a.hkv) * (DK + DV) + it.kv_head;
+  }
+  static __device__ __forceinline__ int64_t value_scale_at(const AttendArgs &a,
+                                                           const AttendItem &it) {
+    return key_scale_at(a, it) + (IN_KEY ? 0 : a.hkv);
+  }
+
+  // For `careful`.  A tile is odd where its codes are (tiles of codes), or where the
+  // values are that went to LDS.
+  struct Values {
+    int64_t key_at, val_at, key_scale, val_scale;
+    const uint8_t *src;
+    bool codes;
+    __device__ __forceinline__ Values(const AttendArgs &a, const AttendItem &it,
+                                      const uint8_t *src)
+        : key_at(AttendHeld::key_at(it)), val_at(value_at(a, it)), key_scale(key_scale_at(a, it)),
+          val_scale(value_scale_at(a, it)), src(src), codes(IN_KEY || !it.wide) {}
+    static __device__ __forceinline__ T one(uint8_t code, uint8_t scale) {
+      return values8<T>(u32x2{code, 0}, scale_of(scale))[0];
+    }
+    __device__ __forceinline__ float key(int64_t off, int e) const {
+      const uint8_t *row = src + off;
+      if (IN_KEY && e >= DV)
+        return static_cast<float>(reinterpret_cast<const T *>(row + DV)[e - DV]);
+      return static_cast<float>(one(row[key_at + e], row[key_scale]));
+    }
+    __device__ __forceinline__ float value(int64_t off, int e) const {
+      return static_cast<float>(one(src[off + val_at + e], src[off + val_scale]));
+    }
+    __device__ __forceinline__ bool odd(int64_t off, int e) const {
+      const uint8_t code = src[off + val_at + e];
+      return codes ? (code & 127) == 127
+                   : Plain::not_finite(__builtin_bit_cast(
+                         uint16_t, one(code, src[off + val_scale])));
+    }
+  };
+
+  // ---- tiles of codes
+
+  // A tile of n held rows in LDS: blocks of n times 64 bytes of a row, 64 bytes a
+  // key, their four chunks moved by bits 2 and 3 of the row.  Sixteen rows at one
+  // chunk, the read of a key operand, then meet in no bank, nor do the rows 0 to 3
+  // and 8 to 11 (or the next four) at two chunks, that of a value operand.  Four
+  // lanes load a row, 64 bytes at a time, so all loads of a lane are of one row (or
+  // two), at constant offsets.
+  static constexpr int BLOCKS = IN_KEY ? (DV + 2 * (DK - DV)) / 64 : (DK + DV) / 64;
+  static constexpr int KEY_BLOCKS = IN_KEY ? BLOCKS : DK / 64;
+  static constexpr int VALUES_FROM = IN_KEY ? 0 : DK / 64;  // block of the first value
+  static constexpr int CODE_STEPS = (IN_KEY ? DV : DK) / 32;  // chunks of codes to a lane
+  static constexpr int KEY_STEPS = KEY_BLOCKS * 2;            // all its chunks of a key
+
+  // Where in a tile the lane reads: key chunk 2 D + half of row lane % 32, even and
+  // odd D; value tile t, even and odd t.
+  struct Spots {
+    uint32_t k[2], v[2];
+    __device__ __forceinline__ Spots(int lane) {
+      const int n = lane & 31, half = lane >> 5, pair = (lane & 15) >> 1;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        k[x] = n * 64 + ((2 * x + half) ^ ((n >> 2) & 3)) * 16;
+        // of 16 lanes, two read eight bytes each of one key; lane i gets value i
+        const int row = 4 * half + (pair & 3) + 8 * (pair >> 2);
+        v[x] = row * 64 + ((2 * x + ((lane >> 4) & 1)) ^ ((row >> 2) & 3)) * 16 + (lane & 1) * 8;
+      }
+    }
+  };
+
+  template <int TILE>
+  static __device__ __forceinline__ u32x4 key_chunk(const lds_u8 *tile, int row0, const Spots &w,
+                                                    int D) {
+    typedef __attribute__((address_space(3))) u32x4 lds16;
+    return *(const lds16 *)(tile + row0 * 64 + w.k[D & 1] + D / 2 * TILE * 64);
+  }
+  template <int TILE>
+  static __device__ __forceinline__ u32x2 value_codes(const lds_u8 *tile, const Spots &w, int key0,
+                                                      int t) {
+    typedef int v2i __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) v2i lds8;
+    return __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                   (lds8 *)(tile + w.v[t & 1] + (VALUES_FROM + t / 2) * TILE * 64 + key0 * 64)));
+  }
+  // Operand E of a lane's chunk D: eight codes of it, or eight values of 16 bits.
+  template <int D, int E>
+  static __device__ __forceinline__ x8 operand(u32x4 chunk, float scale) {
+    if constexpr (D >= CODE_STEPS) return __builtin_bit_cast(x8, chunk);
+    else return values8<T>(u32x2{chunk[2 * E], chunk[2 * E + 1]}, scale);
+  }
+  // The query operand that meets it (see load_queries): steps are two to a chunk of
+  // codes and one to a chunk of values.
+  static constexpr int step_of(int D) { return D < CODE_STEPS ? 2 * D : D + CODE_STEPS; }
+
+  // q.k of the 32 keys in rows row0 .. of a tile and the lane's query row.  Conversions
+  // and reads stand behind the product they run beside.
+  template <int TILE, typename L>
+  static __device__ __forceinline__ void products(const x8 *q, const lds_u8 *tile, int row0,
+                                                  const Spots &w, float scale, const L &next,
+                                                  f32x16 *s) {
+    constexpr int AHEAD = KEY_STEPS < 4 ? KEY_STEPS : 4;
+    u32x4 raw[AHEAD];
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) raw[d] = key_chunk<TILE>(tile, row0, w, d);
+    *s = f32x16{};
+    x8 k[2];
+    k[0] = operand<0, 0>(raw[0], scale);
+    k[1] = operand<0, 1>(raw[0], scale);
+    product_steps<TILE, 0, AHEAD>(q, tile, row0, w, scale, next, raw, k, s);
+  }
+  template <int TILE, int D, int AHEAD, typename L>
+  static __device__ __forceinline__ void product_steps(const x8 *q, const lds_u8 *tile, int row0,
+                                                       const Spots &w, float scale, const L &next,
+                                                       u32x4 *raw, x8 *k, f32x16 *s) {
+    if constexpr (D < KEY_STEPS) {
+      constexpr bool MORE = D + 1 < KEY_STEPS;
+      *s = mma<T>(k[0], q[step_of(D)], *s);
+      in_order();
+      if constexpr (MORE) k[0] = operand<D + 1, 0>(raw[(D + 1) % AHEAD], scale);
+      next.template issue<D>();
+      in_order();
+      if constexpr (D < CODE_STEPS) {
+        *s = mma<T>(k[1], q[step_of(D) + 1], *s);
+        in_order();
+      }
+      if constexpr (MORE && D + 1 < CODE_STEPS) k[1] = operand<D + 1, 1>(raw[(D + 1) % AHEAD], scale);
+      if constexpr (D + AHEAD < KEY_STEPS) raw[D % AHEAD] = key_chunk<TILE>(tile, row0, w, D + AHEAD);
+      in_order();
+      product_steps<TILE, D + 1, AHEAD>(q, tile, row0, w, scale, next, raw, k, s);
+    }
+  }
+
+  // Sums of N output tiles (values 32 t0 ..) += weights p of 16 NP keys, from row0 on.
+  template <int TILE, int NP, int N>
+  static __device__ __forceinline__ void add_values(const x8 *p, const lds_u8 *tile, int row0,
+                                                    const Spots &w, int t0, State *st) {
+    constexpr int AHEAD = NP * N < 6 ? NP * N : 6;
+    u32x2 raw[AHEAD];
+    const lds_u8 *at = tile + t0 / 2 * TILE * 64 + row0 * 64;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) raw[i] = value_codes<TILE>(at, w, i / N * 16, i % N);
+    value_steps<TILE, NP, N, 0, AHEAD>(p, at, w, st, raw, values8<T>(raw[0], 1.0f));
+  }
+  template <int TILE, int NP, int N, int I, int AHEAD>
+  static __device__ __forceinline__ void value_steps(const x8 *p, const lds_u8 *at,
+                                                     const Spots &w, State *st, u32x2 *raw,
+                                                     x8 now) {
+    if constexpr (I < NP * N) {
+      st->o[I % N] = mma<T>(now, p[I / N], st->o[I % N]);
+      in_order();
+      if constexpr (I + 1 < NP * N) now = values8<T>(raw[(I + 1) % AHEAD], 1.0f);
+      if constexpr (I + AHEAD < NP * N)
+        raw[I % AHEAD] = value_codes<TILE>(at, w, (I + AHEAD) / N * 16, (I + AHEAD) % N);
+      in_order();
+      value_steps<TILE, NP, N, I + 1, AHEAD>(p, at, w, st, raw, now);
+    }
+  }
+
+  // Whether these lanes' share of a tile's value codes holds a NaN.
+  template <int TILE>
+  static __device__ __forceinline__ bool odd_codes(const lds_u8 *tile, int id, int ids) {
+    typedef __attribute__((address_space(3))) u32x4 lds16;
+    const lds_u8 *v = tile + VALUES_FROM * TILE * 64;
+    bool odd = false;
+    for (int c = id; c < TILE * DV / 16; c += ids) {
+      const u32x4 x = *(const lds16 *)(v + c * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t y = (x[j] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;  // a byte of it 0: NaN
+        odd |= ((y - 0x01010101u) & ~y & 0x80808080u) != 0;
+      }
+    }
+    return odd;
+  }
+
+  // Scales of the values of a lane's 16 keys of 32, as weights take them: bf16 the
+  // scale; fp16 its log2 and its inverse.
+  struct ValueScales {
+    f32x16 a, b;
+  };
+  // Lane n % 32 has the scale byte of key n's values; `room` is 256 bytes of LDS.
+  static __device__ __forceinline__ void lay_scales(lds_u8 *room, int lane, uint32_t byte) {
+    typedef __attribute__((address_space(3))) float lds_float;
+    if (lane >= 32) return;
+    // (a byte of 255, which no append writes, must not make a weight of 0 NaN)
+    const int e = static_cast<int>(min(byte, 254u)) - 127;
+    if constexpr (kHalf) {
+      ((lds_float *)room)[lane] = static_cast<float>(e);
+      ((lds_float *)room)[32 + lane] = __builtin_amdgcn_ldexpf(1.0f, -e);
+    } else {
+      ((lds_float *)room)[lane] = __builtin_amdgcn_ldexpf(1.0f, e);
+    }
+  }
+  static __device__ __forceinline__ void take_scales(const lds_u8 *room, int half,
+                                                     ValueScales *x) {
+    typedef __attribute__((address_space(3))) f32x4 lds16;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const f32x4 u = *(const lds16 *)(room + (8 * y + 4 * half) * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x->a[4 * y + j] = u[j];
+      if constexpr (kHalf) {
+        const f32x4 z = *(const lds16 *)(room + 128 + (8 * y + 4 * half) * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x->b[4 * y + j] = z[j];
+      }
+    }
+  }
+  // The scores of 32 keys, masked, to units of log2 (fp16: with their scales); returns
+  // the largest.
+  static __device__ __forceinline__ float top_of(const AttendArgs &a, const AttendItem &it,
+                                                 f32x16 *s, int key0, bool whole,
+                                                 const Sight &see, int half,
+                                                 const ValueScales &scales) {
+    if (!whole) Plain::mask(a, it, see, key0, half, *s);
+    if constexpr (kHalf) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) (*s)[i] = __builtin_fmaf((*s)[i], a.c, scales.a[i]);
+    }
+    float top = Plain::largest(*s);
+    if constexpr (!kHalf) top *= a.c;
+    return fmaxf(top, other_half(top, half));
+  }
+  // As Attend::weights, of what top_of left.
+  static __device__ __forceinline__ float weights(const f32x16 &s, float c, float m,
+                                                  const ValueScales &scales, x8 *p) {
+    float sum[4] = {};
+    const float ref = Plain::finite_m(m) - SHIFT;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (kHalf) {
+        const float x = __builtin_amdgcn_exp2f(s[i] - ref);
+        sum[i % 4] = __builtin_fmaf(x, scales.b[i], sum[i % 4]);
+        p[i / 8][i % 8] = static_cast<T>(x);
+      } else {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ref));
+        sum[i % 4] += x;
+        p[i / 8][i % 8] = static_cast<T>(x * scales.a[i]);
+      }
+    }
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  }
+
+  // The rows of a wave's KEYS keys of tiles of TILE (see Attend::Rows).
+  template <int TILE, int KEYS>
+  struct Rows : Source {
+    const AttendItem &it;
+    lds_u8 *ring;
+    int first, lane;
+
+    __device__ __forceinline__ Rows(const AttendArgs &a, const AttendItem &it, lds_u8 *lds,
+                                    int wave, int lane)
+        : Source(a, it), it(it), ring(lds + RING + wave * 1024),
+          first(TILE == KEYS ? 0 : wave * KEYS), lane(lane) {}
+    __device__ __forceinline__ int key(int v, int i) const {
+      return v < it.n_tiles ? Plain::first_key(it, v, TILE) + first + i : this->lo;
+    }
+    __device__ __forceinline__ void ask(int v, int slot) const {
+      if (this->pages)
+        load4_to_lds(this->place(key(v, lane % KEYS)), ring + (slot & 3) * 256);
+    }
+    // Of key i of the wave's.
+    __device__ __forceinline__ uint64_t row(int v, int slot, int i) const {
+      typedef __attribute__((address_space(3))) int lds_int;
+      return this->offset(key(v, i),
+                          this->pages ? ((const lds_int *)(ring + (slot & 3) * 256))[i] : 0);
+    }
+  };
+
+  // ---- narrow items
+
+  // The loads of a wave's tile of 32 keys: rows lane / 4 and 16 + lane / 4, chunk
+  // lane % 4 of 64 bytes at a time; and the four bytes around a scale, of key
+  // lane % 32, the key's (lanes below 32) or the value's.
+  struct NarrowLoader {
+    static constexpr int N = 2 * BLOCKS + 1;
+    static __device__ __forceinline__ void all(const AttendArgs &a, const AttendItem &it,
+                                               const Source &from, uint64_t off, lds_u8 *tile,
+                                               lds_u8 *scales, int lane) {
+      const int64_t scale = lane < 32 ? key_scale_at(a, it) : value_scale_at(a, it);
+      gpb::load4_to_lds(from.src + off + (scale & ~3ll), scales);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int r = 16 * g + (lane >> 2);
+        const uint32_t lo = __shfl(static_cast<uint32_t>(off), r, 64);
+        const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), r, 64);
+        const uint8_t *row = from.src + (lo | static_cast<uint64_t>(hi) << 32) +
+                             ((lane & 3) ^ ((r >> 2) & 3)) * 16;
+        blocks<DK / 64>(row + key_at(it), tile + g * 1024);
+        blocks<DV / 64>(row + value_at(a, it), tile + DK / 64 * 2048 + g * 1024);
+      }
+    }
+    template <int NB, int J = 0>
+    static __device__ __forceinline__ void blocks(const uint8_t *from, lds_u8 *to) {
+      if constexpr (J < NB) {
+        gpb::load_to_lds<J * 64>(from, to + J * 2048);
+        blocks<NB, J + 1>(from, to);
+      }
+    }
+  };
+
+  // As Attend::narrow.  A wave has two tiles' room, so that the loads of the tile
+  // after next go out as soon as one has been read.  Page numbers are asked for two
+  // tiles before the loads that need them: the wait for the tile between has them.
+  template <bool SCAN>
+  static __device__ __forceinline__ bool narrow(const AttendArgs &a, const AttendItem &it,
+                                                lds_u8 *lds) {
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int row = lane & 31, half = lane >> 5;
+    constexpr int BUF = kNarrowTile * 64 * BLOCKS;
+    static_assert(8 * BUF <= TILES_LDS, "two tiles a wave");
+    lds_u8 *own = lds + wave * 2 * BUF, *scales = lds + SCALES + wave * 1024;
+    const Rows<kNarrowTile, kNarrowTile> rows(a, it, lds, wave, lane);
+    if (wave < it.n_tiles) {
+      rows.ask(wave, 0);
+      rows.ask(wave + 4, 1);
+    }
+    x8 q[DK / 16];
+    int pos;
+    load_queries(a, it, row, half, q, &pos);
+    const Spots w(lane);
+    const Sight see = Plain::sight(a, it, pos);
+    State st;
+    st.clear();
+    bool left = false;  // SCAN: a tile is left to `careful`
+    const auto load = [&](int v, int n) {
+      rows.ask(v + 8, n + 2);
+      NarrowLoader::all(a, it, rows, rows.row(v, n, lane & 31), own + (n & 1) * BUF,
+                        scales + (n & 1) * 256, lane);
+    };
+    if (wave < it.n_tiles) {
+      typedef __attribute__((address_space(3))) uint32_t lds_u32;
+      loads_done();
+      load(wave, 0);
+      if (wave + 4 < it.n_tiles) load(wave + 4, 1);
+      const int key_shift = static_cast<int>(key_scale_at(a, it) & 3) * 8;
+      const int value_shift = static_cast<int>(value_scale_at(a, it) & 3) * 8;
+      int n = 0;  // tiles of the wave so far
+      lds_reads_done();
+      loop_aligned();
+      for (int v = wave; v < it.n_tiles; v += 4, ++n) {
+        const lds_u8 *now = own + (n & 1) * BUF;
+        const int key0 = Plain::first_key(it, v, kNarrowTile);
+        const bool whole = Plain::whole_tile(a, it, key0, kNarrowTile);
+        if (v + 4 >= it.n_tiles) loads_done();
+        else if (rows.pages) loads_done<NarrowLoader::N + 1>();
+        else loads_done<NarrowLoader::N>();
+        if (SCAN && !whole && __any(odd_codes<kNarrowTile>(now, lane, 64))) {
+          left = true;
+        } else {
+          const lds_u8 *sc = scales + (n & 1) * 256;
+          const uint32_t ks = ((const lds_u32 *)sc)[row] >> key_shift & 255;
+          const uint32_t vs = ((const lds_u32 *)sc)[32 + row] >> value_shift & 255;
+          lay_scales(scales + 512, lane, vs);
+          f32x16 s;
+          products<kNarrowTile>(q, now, 0, w, scale_of(ks), NoLoader(), &s);
+          ValueScales by;
+          take_scales(scales + 512, half, &by);
+          Plain::take_top(st, top_of(a, it, &s, key0, whole, see, half, by), false);
+          x8 p[2];
+          st.l += weights(s, a.c, st.m, by, p);
+          add_values<kNarrowTile, 2, NT>(p, now, 0, w, 0, &st);
+        }
+        lds_reads_done();
+        if (v + 8 < it.n_tiles) load(v + 8, n + 2);
+      }
+    }
+    return Plain::template narrow_end<SCAN, Values>(a, it, lds, wave, lane, st, left);
+  }
+
+  // The lane's query row, in the order of its key chunks' codes: of 32 values, the
+  // first half of the lanes have the first 16.
+  static __device__ __forceinline__ void load_queries(const AttendArgs &a, const AttendItem &it,
+                                                      int row, int half, x8 *q, int *pos) {
+    const bool has = row < it.n_rows;
+    const int g = it.row0 + (has ? row : 0);
+    const int t = g / a.G, h = g - t * a.G + it.kv_head * a.G;
+    *pos = has ? a.list[a.positions_at + t] : -1;
+    const uint16_t *src = a.q + t * a.q_ts + h * a.q_hs + half * 16;
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d)
+      q[d] = has ? *reinterpret_cast<const x8 *>(src + d / 2 * 32 + d % 2 * 8) : x8{};
+    // (arrived before the tiles' loads start, as in Attend::load_queries)
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) asm volatile("" : "+v"(q[d]));
+    asm volatile("" : "+v"(*pos));
+  }
+
+  // ---- latent rows
+
+  // The loads of a wave's 16 keys of a tile: row lane / 4, chunk lane % 4 of 64 bytes
+  // at a time, then the four bytes from its scale on.
+  struct LatentLoader {
+    static constexpr int N = BLOCKS + 1;
+    const uint8_t *row;
+    lds_u8 *to, *scales;
+    int chunk;
+    __device__ __forceinline__ LatentLoader(const uint8_t *row, lds_u8 *tile, lds_u8 *scales,
+                                            int wave, int lane)
+        : row(row), to(tile + wave * 1024), scales(scales + wave * 256),
+          chunk(((lane & 3) ^ ((lane >> 4) & 3)) * 16) {}
+    template <int I>
+    __device__ __forceinline__ void issue() const {
+      if constexpr (I < BLOCKS) gpb::load_to_lds<I * 64>(row + chunk, to + I * kWideTile * 64);
+      else if constexpr (I == BLOCKS) gpb::load4_to_lds(row + DV + 2 * (DK - DV), scales);
+    }
+    template <int I = 0>
+    __device__ __forceinline__ void all() const {
+      if constexpr (I < N) {
+        issue<I>();
+        all<I + 1>();
+      }
+    }
+  };
+
+  // As Attend::latent, over tiles of codes.  Three of them fit, so a tile's loads go
+  // out two tiles ahead.
+  template <bool SCAN>
+  static __device__ __forceinline__ bool latent(const AttendArgs &a, const AttendItem &it,
+                                                lds_u8 *lds) {
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int part = wave & 1, half = lane >> 5;
+    const int row = (wave >> 1) * 32 + (lane & 31);
+    const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
+    const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
+    constexpr int BUF = kWideTile * 64 * BLOCKS;
+    static_assert(3 * BUF == SCALES && SCALES + 3072 + 1024 <= TILES_LDS, "room for scales");
+    lds_u8 *mine = lds + TILES_LDS + wave * WAVE_XCHG;
+    const lds_u8 *theirs = lds + TILES_LDS + (wave ^ 1) * WAVE_XCHG;
+    lds_u8 *by_key = lds + SCALES + 3072 + wave * 256;
+    typedef __attribute__((address_space(3))) x8 lds8;
+    typedef __attribute__((address_space(3))) float lds_float;
+    typedef __attribute__((address_space(3))) uint32_t lds_u32;
+    x8 q[DK / 16] = {};
+    const Spots w(lane);
+    const Sight see = Plain::sight(a, it, Plain::position(a, it, row));
+    State st;
+    st.clear();
+    bool left = false;  // SCAN: a tile is left to `careful`
+    const auto loader = [&](int v, int buf) {
+      return LatentLoader(rows.src + rows.row(v, v, lane >> 2), lds + buf * BUF,
+                          lds + SCALES + buf * 1024, wave, lane);
+    };
+    if (it.n_tiles > 0) {
+      typedef typename Plain::template Loader<kWideTile, 4> Queries;
+      rows.ask(0, 0);
+      rows.ask(1, 1);
+      {
+        // the queries come as a tile of 16-bit rows, behind the first tile
+        const int g = it.row0 + min(wave * 16 + (lane & 15), it.n_rows - 1);
+        const int t = g / a.G, h = g - t * a.G + it.kv_head * a.G;
+        Queries(reinterpret_cast<const uint8_t *>(a.q),
+                static_cast<uint64_t>(t * a.q_ts + h * a.q_hs) * 2, lds + BUF, wave, lane)
+            .all();
+      }
+      loads_done<Queries::N>();
+      rows.ask(2, 2);
+      loader(0, 0).all();
+      if (rows.pages) loads_done<LatentLoader::N + 1>();
+      else loads_done<LatentLoader::N>();
+      __syncthreads();
+      const int n = 32 * (wave >> 1) + (lane & 31);
+      static_assert(BUF + kWideTile * ROW <= TILES_LDS, "room for the queries");
+#pragma unroll
+      for (int d = 0; d < DK / 16; ++d) {
+        if (d < 2 * CODE_STEPS) {
+          const int c = d / 2 * 4 + half * 2 + d % 2;
+          q[d] = *(const lds8 *)(lds + BUF + n * R0 + place_of<R0>(n, c) * 16);
+        } else {
+          const int c = (d - 2 * CODE_STEPS) * 2 + half;
+          q[d] = *(const lds8 *)(lds + BUF + kWideTile * R0 + n * R1 + place_of<R1>(n, c) * 16);
+        }
+        // to the accumulation registers, from which a matrix instruction takes
+        // an operand as well: the sums need the others
+        asm volatile("" : "+a"(q[d]));
+      }
+      lds_reads_done();
+      __syncthreads();
+      rows.ask(3, 3);
+      loader(1, 1).all();
+      int buf = 0;
+      loop_aligned();
+      for (int v = 0; v < it.n_tiles; ++v) {
+        if (rows.pages) loads_done<LatentLoader::N + 1>();
+        else loads_done<LatentLoader::N>();
+        __syncthreads();
+        const lds_u8 *now = lds + buf * BUF, *sc = lds + SCALES + buf * 1024;
+        const int key0 = Plain::first_key(it, v, kWideTile);
+        const bool whole = Plain::whole_tile(a, it, key0, kWideTile);
+        const bool agree = v == 0 || !whole;
+        const bool odd =
+            SCAN && !whole && __syncthreads_or(odd_codes<kWideTile>(now, threadIdx.x, 256));
+        left |= odd;
+        rows.ask(v + 4, v + 4);
+        const LatentLoader load = loader(v + 2, buf == 0 ? 2 : buf - 1);
+        buf = buf == 2 ? 0 : buf + 1;
+        if (odd || idle) {
+          load.all();
+          if (!odd && agree) __syncthreads();
+          if (!odd) __syncthreads();
+          continue;
+        }
+        const uint32_t scale = ((const lds_u32 *)sc)[(32 * part + (lane & 31)) * 4] & 255;
+        lay_scales(by_key, lane, scale);
+        f32x16 s;
+        products<kWideTile>(q, now, 32 * part, w, scale_of(scale), load, &s);
+        ValueScales by;
+        take_scales(by_key, half, &by);
+        float top = top_of(a, it, &s, key0 + 32 * part, whole, see, half, by);
+        if (agree) {
+          if (half == 0) ((lds_float *)(mine + 2048 + 128))[lane] = top;
+          __syncthreads();
+          top = fmaxf(top, ((const lds_float *)(theirs + 2048 + 128))[lane & 31]);
+        }
+        Plain::take_top(st, top, !agree);
+        x8 p[2];
+        st.l += weights(s, a.c, st.m, by, p);
+        const float m = st.m;
+        ((lds8 *)mine)[lane] = p[0];
+        ((lds8 *)mine)[64 + lane] = p[1];
+        if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
+        add_values<kWideTile, 2, NT>(p, now, 32 * part, w, part * NT, &st);
+        __syncthreads();
+        p[0] = ((const lds8 *)theirs)[lane];
+        p[1] = ((const lds8 *)theirs)[64 + lane];
+        const float m2 = ((const lds_float *)(theirs + 2048))[lane & 31];
+        if (__any(m2 != m)) {
+          const float both = fmaxf(m, m2);
+          const float f2 = __builtin_amdgcn_exp2f(m2 - Plain::finite_m(both));
+          Plain::template rescale<NT>(st.o, &st.l,
+                                      __builtin_amdgcn_exp2f(m - Plain::finite_m(both)));
+          st.m = both;
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              p[b][j] = static_cast<T>(static_cast<float>(p[b][j]) * f2);
+        }
+        add_values<kWideTile, 2, NT>(p, now, 32 * (1 - part), w, part * NT, &st);
+      }
+      loads_done();
+    }
+    // each wave has summed the weights of its own keys
+    float l = st.l + other_half(st.l, half);
+    __syncthreads();
+    ((lds_float *)mine)[lane] = l;
+    __syncthreads();
+    l += ((const lds_float *)theirs)[lane];
+    if constexpr (SCAN) {
+      if (__syncthreads_or(left)) {
+        Plain::lay_down(it, lds, row, half, st, l, part * NT, true);
+        Plain::template careful<Values>(a, it, lds);
+        return true;
+      }
+    } else if (__syncthreads_or(row < it.n_rows && Plain::odd_sums(st.o, l))) {
+      return false;
+    }
+    Plain::store(a, it, lds + wave * 128 * NT * 32, (wave >> 1) * 32, lane, st, l, part * NT);
+    return true;
+  }
+
+  // ---- wide items
+
+  // A wave's share of a tile, 16 keys: its codes come to registers while an earlier
+  // tile is worked on, and go to LDS as the values they stand for, to where a tile of
+  // 16-bit rows has them.  Row lane / 4, chunk lane % 4 of 64 bytes at a time.
+  struct Share {
+    static constexpr int N0 = DK / 64, N1 = DV / 64;
+    u32x4 raw0[N0], raw1[N1];
+    uint32_t scale[2];
+
+    __device__ __forceinline__ void ask(const AttendArgs &a, const AttendItem &it,
+                                        const uint8_t *row, int lane) {
+      const uint8_t *from = row + lane % 4 * 16;
+#pragma unroll
+      for (int j = 0; j < N0; ++j)
+        raw0[j] = *reinterpret_cast<const u32x4 *>(from + key_at(it) + 64 * j);
+#pragma unroll
+      for (int j = 0; j < N1; ++j)
+        raw1[j] = *reinterpret_cast<const u32x4 *>(from + value_at(a, it) + 64 * j);
+      scale[0] = row[key_scale_at(a, it)];
+      scale[1] = row[value_scale_at(a, it)];
+    }
+    __device__ __forceinline__ void put(lds_u8 *tile, int wave, int lane) const {
+      typedef __attribute__((address_space(3))) x8 lds8;
+      const int row = wave * 16 + lane / 4;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const float f = scale_of(scale[part]);
+        lds_u8 *to = tile + (part ? kWideTile * R0 + row * R1 : row * R0);
+#pragma unroll
+        for (int j = 0; j < (part ? N1 : N0); ++j) {
+          const u32x4 raw = part ? raw1[j] : raw0[j];
+          const int c = lane % 4 * 2 + 8 * j;
+          *(lds8 *)(to + place_of<R0>(row, c) * 16) = values8<T>(u32x2{raw[0], raw[1]}, f);
+          *(lds8 *)(to + place_of<R0>(row, c + 1) * 16) = values8<T>(u32x2{raw[2], raw[3]}, f);
+        }
+      }
+    }
+  };
+
+  // As Attend::wide.
+  template <bool SCAN>
+  static __device__ __forceinline__ bool wide(const AttendArgs &a, const AttendItem &it,
+                                              lds_u8 *lds) {
+    constexpr int RH = kRows / 128, BUF = kWideTile * ROW;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int row = wave * 32 * RH + (lane & 31), half = lane >> 5;
+    const bool idle = wave * 32 * RH >= it.n_rows;  // a wave without rows only loads
+    const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
+    if (it.n_tiles > 0) {
+      rows.ask(0, 0);
+      rows.ask(1, 1);
+    }
+    x8 q[RH * (DK / 16)];
+    Sight see[RH];
+    State st[RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      int pos;
+      Plain::load_queries(a, it, row + 32 * r, half, q + r * (DK / 16), &pos);
+      see[r] = Plain::sight(a, it, pos);
+      st[r].clear();
+    }
+    typename Plain::Places w;
+    Plain::find_places(w, lane);
+    bool left = false;  // SCAN: a tile is left to `careful`
+    if (it.n_tiles > 0) {
+      Share share;
+      const auto ask = [&](int v) {
+        share.ask(a, it, rows.src + rows.row(v, v, lane >> 2), lane);
+        rows.ask(v + 2, v + 2);
+      };
+      loads_done();
+      ask(0);
+      share.put(lds, wave, lane);
+      ask(1);
+      lds_reads_done();
+      loop_aligned();
+      for (int v = 0; v < it.n_tiles; ++v) {
+        __syncthreads();
+        lds_u8 *now = lds + (v & 1) * BUF;
+        const int key0 = Plain::first_key(it, v, kWideTile);
+        const bool whole = Plain::whole_tile(a, it, key0, kWideTile);
+        const bool odd =
+            SCAN && !whole &&
+            __syncthreads_or(Plain::template odd_values<kWideTile>(now, threadIdx.x, 256));
+        left |= odd;
+        const auto next = [&]() {
+          share.put(lds + (~v & 1) * BUF, wave, lane);
+          loads_done();  // (the page numbers of tile v + 2)
+          ask(v + 2);
+        };
+        if (odd || idle) {
+          next();
+          continue;
+        }
+        if constexpr (RH == 1) {
+          f32x16 s[2];
+          Plain::template products<kWideTile, 0, 2>(q, now, 0, w, NoLoader(), s);
+          Plain::template products<kWideTile, DK / 32, 2>(q, now, 32, w, NoLoader(), s + 1);
+          x8 p[4];
+          Plain::template weigh<2>(a, it, s, key0, whole, see[0], st[0], half, p);
+          next();
+          Plain::template add_values<4, NT, 0>(p, now + kWideTile * R0, w, 0, st, NoLoader());
+        } else {
+          Plain::template thirty_two<0, RH>(a, it, q, now, w, key0, whole, see, st, half,
+                                            NoLoader());
+          next();
+          Plain::template thirty_two<1, RH>(a, it, q, now, w, key0, whole, see, st, half,
+                                            NoLoader());
+        }
+      }
+      loads_done();
+    }
+    float l[RH];
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      l[r] = st[r].l + other_half(st[r].l, half);
+      bad |= row + 32 * r < it.n_rows && Plain::odd_sums(st[r].o, l[r]);
+    }
+    if constexpr (SCAN) {
+      if (__syncthreads_or(left)) {
+#pragma unroll
+        for (int r = 0; r < RH; ++r)
+          Plain::lay_down(it, lds, row + 32 * r, half, st[r], l[r], 0, true);
+        Plain::template careful<Values>(a, it, lds);
+        return true;
+      }
+    } else if (__syncthreads_or(bad)) {
+      return false;
+    }
+#pragma unroll
+    for (int r = 0; r < RH; ++r)
+      Plain::store(a, it, lds + wave * 128 * NT * 32, (wave * RH + r) * 32, lane, st[r], l[r], 0);
+    return true;
+  }
+
+  template <bool SCAN>
+  static __device__ __forceinline__ bool item(const AttendArgs &a, const AttendItem &it,
+                                              lds_u8 *lds) {
+    if constexpr (IN_KEY) return latent<SCAN>(a, it, lds);
+    else if constexpr (NARROW) return narrow<SCAN>(a, it, lds);
+    else return it.wide ? wide<SCAN>(a, it, lds) : narrow<SCAN>(a, it, lds);
+  }
+  // Apart, so that the registers of the common case are allotted without it.
+  static __device__ __attribute__((noinline)) void again(AttendArgs a, AttendItem it,
+                                                         lds_u8 *lds) {
+    item<true>(uniform(a), uniform(it), uniform(lds));
+  }
+};
+
+}  // namespace
 
 int launch_attend_held(int type, int which, const AttendArgs &a, bool narrow,
                        hipStream_t stream) {
-  return type == GPB_BF16 ? launch_format<__bf16, true>(which, a, narrow, stream)
-                          : launch_format<_Float16, true>(which, a, narrow, stream);
+  return type == GPB_BF16 ? launch_format<__bf16, AttendHeld>(which, a, narrow, stream)
+                          : launch_format<_Float16, AttendHeld>(which, a, narrow, stream);
 }
 
 }  // namespace gpb

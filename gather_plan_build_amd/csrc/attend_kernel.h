@@ -40,7 +40,6 @@
 #include <cmath>
 
 #include "attend.h"
-#include "held.h"
 
 namespace gpb {
 namespace {
@@ -181,16 +180,17 @@ __device__ __forceinline__ constexpr int chunk_at(int r, int place) {
   return turned_back<ROW_BYTES>(place ^ row_bits<ROW_BYTES>(r));
 }
 
-// NARROW: a kernel of narrow items alone, with the LDS of those.  HELD: rows held
-// in 8 bits, which become rows of 16 on their way to LDS.
-template <typename T, int DK, int DV, bool IN_KEY, bool NARROW, bool HELD>
+// NARROW: a kernel of narrow items alone, with the LDS of those.
+template <typename T, int DK, int DV, bool IN_KEY, bool NARROW>
 struct Attend {
+  static constexpr int KERNEL = IN_KEY ? 2 : DK / 128;        // as attend_kernel
+  static constexpr bool NARROW_ALONE = NARROW;
   static constexpr int KB = DK * 2, VB = DV * 2;              // bytes of a key, a value
   // A tile of n keys in LDS: n rows of K0 bytes (a key, or the value part of a
   // latent), then n rows of R1 bytes (a value, or the rest of a latent).
   static constexpr int R0 = IN_KEY ? VB : KB, R1 = IN_KEY ? KB - VB : VB;
   static constexpr int ROW = R0 + R1;                          // LDS bytes per key
-  static constexpr int kRows = rows_of(IN_KEY ? 2 : DK / 128, !NARROW);  // of an item, at most
+  static constexpr int kRows = rows_of(KERNEL, !NARROW);  // of an item, at most
   // the tile in use and the one under way, or in the end a row's sums
   static constexpr int TILES_LDS =
       NARROW ? 4 * kNarrowTile * ROW : std::max(2 * kWideTile * ROW, kRows * DV * 4);
@@ -367,77 +367,6 @@ struct Attend {
     template <int I>
     __device__ __forceinline__ void issue() const {}
   };
-
-  // A tile of held rows, a wave's share of TILE / WAVES keys: its codes come to
-  // registers while an earlier tile is worked on, and go to LDS as the values they
-  // stand for, to where a tile of 16-bit rows has them.  `scale` is of the key
-  // whose place the lane finds.
-  template <int TILE, int WAVES>
-  struct HeldTile {
-    static constexpr int KEYS = TILE / WAVES;
-    // 16-byte chunks of the two parts of a held row, and loads of a wave
-    static constexpr int C0 = R0 / 32, C1 = IN_KEY ? R1 / 16 : R1 / 32;
-    static constexpr int N0 = KEYS * C0 / 64, N1 = KEYS * C1 / 64;
-    u32x4 raw0[N0], raw1[N1];
-    uint32_t scale[2];
-
-    __device__ __forceinline__ void ask(const AttendArgs &a, const AttendItem &it,
-                                        const Source &from, uint64_t off, int lane) {
-      const uint8_t *src = uniform(from.src);
-      const int64_t at0 = IN_KEY ? 0 : static_cast<int64_t>(it.kv_head) * DK;
-      const int64_t at1 = IN_KEY ? DV : static_cast<int64_t>(a.hkv) * DK +
-                                            static_cast<int64_t>(it.kv_head) * DV;
-#pragma unroll
-      for (int j = 0; j < N0; ++j)
-        raw0[j] = *reinterpret_cast<const u32x4 *>(
-            src + at0 + place(off, j * (64 / C0) + lane / C0) + lane % C0 * 16);
-#pragma unroll
-      for (int j = 0; j < N1; ++j)
-        raw1[j] = *reinterpret_cast<const u32x4 *>(
-            src + at1 + place(off, j * (64 / C1) + lane / C1) + lane % C1 * 16);
-      const uint8_t *s = src + held_scales(a) + it.kv_head + off;
-      scale[0] = *s;
-      if constexpr (!IN_KEY) scale[1] = s[a.hkv];
-    }
-    static __device__ __forceinline__ uint64_t place(uint64_t off, int r) {
-      const uint32_t lo = __shfl(static_cast<uint32_t>(off), r, 64);
-      const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), r, 64);
-      return lo | static_cast<uint64_t>(hi) << 32;
-    }
-    __device__ __forceinline__ void put(lds_u8 *tile, int wave, int lane) const {
-      typedef __attribute__((address_space(3))) x8 lds8;
-      typedef __attribute__((address_space(3))) u32x4 lds16;
-#pragma unroll
-      for (int j = 0; j < N0; ++j) {
-        const int r = j * (64 / C0) + lane / C0, c = lane % C0 * 2, row = wave * KEYS + r;
-        const float f = scale_of(__shfl(scale[0], r, 64));
-        lds_u8 *to = tile + row * R0;
-        *(lds8 *)(to + place_of<R0>(row, c) * 16) =
-            values8<T>(u32x2{raw0[j][0], raw0[j][1]}, f);
-        *(lds8 *)(to + place_of<R0>(row, c + 1) * 16) =
-            values8<T>(u32x2{raw0[j][2], raw0[j][3]}, f);
-      }
-#pragma unroll
-      for (int j = 0; j < N1; ++j) {
-        const int r = j * (64 / C1) + lane / C1, row = wave * KEYS + r;
-        lds_u8 *to = tile + TILE * R0 + row * R1;
-        if constexpr (IN_KEY) {
-          *(lds16 *)(to + place_of<R1>(row, lane % C1) * 16) = raw1[j];
-        } else {
-          const int c = lane % C1 * 2;
-          const float f = scale_of(__shfl(scale[1], r, 64));
-          *(lds8 *)(to + place_of<R1>(row, c) * 16) =
-              values8<T>(u32x2{raw1[j][0], raw1[j][1]}, f);
-          *(lds8 *)(to + place_of<R1>(row, c + 1) * 16) =
-              values8<T>(u32x2{raw1[j][2], raw1[j][3]}, f);
-        }
-      }
-    }
-  };
-  // Bytes from a held row's start to its first scale.
-  static __device__ __forceinline__ int64_t held_scales(const AttendArgs &a) {
-    return IN_KEY ? DV + 2 * (DK - DV) : static_cast<int64_t>(a.hkv) * (DK + DV);
-  }
 
   struct State {
     f32x16 o[NT];
@@ -833,6 +762,26 @@ struct Attend {
       ml[2 * row + 1] = l;
     }
   }
+  // Values of rows, by their byte offset from src.
+  struct Values {
+    const T *keys, *vals;
+    __device__ __forceinline__ Values(const AttendArgs &a, const AttendItem &it,
+                                      const uint8_t *src)
+        : keys(reinterpret_cast<const T *>(src) + static_cast<int64_t>(it.kv_head) * DK),
+          vals(IN_KEY ? keys : reinterpret_cast<const T *>(src) +
+                                   static_cast<int64_t>(a.hkv) * DK +
+                                   static_cast<int64_t>(it.kv_head) * DV) {}
+    __device__ __forceinline__ float key(int64_t off, int e) const {
+      return static_cast<float>(keys[off / 2 + e]);
+    }
+    __device__ __forceinline__ float value(int64_t off, int e) const {
+      return static_cast<float>(vals[off / 2 + e]);
+    }
+    __device__ __forceinline__ bool odd(int64_t off, int e) const {
+      return not_finite(__builtin_bit_cast(uint16_t, vals[off / 2 + e]));
+    }
+  };
+  template <class V = Values>
   static __device__ void careful(const AttendArgs &a, const AttendItem &it, lds_u8 *lds) {
     typedef __attribute__((address_space(3))) float lds_float;
     lds_float *sums = (lds_float *)lds, *ml = (lds_float *)(lds + TILES_LDS);
@@ -841,22 +790,7 @@ struct Attend {
     __syncthreads();
     const int tile = it.wide ? kWideTile : kNarrowTile;
     const Source from(a, it);
-    const int64_t key_at = static_cast<int64_t>(it.kv_head) * DK;
-    const int64_t val_at =
-        IN_KEY ? 0 : static_cast<int64_t>(a.hkv) * DK + static_cast<int64_t>(it.kv_head) * DV;
-    // value e of the key, or of the value, of the row at `off`
-    const auto key_value = [&](uint64_t off, int e) -> T {
-      const uint8_t *row = from.src + off;
-      if constexpr (!HELD) return reinterpret_cast<const T *>(row)[key_at + e];
-      if (IN_KEY && e >= DV) return reinterpret_cast<const T *>(row + DV)[e - DV];
-      return values8<T>(u32x2{row[key_at + e], 0}, scale_of(row[held_scales(a) + it.kv_head]))[0];
-    };
-    const auto val_value = [&](uint64_t off, int e) -> T {
-      const uint8_t *row = from.src + off;
-      if constexpr (!HELD) return reinterpret_cast<const T *>(row)[val_at + e];
-      return values8<T>(u32x2{row[val_at + e], 0},
-                        scale_of(row[held_scales(a) + (IN_KEY ? 0 : a.hkv) + it.kv_head]))[0];
-    };
+    const V rows(a, it, from.src);
     for (int r = threadIdx.x >> 6; r < it.n_rows; r += 4) {
       const int g = it.row0 + r;
       const int token = g / a.G, h = g - token * a.G + it.kv_head * a.G;
@@ -872,18 +806,17 @@ struct Attend {
         if (whole_tile(a, it, key0, tile)) continue;
         bool odd = false;
         for (int x = 0; x < tile; ++x) {
-          const uint64_t off = from.offset(key0 + x);
-          for (int e = lane; e < DV; e += 64)
-            odd |= not_finite(__builtin_bit_cast(uint16_t, val_value(off, e)));
+          const int64_t off = from.offset(key0 + x);
+          for (int e = lane; e < DV; e += 64) odd |= rows.odd(off, e);
         }
         if (!__any(odd)) continue;
         for (int x = 0; x < tile; ++x) {
           const unsigned key = key0 + x;
           if (key - see.from >= see.n && key - it.key_lo >= see.sunk) continue;
-          const uint64_t at = from.offset(key);
+          const int64_t at = from.offset(key);
           float s = 0.0f;
 #pragma unroll
-          for (int e = 0; e < PK; ++e) s += q[e] * static_cast<float>(key_value(at, e * 64 + lane));
+          for (int e = 0; e < PK; ++e) s += q[e] * rows.key(at, e * 64 + lane);
 #pragma unroll
           for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
           s *= a.c;
@@ -893,7 +826,7 @@ struct Attend {
           sum = sum * f + w;
 #pragma unroll
           for (int e = 0; e < PV; ++e)
-            o[e] = o[e] * f + w * static_cast<float>(val_value(at, e * 64 + lane));
+            o[e] = o[e] * f + w * rows.value(at, e * 64 + lane);
           m = top;
         }
       }
@@ -947,24 +880,14 @@ struct Attend {
     Places w;
     find_places(w, lane);
     bool left = false;  // SCAN: a tile is left to `careful`
-    HeldTile<kWideTile, 4> held;
     if (it.n_tiles > 0) {
       loads_done();
-      if constexpr (HELD) {
-        held.ask(a, it, rows, rows.row(0, 0, lane), lane);
-        rows.ask(1, 1);
-        held.put(lds, wave, lane);
-        loads_done();
-        held.ask(a, it, rows, rows.row(1, 1, lane), lane);
-        rows.ask(2, 2);
-      } else {
-        Load(a, it, rows, rows.row(0, 0, lane), lds, wave, lane).all();
-        rows.ask(1, 1);
-      }
+      Load(a, it, rows, rows.row(0, 0, lane), lds, wave, lane).all();
+      rows.ask(1, 1);
       lds_reads_done();
       loop_aligned();
       for (int v = 0; v < it.n_tiles; ++v) {
-        if constexpr (!HELD) loads_done();
+        loads_done();
         __syncthreads();
         lds_u8 *now = lds + (v & 1) * BUF;
         const int key0 = first_key(it, v, kWideTile);
@@ -972,32 +895,6 @@ struct Attend {
         const bool odd = SCAN && !whole &&
                          __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        if constexpr (HELD) {
-          const auto next = [&]() {
-            held.put(lds + (~v & 1) * BUF, wave, lane);
-            loads_done();
-            held.ask(a, it, rows, rows.row(v + 2, v + 2, lane), lane);
-            rows.ask(v + 3, v + 3);
-          };
-          if (odd || idle) {
-            next();
-            continue;
-          }
-          if constexpr (RH == 1) {
-            f32x16 s[2];
-            products<kWideTile, 0, 2>(q, now, 0, w, NoLoader(), s);
-            products<kWideTile, DK / 32, 2>(q, now, 32, w, NoLoader(), s + 1);
-            x8 p[4];
-            weigh<2>(a, it, s, key0, whole, see[0], st[0], half, p);
-            next();
-            add_values<4, NT, 0>(p, now + kWideTile * R0, w, 0, st, NoLoader());
-          } else {
-            thirty_two<0, RH>(a, it, q, now, w, key0, whole, see, st, half, NoLoader());
-            next();
-            thirty_two<1, RH>(a, it, q, now, w, key0, whole, see, st, half, NoLoader());
-          }
-          continue;
-        }
         const Load load(a, it, rows, rows.row(v + 1, v + 1, lane), lds + (~v & 1) * BUF, wave, lane);
         rows.ask(v + 2, v + 2);
         if (odd || idle) {
@@ -1088,7 +985,6 @@ struct Attend {
     State st;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
-    HeldTile<kWideTile, 4> held;
     if (it.n_tiles > 0) {
       typedef Loader<kWideTile, 4> Load;
       rows.ask(0, 0);
@@ -1101,17 +997,11 @@ struct Attend {
              static_cast<uint64_t>(t * a.q_ts + h * a.q_hs) * 2, lds + BUF, wave, lane)
             .all();
       }
-      if constexpr (HELD) {
-        loads_done();
-        held.ask(a, it, rows, rows.row(0, 0, lane), lane);
-        rows.ask(1, 1);
-      } else {
-        loads_done<Load::N>();
-        Load(a, it, rows, rows.row(0, 0, lane), lds, wave, lane).all();
-        rows.ask(1, 1);
-        if (rows.pages) loads_done<Load::N + 1>();
-        else loads_done<Load::N>();
-      }
+      loads_done<Load::N>();
+      Load(a, it, rows, rows.row(0, 0, lane), lds, wave, lane).all();
+      rows.ask(1, 1);
+      if (rows.pages) loads_done<Load::N + 1>();
+      else loads_done<Load::N>();
       __syncthreads();
 #pragma unroll
       for (int d = 0; d < DK / 16; ++d) {
@@ -1120,16 +1010,10 @@ struct Attend {
         // an operand as well: the sums need the others
         asm volatile("" : "+a"(q[d]));
       }
-      if constexpr (HELD) {
-        held.put(lds, wave, lane);
-        loads_done();
-        held.ask(a, it, rows, rows.row(1, 1, lane), lane);
-        rows.ask(2, 2);
-      }
       lds_reads_done();
       loop_aligned();
       for (int v = 0; v < it.n_tiles; ++v) {
-        if constexpr (!HELD) loads_done();
+        loads_done();
         __syncthreads();
         lds_u8 *now = lds + (v & 1) * BUF;
         const int key0 = first_key(it, v, kWideTile);
@@ -1138,24 +1022,10 @@ struct Attend {
         const bool odd =
             SCAN && !whole && __syncthreads_or(odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const auto next = [&]() {
-          if constexpr (HELD) {
-            held.put(lds + (~v & 1) * BUF, wave, lane);
-            loads_done();
-            held.ask(a, it, rows, rows.row(v + 2, v + 2, lane), lane);
-            rows.ask(v + 3, v + 3);
-          }
-        };
-        const auto load = [&]() {
-          if constexpr (HELD) return NoLoader();
-          else
-            return Load(a, it, rows, rows.row(v + 1, v + 1, lane), lds + (~v & 1) * BUF, wave,
-                        lane);
-        }();
-        if constexpr (!HELD) rows.ask(v + 2, v + 2);
+        const Load load(a, it, rows, rows.row(v + 1, v + 1, lane), lds + (~v & 1) * BUF, wave, lane);
+        rows.ask(v + 2, v + 2);
         if (odd || idle) {
-          if constexpr (HELD) next();
-          else load.all();
+          load.all();
           if (!odd && agree) __syncthreads();
           if (!odd) __syncthreads();
           continue;
@@ -1175,7 +1045,6 @@ struct Attend {
         ((lds8 *)mine)[lane] = p[0];
         ((lds8 *)mine)[64 + lane] = p[1];
         if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
-        next();
         add_values<2, NT, DK / 48>(p, now + 32 * part * VS, w, part * NT, &st, load);
         __syncthreads();
         p[0] = ((const lds8 *)theirs)[lane];
@@ -1240,39 +1109,18 @@ struct Attend {
     const Sight see = sight(a, it, pos);
     State st;
     lds_u8 *own = lds + wave * kNarrowTile * ROW;
-    typedef __attribute__((address_space(3))) float lds_float;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
     if (wave < it.n_tiles) {
       typedef Loader<kNarrowTile, 1> Load;
-      HeldTile<kNarrowTile, 1> held;
       loads_done();
-      if constexpr (HELD) held.ask(a, it, rows, rows.row(wave, 0, lane), lane);
-      else Load(a, it, rows, rows.row(wave, 0, lane), own, 0, lane).all();
+      Load(a, it, rows, rows.row(wave, 0, lane), own, 0, lane).all();
       int n = 0;  // tiles of the wave so far
       lds_reads_done();
       loop_aligned();
       for (int v = wave; v < it.n_tiles; v += 4, ++n) {
         const int key0 = first_key(it, v, kNarrowTile);
         const bool whole = whole_tile(a, it, key0, kNarrowTile);
-        if constexpr (HELD) {
-          held.put(own, 0, lane);
-          loads_done();
-          if (v + 4 < it.n_tiles) {
-            held.ask(a, it, rows, rows.row(v + 4, n + 1, lane), lane);
-            rows.ask(v + 8, n + 2);
-          }
-          if (SCAN && !whole && __any(odd_values<kNarrowTile>(own, lane, 64))) {
-            left = true;
-            continue;
-          }
-          f32x16 s;
-          products<kNarrowTile, 0, 1>(q, own, 0, w, NoLoader(), &s);
-          x8 p[2];
-          weigh<1>(a, it, &s, key0, whole, see, st, half, p);
-          add_values<2, NT, 0>(p, own + kNarrowTile * R0, w, 0, &st, NoLoader());
-          continue;
-        }
         if constexpr (SCAN) loads_done();
         else loads_done<Load::N1>();  // the keys; the values may be on their way
         if (SCAN && !whole && __any(odd_values<kNarrowTile>(own, lane, 64))) {
@@ -1303,14 +1151,22 @@ struct Attend {
       }
       loads_done();
     }
-    const float l = st.l + other_half(st.l, half);
+    return narrow_end<SCAN>(a, it, lds, wave, lane, st, left);
+  }
 
-    // The waves lay their sums side by side, and a wave takes a row at a time
-    // of all four.
+  // The waves of a narrow item lay their sums side by side, and a wave takes a row
+  // at a time of all four.
+  template <bool SCAN, class V = Values>
+  static __device__ __forceinline__ bool narrow_end(const AttendArgs &a, const AttendItem &it,
+                                                    lds_u8 *lds, int wave, int lane,
+                                                    const State &st, bool left) {
+    const int row = lane & 31, half = lane >> 5;
+    const float l = st.l + other_half(st.l, half);
     constexpr int C = DV / 4, M = C < 32 ? C - 1 : 31, PER = DV / 64;
     typedef __attribute__((address_space(3))) u32x4 lds16;
-    typedef float Values __attribute__((ext_vector_type(PER)));
-    typedef __attribute__((address_space(3))) Values lds_values;
+    typedef float Sums __attribute__((ext_vector_type(PER)));
+    typedef __attribute__((address_space(3))) Sums lds_sums;
+    typedef __attribute__((address_space(3))) float lds_float;
     lds_float *ml = (lds_float *)(lds + TILES_LDS);  // of wave w, row r: w * 32 + r
     __syncthreads();
     if (row < it.n_rows) {
@@ -1338,13 +1194,13 @@ struct Attend {
         m[x] = ml[2 * (x * 32 + r)];
         top = fmaxf(top, m[x]);
       }
-      Values o = {};
+      Sums o = {};
       const int chunk = lane * PER / 4, rest = lane * PER % 4;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const float f = __builtin_amdgcn_exp2f(m[x] - finite_m(top));
         sum += ml[2 * (x * 32 + r) + 1] * f;
-        o += *(const lds_values *)(lds + ((x * 32 + r) * C + (chunk ^ (r & M))) * 16 + rest * 4) * f;
+        o += *(const lds_sums *)(lds + ((x * 32 + r) * C + (chunk ^ (r & M))) * 16 + rest * 4) * f;
       }
       float zero = sum * 0.0f;
 #pragma unroll
@@ -1362,7 +1218,7 @@ struct Attend {
       }
       if (it.partial >= 0) {
         const int64_t at = static_cast<int64_t>(it.partial) + r;
-        *reinterpret_cast<Values *>(a.sums + at * DV + lane * PER) = o;
+        *reinterpret_cast<Sums *>(a.sums + at * DV + lane * PER) = o;
         if (lane == 0) *reinterpret_cast<f32x2 *>(a.ml + 2 * at) = f32x2{top, sum};
         continue;
       }
@@ -1376,7 +1232,7 @@ struct Attend {
       if (lane == 0 && a.lse) a.lse[lse_at] = log_sum(top, sum);
     }
     if constexpr (SCAN) {
-      if (left) careful(a, it, lds);
+      if (left) careful<V>(a, it, lds);
       return true;
     } else {
       return !__syncthreads_or(odd);  // (what was written is written over)
@@ -1398,9 +1254,8 @@ struct Attend {
   }
 };
 
-template <typename T, int DK, int DV, bool IN_KEY, bool NARROW, bool HELD>
-__global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128)) void k_attend(AttendArgs a) {
-  typedef Attend<T, DK, DV, IN_KEY, NARROW, HELD> A;
+template <class A>
+__global__ __launch_bounds__(256, blocks_per_cu(A::KERNEL)) void k_attend(AttendArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t memory[A::LDS];
   lds_u8 *lds = (lds_u8 *)memory;
   // The arguments come in lines of 64 bytes, each a trip to memory: one of every
@@ -1408,7 +1263,7 @@ __global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128)) void 
   // of latent rows: 21.1 us so, 22.0 without).
   asm volatile("" ::"s"(a.list), "s"(a.sums), "s"(a.status), "s"(a.positions_at));
   const AttendItem it = reinterpret_cast<const AttendItem *>(a.list)[blockIdx.x];
-  if (!item_fits(a, it, IN_KEY ? 2 : DK / 128, NARROW)) {
+  if (!item_fits(a, it, A::KERNEL, A::NARROW_ALONE)) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, GPB_STATUS_BAD_PLAN_INPUT);
     return;
   }
@@ -1422,7 +1277,7 @@ __global__ __launch_bounds__(256, blocks_per_cu(DK == 576 ? 2 : DK / 128)) void 
 // rows, by the sums: 8.8 us for 22 MB.
 template <typename T, int DV>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
-  typedef Attend<T, 64, 64, false, false, false> A;  // for what depends on T alone
+  typedef Attend<T, 64, 64, false, false> A;  // for what depends on T alone
   const AttendJoin j = reinterpret_cast<const AttendJoin *>(a.list + a.joins_at)[blockIdx.x];
   const int lane = threadIdx.x & 63, r = blockIdx.y * 4 + wave_id();
   constexpr int PER = DV / 64;
@@ -1488,13 +1343,13 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   if (lane == 0 && a.lse) a.lse[static_cast<int64_t>(t) * a.n_heads + h] = A::log_sum(top, l);
 }
 
-template <typename T, bool HELD, int DK, int DV, bool IN_KEY>
+// One launch for the items and, where there are parts, one for their joins.  The
+// classes are what the kernels run, of items of both kinds and of narrow ones alone.
+template <typename T, int DV, class BOTH, class ALONE>
 int launch_attend(const AttendArgs &a, bool narrow, hipStream_t st) {
   const dim3 items(a.n_items), block(256);
-  int rc;
-  if constexpr (IN_KEY) rc = launch(k_attend<T, DK, DV, true, false, HELD>, items, block, st, a);
-  else rc = narrow ? launch(k_attend<T, DK, DV, false, true, HELD>, items, block, st, a)
-                   : launch(k_attend<T, DK, DV, false, false, HELD>, items, block, st, a);
+  int rc = narrow ? launch(k_attend<ALONE>, items, block, st, a)
+                  : launch(k_attend<BOTH>, items, block, st, a);
   if (rc == GPB_OK && a.n_joins > 0)
     rc = launch(k_attend_join<T, DV>,
                 dim3(a.n_joins, static_cast<uint32_t>(std::min(a.G, kNarrowRows) + 3) / 4), block,
@@ -1502,11 +1357,17 @@ int launch_attend(const AttendArgs &a, bool narrow, hipStream_t st) {
   return rc;
 }
 
-template <typename T, bool HELD>
+// `Kernel`: Attend, or AttendHeld.
+template <typename T, template <typename, int, int, bool, bool> class Kernel>
 int launch_format(int which, const AttendArgs &a, bool narrow, hipStream_t st) {
-  if (which == 0) return launch_attend<T, HELD, 64, 64, false>(a, narrow, st);
-  if (which == 1) return launch_attend<T, HELD, 128, 128, false>(a, narrow, st);
-  return launch_attend<T, HELD, 576, 512, true>(a, narrow, st);
+  if (which == 0)
+    return launch_attend<T, 64, Kernel<T, 64, 64, false, false>, Kernel<T, 64, 64, false, true>>(
+        a, narrow, st);
+  if (which == 1)
+    return launch_attend<T, 128, Kernel<T, 128, 128, false, false>,
+                         Kernel<T, 128, 128, false, true>>(a, narrow, st);
+  typedef Kernel<T, 576, 512, true, false> Latent;  // (all of one kind)
+  return launch_attend<T, 512, Latent, Latent>(a, false, st);
 }
 
 }  // namespace
