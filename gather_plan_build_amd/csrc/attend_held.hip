@@ -18,6 +18,8 @@
 // does not: its m is the maximum of s + log2 scale, the weight 2^(s + log2 scale -
 // m) at most 1 again, and l sums it over the scale.  Powers of two throughout: the
 // weight is rounded as it would be without.
+#include <type_traits>
+
 #include "attend_kernel.h"
 #include "held.h"
 
@@ -35,6 +37,35 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *from, lds_u8 *to) {
 }
 __device__ __forceinline__ void load4_to_lds(const uint8_t *from, lds_u8 *to) {
   load4_to_lds(reinterpret_cast<const int32_t *>(from), to);
+}
+
+// A number of the launch's that loops use, kept in a register: left to itself the
+// compiler, short of scalar registers, asks for the argument again in the loop, and
+// the wait for it is one for all that LDS owes as well.  What it then has to lay
+// aside goes to a vector register's lanes, without a wait.  44,600 queries over
+// latent rows: PINNED_FIGURE.
+template <typename V>
+__device__ __forceinline__ void keep(V &x) {
+  asm volatile("" : "+s"(x));
+}
+__device__ __forceinline__ AttendArgs kept(AttendArgs a) {
+  keep(a.window);
+  keep(a.sinks);
+  return a;
+}
+
+// What runs beside step I of a product: f(integral_constant I).
+template <typename F>
+struct Beside {
+  F f;
+  template <int I>
+  __device__ __forceinline__ void issue() const {
+    f(std::integral_constant<int, I>());
+  }
+};
+template <typename F>
+__device__ __forceinline__ Beside<F> beside(F f) {
+  return {f};
 }
 
 template <typename T, int DK, int DV, bool IN_KEY, bool NARROW>
@@ -163,26 +194,35 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
   // codes and one to a chunk of values.
   static constexpr int step_of(int D) { return D < CODE_STEPS ? 2 * D : D + CODE_STEPS; }
 
-  // q.k of the 32 keys in rows row0 .. of a tile and the lane's query row.  Conversions
-  // and reads stand behind the product they run beside.
+  // The first chunks of a product's keys.
+  template <int TILE>
+  struct KeyAhead {
+    static constexpr int N = KEY_STEPS < 4 ? KEY_STEPS : 4;
+    u32x4 raw[N];
+    __device__ __forceinline__ void read(const lds_u8 *tile, int row0, const Spots &w) {
+#pragma unroll
+      for (int d = 0; d < N; ++d) raw[d] = key_chunk<TILE>(tile, row0, w, d);
+    }
+  };
+  // q.k of the 32 keys in rows row0 .. of a tile, whose first chunks are in `ahead`, and
+  // the lane's query row.  Conversions and reads stand behind the product they run
+  // beside.
   template <int TILE, typename L>
   static __device__ __forceinline__ void products(const x8 *q, const lds_u8 *tile, int row0,
-                                                  const Spots &w, float scale, const L &next,
+                                                  const Spots &w, float scale,
+                                                  KeyAhead<TILE> &ahead, const L &next,
                                                   f32x16 *s) {
-    constexpr int AHEAD = KEY_STEPS < 4 ? KEY_STEPS : 4;
-    u32x4 raw[AHEAD];
-#pragma unroll
-    for (int d = 0; d < AHEAD; ++d) raw[d] = key_chunk<TILE>(tile, row0, w, d);
     *s = f32x16{};
     x8 k[2];
-    k[0] = operand<0, 0>(raw[0], scale);
-    k[1] = operand<0, 1>(raw[0], scale);
-    product_steps<TILE, 0, AHEAD>(q, tile, row0, w, scale, next, raw, k, s);
+    k[0] = operand<0, 0>(ahead.raw[0], scale);
+    k[1] = operand<0, 1>(ahead.raw[0], scale);
+    product_steps<TILE, 0>(q, tile, row0, w, scale, ahead.raw, k, next, s);
   }
-  template <int TILE, int D, int AHEAD, typename L>
+  template <int TILE, int D, typename L>
   static __device__ __forceinline__ void product_steps(const x8 *q, const lds_u8 *tile, int row0,
-                                                       const Spots &w, float scale, const L &next,
-                                                       u32x4 *raw, x8 *k, f32x16 *s) {
+                                                       const Spots &w, float scale, u32x4 *raw,
+                                                       x8 *k, const L &next, f32x16 *s) {
+    constexpr int AHEAD = KeyAhead<TILE>::N;
     if constexpr (D < KEY_STEPS) {
       constexpr bool MORE = D + 1 < KEY_STEPS;
       *s = mma<T>(k[0], q[step_of(D)], *s);
@@ -197,35 +237,45 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       if constexpr (MORE && D + 1 < CODE_STEPS) k[1] = operand<D + 1, 1>(raw[(D + 1) % AHEAD], scale);
       if constexpr (D + AHEAD < KEY_STEPS) raw[D % AHEAD] = key_chunk<TILE>(tile, row0, w, D + AHEAD);
       in_order();
-      product_steps<TILE, D + 1, AHEAD>(q, tile, row0, w, scale, next, raw, k, s);
+      product_steps<TILE, D + 1>(q, tile, row0, w, scale, raw, k, next, s);
     }
   }
 
-  // Sums of N output tiles (values 32 t0 ..) += weights p of 16 NP keys, from row0 on.
+  // Sums of N output tiles (values 32 t0 ..) += weights p of 16 NP keys, from row0 on:
+  // the first codes, then steps FROM .. TO, with each of which one of the loads of
+  // `next` goes out.
   template <int TILE, int NP, int N>
-  static __device__ __forceinline__ void add_values(const x8 *p, const lds_u8 *tile, int row0,
-                                                    const Spots &w, int t0, State *st) {
-    constexpr int AHEAD = NP * N < 6 ? NP * N : 6;
+  struct ValueAhead {
+    static constexpr int AHEAD = NP * N < 6 ? NP * N : 6;
     u32x2 raw[AHEAD];
-    const lds_u8 *at = tile + t0 / 2 * TILE * 64 + row0 * 64;
+    __device__ __forceinline__ void read(const lds_u8 *tile, int row0, const Spots &w, int t0) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) raw[i] = value_codes<TILE>(at, w, i / N * 16, i % N);
-    value_steps<TILE, NP, N, 0, AHEAD>(p, at, w, st, raw, values8<T>(raw[0], 1.0f));
-  }
-  template <int TILE, int NP, int N, int I, int AHEAD>
-  static __device__ __forceinline__ void value_steps(const x8 *p, const lds_u8 *at,
-                                                     const Spots &w, State *st, u32x2 *raw,
-                                                     x8 now) {
-    if constexpr (I < NP * N) {
-      st->o[I % N] = mma<T>(now, p[I / N], st->o[I % N]);
-      in_order();
-      if constexpr (I + 1 < NP * N) now = values8<T>(raw[(I + 1) % AHEAD], 1.0f);
-      if constexpr (I + AHEAD < NP * N)
-        raw[I % AHEAD] = value_codes<TILE>(at, w, (I + AHEAD) / N * 16, (I + AHEAD) % N);
-      in_order();
-      value_steps<TILE, NP, N, I + 1, AHEAD>(p, at, w, st, raw, now);
+      for (int i = 0; i < AHEAD; ++i) raw[i] = codes(tile, row0, w, t0, i);
     }
-  }
+    static __device__ __forceinline__ u32x2 codes(const lds_u8 *tile, int row0, const Spots &w,
+                                                  int t0, int i) {
+      return value_codes<TILE>(tile + t0 / 2 * TILE * 64 + row0 * 64, w, i / N * 16, i % N);
+    }
+    template <int FROM, int TO, typename L>
+    __device__ __forceinline__ void add(const x8 *p, const lds_u8 *tile, int row0,
+                                        const Spots &w, int t0, State *st, const L &next) {
+      steps<FROM, TO>(p, tile, row0, w, t0, st, next, values8<T>(raw[FROM % AHEAD], 1.0f));
+    }
+    template <int I, int TO, typename L>
+    __device__ __forceinline__ void steps(const x8 *p, const lds_u8 *tile, int row0,
+                                          const Spots &w, int t0, State *st, const L &next,
+                                          x8 now) {
+      if constexpr (I < TO) {
+        st->o[I % N] = mma<T>(now, p[I / N], st->o[I % N]);
+        in_order();
+        if constexpr (I + 1 < TO) now = values8<T>(raw[(I + 1) % AHEAD], 1.0f);
+        if constexpr (I + AHEAD < NP * N) raw[I % AHEAD] = codes(tile, row0, w, t0, I + AHEAD);
+        next.template issue<I>();
+        in_order();
+        steps<I + 1, TO>(p, tile, row0, w, t0, st, next, now);
+      }
+    }
+  };
 
   // Whether these lanes' share of a tile's value codes holds a NaN.
   template <int TILE>
@@ -277,19 +327,25 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       }
     }
   }
+  // In a vector register, where the loops have room for it: else they ask for the
+  // argument again and wait.
+  static __device__ __forceinline__ float in_vector(float x) {
+    asm volatile("" : "+v"(x));
+    return x;
+  }
   // The scores of 32 keys, masked, to units of log2 (fp16: with their scales); returns
   // the largest.
   static __device__ __forceinline__ float top_of(const AttendArgs &a, const AttendItem &it,
-                                                 f32x16 *s, int key0, bool whole,
+                                                 float c, f32x16 *s, int key0, bool whole,
                                                  const Sight &see, int half,
                                                  const ValueScales &scales) {
     if (!whole) Plain::mask(a, it, see, key0, half, *s);
     if constexpr (kHalf) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) (*s)[i] = __builtin_fmaf((*s)[i], a.c, scales.a[i]);
+      for (int i = 0; i < 16; ++i) (*s)[i] = __builtin_fmaf((*s)[i], c, scales.a[i]);
     }
     float top = Plain::largest(*s);
-    if constexpr (!kHalf) top *= a.c;
+    if constexpr (!kHalf) top *= c;
     return fmaxf(top, other_half(top, half));
   }
   // As Attend::weights, of what top_of left.
@@ -312,7 +368,9 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     return (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 
-  // The rows of a wave's KEYS keys of tiles of TILE (see Attend::Rows).
+  // The rows of a wave's KEYS keys of tiles of TILE (see Attend::Rows).  Where they
+  // are all to be read as they are, and a page has 2^n rows, their places take a few
+  // instructions; the loops have no room for more.
   template <int TILE, int KEYS>
   struct Rows : Source {
     const AttendItem &it;
@@ -322,19 +380,53 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     __device__ __forceinline__ Rows(const AttendArgs &a, const AttendItem &it, lds_u8 *lds,
                                     int wave, int lane)
         : Source(a, it), it(it), ring(lds + RING + wave * 1024),
-          first(TILE == KEYS ? 0 : wave * KEYS), lane(lane) {}
+          first(TILE == KEYS ? 0 : wave * KEYS), lane(lane) {
+      keep(this->src);
+      keep(this->pages);
+      keep(this->status);
+      keep(this->stride);
+      keep(this->page_rows);
+      keep(this->page_shift);
+      keep(this->n_pages);
+    }
+    // The first of the wave's keys of tile v.
+    __device__ __forceinline__ int key0(int v) const {
+      return Plain::first_key(it, v, TILE) + first;
+    }
+    __device__ __forceinline__ bool easy(int v) const {
+      const int k = key0(v), end = k + KEYS - 1;
+      return v < it.n_tiles && k >= this->lo && end <= this->last &&
+             (k >= this->near || end < this->sunk) && this->page_shift >= 0;
+    }
     __device__ __forceinline__ int key(int v, int i) const {
-      return v < it.n_tiles ? Plain::first_key(it, v, TILE) + first + i : this->lo;
+      return v < it.n_tiles ? key0(v) + i : this->lo;
     }
     __device__ __forceinline__ void ask(int v, int slot) const {
-      if (this->pages)
-        load4_to_lds(this->place(key(v, lane % KEYS)), ring + (slot & 3) * 256);
+      if (!this->pages) return;
+      lds_u8 *to = ring + (slot & 3) * 256;
+      if (easy(v)) {
+        const uint32_t at = static_cast<uint32_t>(key0(v) + lane % KEYS) >> this->page_shift;
+        load4_to_lds(this->pages + at, to);
+      } else {
+        load4_to_lds(this->place(key(v, lane % KEYS)), to);
+      }
     }
-    // Of key i of the wave's.
-    __device__ __forceinline__ uint64_t row(int v, int slot, int i) const {
-      typedef __attribute__((address_space(3))) int lds_int;
-      return this->offset(key(v, i),
-                          this->pages ? ((const lds_int *)(ring + (slot & 3) * 256))[i] : 0);
+    // Of key i of the wave's: its page's number, and its place.
+    __device__ __forceinline__ uint32_t page(int slot, int i) const {
+      typedef __attribute__((address_space(3))) uint32_t lds_u32;
+      return this->pages ? ((const lds_u32 *)(ring + (slot & 3) * 256))[i] : 0;
+    }
+    __device__ __forceinline__ const uint8_t *row(int v, uint32_t page, int i) const {
+      uint64_t off;
+      if (easy(v) && !__any(page >= this->n_pages && this->pages)) {
+        uint32_t r = key0(v) + i;
+        if (this->pages)
+          r = (page << this->page_shift) | (r & (this->page_rows - 1));
+        off = static_cast<uint64_t>(r) * this->stride;
+      } else {
+        off = this->offset(key(v, i), page);
+      }
+      return this->src + off;
     }
   };
 
@@ -346,16 +438,17 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
   struct NarrowLoader {
     static constexpr int N = 2 * BLOCKS + 1;
     static __device__ __forceinline__ void all(const AttendArgs &a, const AttendItem &it,
-                                               const Source &from, uint64_t off, lds_u8 *tile,
+                                               const uint8_t *own, lds_u8 *tile,
                                                lds_u8 *scales, int lane) {
       const int64_t scale = lane < 32 ? key_scale_at(a, it) : value_scale_at(a, it);
-      gpb::load4_to_lds(from.src + off + (scale & ~3ll), scales);
+      gpb::load4_to_lds(own + (scale & ~3ll), scales);
+      const uint64_t at = reinterpret_cast<uint64_t>(own);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int r = 16 * g + (lane >> 2);
-        const uint32_t lo = __shfl(static_cast<uint32_t>(off), r, 64);
-        const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), r, 64);
-        const uint8_t *row = from.src + (lo | static_cast<uint64_t>(hi) << 32) +
+        const uint32_t lo = __shfl(static_cast<uint32_t>(at), r, 64);
+        const uint32_t hi = __shfl(static_cast<uint32_t>(at >> 32), r, 64);
+        const uint8_t *row = reinterpret_cast<const uint8_t *>(lo | static_cast<uint64_t>(hi) << 32) +
                              ((lane & 3) ^ ((r >> 2) & 3)) * 16;
         blocks<DK / 64>(row + key_at(it), tile + g * 1024);
         blocks<DV / 64>(row + value_at(a, it), tile + DK / 64 * 2048 + g * 1024);
@@ -374,8 +467,9 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
   // after next go out as soon as one has been read.  Page numbers are asked for two
   // tiles before the loads that need them: the wait for the tile between has them.
   template <bool SCAN>
-  static __device__ __forceinline__ bool narrow(const AttendArgs &a, const AttendItem &it,
+  static __device__ __forceinline__ bool narrow(const AttendArgs &args, const AttendItem &it,
                                                 lds_u8 *lds) {
+    const AttendArgs a = kept(args);
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int row = lane & 31, half = lane >> 5;
     constexpr int BUF = kNarrowTile * 64 * BLOCKS;
@@ -394,10 +488,11 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     State st;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
+    const float c = in_vector(a.c);
     const auto load = [&](int v, int n) {
       rows.ask(v + 8, n + 2);
-      NarrowLoader::all(a, it, rows, rows.row(v, n, lane & 31), own + (n & 1) * BUF,
-                        scales + (n & 1) * 256, lane);
+      NarrowLoader::all(a, it, rows.row(v, rows.page(n, lane & 31), lane & 31),
+                        own + (n & 1) * BUF, scales + (n & 1) * 256, lane);
     };
     if (wave < it.n_tiles) {
       typedef __attribute__((address_space(3))) uint32_t lds_u32;
@@ -423,14 +518,18 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
           const uint32_t ks = ((const lds_u32 *)sc)[row] >> key_shift & 255;
           const uint32_t vs = ((const lds_u32 *)sc)[32 + row] >> value_shift & 255;
           lay_scales(scales + 512, lane, vs);
+          KeyAhead<kNarrowTile> keys;
+          keys.read(now, 0, w);
           f32x16 s;
-          products<kNarrowTile>(q, now, 0, w, scale_of(ks), NoLoader(), &s);
+          products<kNarrowTile>(q, now, 0, w, scale_of(ks), keys, NoLoader(), &s);
+          ValueAhead<kNarrowTile, 2, NT> values;
+          values.read(now, 0, w, 0);
           ValueScales by;
           take_scales(scales + 512, half, &by);
-          Plain::take_top(st, top_of(a, it, &s, key0, whole, see, half, by), false);
+          Plain::take_top(st, top_of(a, it, c, &s, key0, whole, see, half, by), false);
           x8 p[2];
-          st.l += weights(s, a.c, st.m, by, p);
-          add_values<kNarrowTile, 2, NT>(p, now, 0, w, 0, &st);
+          st.l += weights(s, c, st.m, by, p);
+          values.template add<0, 2 * NT>(p, now, 0, w, 0, &st, NoLoader());
         }
         lds_reads_done();
         if (v + 8 < it.n_tiles) load(v + 8, n + 2);
@@ -475,30 +574,33 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       if constexpr (I < BLOCKS) gpb::load_to_lds<I * 64>(row + chunk, to + I * kWideTile * 64);
       else if constexpr (I == BLOCKS) gpb::load4_to_lds(row + DV + 2 * (DK - DV), scales);
     }
-    template <int I = 0>
+    template <int I = 0, int END = N>
     __device__ __forceinline__ void all() const {
-      if constexpr (I < N) {
+      if constexpr (I < END) {
         issue<I>();
-        all<I + 1>();
+        all<I + 1, END>();
       }
     }
   };
 
-  // As Attend::latent, over tiles of codes.  Three of them fit, so a tile's loads go
-  // out two tiles ahead.
+  // As Attend::latent, over tiles of codes.  Three of them fit, and the weights that
+  // pass between the waves of a pair have two places, so that one barrier a tile
+  // serves both: behind it the next tile is there, and nobody reads the last one,
+  // whose place the loads of the tile after next take.  What a product needs first
+  // from LDS is asked for before what comes ahead of the product.
   template <bool SCAN>
-  static __device__ __forceinline__ bool latent(const AttendArgs &a, const AttendItem &it,
+  static __device__ __forceinline__ bool latent(const AttendArgs &args, const AttendItem &it,
                                                 lds_u8 *lds) {
+    const AttendArgs a = kept(args);
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int part = wave & 1, half = lane >> 5;
     const int row = (wave >> 1) * 32 + (lane & 31);
     const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
     const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
-    constexpr int BUF = kWideTile * 64 * BLOCKS;
-    static_assert(3 * BUF == SCALES && SCALES + 3072 + 1024 <= TILES_LDS, "room for scales");
-    lds_u8 *mine = lds + TILES_LDS + wave * WAVE_XCHG;
-    const lds_u8 *theirs = lds + TILES_LDS + (wave ^ 1) * WAVE_XCHG;
-    lds_u8 *by_key = lds + SCALES + 3072 + wave * 256;
+    constexpr int BUF = kWideTile * 64 * BLOCKS, BY_KEY = SCALES + 3072, XCHG = BY_KEY + 1024;
+    static_assert(3 * BUF == SCALES && XCHG + 8 * WAVE_XCHG <= TILES_LDS, "room");
+    constexpr int EARLY = 5;  // loads of a tile that go out before its turn begins
+    lds_u8 *by_key = lds + BY_KEY + wave * 256;
     typedef __attribute__((address_space(3))) x8 lds8;
     typedef __attribute__((address_space(3))) float lds_float;
     typedef __attribute__((address_space(3))) uint32_t lds_u32;
@@ -508,8 +610,9 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     State st;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
+    const float c = in_vector(a.c);
     const auto loader = [&](int v, int buf) {
-      return LatentLoader(rows.src + rows.row(v, v, lane >> 2), lds + buf * BUF,
+      return LatentLoader(rows.row(v, rows.page(v, lane >> 2), lane >> 2), lds + buf * BUF,
                           lds + SCALES + buf * 1024, wave, lane);
     };
     if (it.n_tiles > 0) {
@@ -546,38 +649,66 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         asm volatile("" : "+a"(q[d]));
       }
       lds_reads_done();
+      loads_done();
       __syncthreads();
       rows.ask(3, 3);
-      loader(1, 1).all();
-      int buf = 0;
+      LatentLoader load = loader(1, 1);  // of the tile after this one
+      load.template all<0, EARLY>();
+      int buf = 0, odd_turn = 0;
+      KeyAhead<kWideTile> keys;
+      uint32_t scale;
+      const auto begin = [&]() {  // the first reads of the tile in `buf`
+        scale = ((const lds_u32 *)(lds + SCALES + buf * 1024))[(32 * part + (lane & 31)) * 4] & 255;
+        keys.read(lds + buf * BUF, 32 * part, w);
+      };
+      begin();
       loop_aligned();
       for (int v = 0; v < it.n_tiles; ++v) {
-        if (rows.pages) loads_done<LatentLoader::N + 1>();
-        else loads_done<LatentLoader::N>();
-        __syncthreads();
-        const lds_u8 *now = lds + buf * BUF, *sc = lds + SCALES + buf * 1024;
+        const lds_u8 *now = lds + buf * BUF;
+        lds_u8 *mine = lds + XCHG + (odd_turn * 4 + wave) * WAVE_XCHG;
+        const lds_u8 *theirs = lds + XCHG + (odd_turn * 4 + (wave ^ 1)) * WAVE_XCHG;
+        odd_turn ^= 1;
         const int key0 = Plain::first_key(it, v, kWideTile);
-        const bool whole = Plain::whole_tile(a, it, key0, kWideTile);
-        const bool agree = v == 0 || !whole;
-        const bool odd =
-            SCAN && !whole && __syncthreads_or(odd_codes<kWideTile>(now, threadIdx.x, 256));
-        left |= odd;
-        rows.ask(v + 4, v + 4);
-        const LatentLoader load = loader(v + 2, buf == 0 ? 2 : buf - 1);
+        const int after = buf == 0 ? 2 : buf - 1;  // of tile v + 2, and v - 1
         buf = buf == 2 ? 0 : buf + 1;
+        bool whole, odd = false;
+        if constexpr (SCAN) {
+          whole = Plain::whole_tile(a, it, key0, kWideTile);
+          odd = !whole && __syncthreads_or(odd_codes<kWideTile>(now, threadIdx.x, 256));
+          left |= odd;
+        }
         if (odd || idle) {
-          load.all();
-          if (!odd && agree) __syncthreads();
-          if (!odd) __syncthreads();
+          whole = Plain::whole_tile(a, it, key0, kWideTile);
+          load.template all<EARLY>();
+          if (!odd && (v == 0 || !whole)) __syncthreads();
+          load = loader(v + 2, after);
+          rows.ask(v + 4, v + 4);
+          loads_done();
+          __syncthreads();
+          load.template all<0, EARLY>();
+          begin();
           continue;
         }
-        const uint32_t scale = ((const lds_u32 *)sc)[(32 * part + (lane & 31)) * 4] & 255;
-        lay_scales(by_key, lane, scale);
         f32x16 s;
-        products<kWideTile>(q, now, 32 * part, w, scale_of(scale), load, &s);
+        uint32_t page;
+        const uint8_t *next_row;
+        products<kWideTile>(
+            q, now, 32 * part, w, scale_of(scale), keys, beside([&](auto d) {
+              constexpr int D = decltype(d)::value;
+              if constexpr (D % 2 == 0) load.template issue<EARLY + D / 2>();
+              if constexpr (D == 1) lay_scales(by_key, lane, scale);
+              if constexpr (D == 3) page = rows.page(v + 2, lane >> 2);
+              if constexpr (D == 5) whole = Plain::whole_tile(a, it, key0, kWideTile);
+              if constexpr (D == 13) next_row = rows.row(v + 2, page, lane >> 2);
+              if constexpr (D == 15) rows.ask(v + 4, v + 4);
+            }),
+            &s);
+        const bool agree = v == 0 || !whole;
         ValueScales by;
         take_scales(by_key, half, &by);
-        float top = top_of(a, it, &s, key0 + 32 * part, whole, see, half, by);
+        ValueAhead<kWideTile, 2, NT> first;
+        first.read(now, 32 * part, w, part * NT);
+        float top = top_of(a, it, c, &s, key0 + 32 * part, whole, see, half, by);
         if (agree) {
           if (half == 0) ((lds_float *)(mine + 2048 + 128))[lane] = top;
           __syncthreads();
@@ -585,16 +716,21 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         }
         Plain::take_top(st, top, !agree);
         x8 p[2];
-        st.l += weights(s, a.c, st.m, by, p);
+        st.l += weights(s, c, st.m, by, p);
         const float m = st.m;
         ((lds8 *)mine)[lane] = p[0];
         ((lds8 *)mine)[64 + lane] = p[1];
         if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
-        add_values<kWideTile, 2, NT>(p, now, 32 * part, w, part * NT, &st);
+        first.template add<0, 2 * NT - 4>(p, now, 32 * part, w, part * NT, &st, NoLoader());
+        ValueAhead<kWideTile, 2, NT> second;
+        second.read(now, 32 * (1 - part), w, part * NT);
+        loads_done();
         __syncthreads();
-        p[0] = ((const lds8 *)theirs)[lane];
-        p[1] = ((const lds8 *)theirs)[64 + lane];
+        x8 p2[2];
+        p2[0] = ((const lds8 *)theirs)[lane];
+        p2[1] = ((const lds8 *)theirs)[64 + lane];
         const float m2 = ((const lds_float *)(theirs + 2048))[lane & 31];
+        first.template add<2 * NT - 4, 2 * NT>(p, now, 32 * part, w, part * NT, &st, NoLoader());
         if (__any(m2 != m)) {
           const float both = fmaxf(m, m2);
           const float f2 = __builtin_amdgcn_exp2f(m2 - Plain::finite_m(both));
@@ -605,13 +741,23 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              p[b][j] = static_cast<T>(static_cast<float>(p[b][j]) * f2);
+              p2[b][j] = static_cast<T>(static_cast<float>(p2[b][j]) * f2);
         }
-        add_values<kWideTile, 2, NT>(p, now, 32 * (1 - part), w, part * NT, &st);
+        load = LatentLoader(next_row, lds + after * BUF, lds + SCALES + after * 1024, wave, lane);
+        second.template add<0, 2 * NT - 4>(
+            p2, now, 32 * (1 - part), w, part * NT, &st, beside([&](auto i) {
+              constexpr int I = decltype(i)::value;
+              if constexpr (I % 2 == 0 && I / 2 < EARLY) load.template issue<I / 2>();
+            }));
+        begin();
+        second.template add<2 * NT - 4, 2 * NT>(p2, now, 32 * (1 - part), w, part * NT, &st,
+                                                NoLoader());
       }
       loads_done();
     }
     // each wave has summed the weights of its own keys
+    lds_u8 *mine = lds + TILES_LDS + wave * WAVE_XCHG;
+    const lds_u8 *theirs = lds + TILES_LDS + (wave ^ 1) * WAVE_XCHG;
     float l = st.l + other_half(st.l, half);
     __syncthreads();
     ((lds_float *)mine)[lane] = l;
@@ -634,46 +780,71 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
 
   // A wave's share of a tile, 16 keys: its codes come to registers while an earlier
   // tile is worked on, and go to LDS as the values they stand for, to where a tile of
-  // 16-bit rows has them.  Row lane / 4, chunk lane % 4 of 64 bytes at a time.
+  // 16-bit rows has them.  Four lanes have a row, chunk lane % 4 of 64 bytes at a time,
+  // of keys and then of values; the rows are dealt to the lanes so that four of them
+  // next to each other write to all banks (row lane / 4: four writes' time for one).
   struct Share {
-    static constexpr int N0 = DK / 64, N1 = DV / 64;
-    u32x4 raw0[N0], raw1[N1];
+    static constexpr int N0 = DK / 64, N = (DK + DV) / 64;
+    u32x4 raw[N];
     uint32_t scale[2];
+    int i;        // of the wave's 16 rows, the lane's
+    uint32_t to;  // in a tile, of the lane's first chunk
 
+    __device__ __forceinline__ Share(int wave, int lane) {
+      const int b0 = lane >> 2 & 1, b1 = lane >> 3 & 1, b2 = lane >> 4 & 1, b3 = lane >> 5;
+      i = R0 % 256 ? b0 | b1 << 2 | b2 << 1 | b3 << 3 : b0 << 3 | b1 << 1 | b2 | b3 << 2;
+      const int row = wave * 16 + i;
+      to = row * R0 + place_of<R0>(row, lane % 4 * 2) * 16;
+    }
+    template <int J>
     __device__ __forceinline__ void ask(const AttendArgs &a, const AttendItem &it,
                                         const uint8_t *row, int lane) {
-      const uint8_t *from = row + lane % 4 * 16;
-#pragma unroll
-      for (int j = 0; j < N0; ++j)
-        raw0[j] = *reinterpret_cast<const u32x4 *>(from + key_at(it) + 64 * j);
-#pragma unroll
-      for (int j = 0; j < N1; ++j)
-        raw1[j] = *reinterpret_cast<const u32x4 *>(from + value_at(a, it) + 64 * j);
-      scale[0] = row[key_scale_at(a, it)];
-      scale[1] = row[value_scale_at(a, it)];
+      // (said to be global memory, which `keep` has made the compiler forget)
+      typedef const __attribute__((address_space(1))) u32x4 global16;
+      const int64_t at = J < N0 ? key_at(it) + 64 * J : value_at(a, it) + 64 * (J - N0);
+      raw[J] = *(global16 *)(row + at + lane % 4 * 16);
     }
-    __device__ __forceinline__ void put(lds_u8 *tile, int wave, int lane) const {
+    __device__ __forceinline__ void ask_scales(const AttendArgs &a, const AttendItem &it,
+                                               const uint8_t *row) {
+      typedef const __attribute__((address_space(1))) uint8_t global1;
+      scale[0] = *(global1 *)(row + key_scale_at(a, it));
+      scale[1] = *(global1 *)(row + value_scale_at(a, it));
+    }
+    // (place_of is an exclusive or of what row and chunk give)
+    template <int J>
+    __device__ __forceinline__ void put(lds_u8 *tile) const {
       typedef __attribute__((address_space(3))) x8 lds8;
-      const int row = wave * 16 + lane / 4;
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const float f = scale_of(scale[part]);
-        lds_u8 *to = tile + (part ? kWideTile * R0 + row * R1 : row * R0);
-#pragma unroll
-        for (int j = 0; j < (part ? N1 : N0); ++j) {
-          const u32x4 raw = part ? raw1[j] : raw0[j];
-          const int c = lane % 4 * 2 + 8 * j;
-          *(lds8 *)(to + place_of<R0>(row, c) * 16) = values8<T>(u32x2{raw[0], raw[1]}, f);
-          *(lds8 *)(to + place_of<R0>(row, c + 1) * 16) = values8<T>(u32x2{raw[2], raw[3]}, f);
-        }
-      }
+      constexpr int C = 8 * (J < N0 ? J : J - N0);
+      const float f = scale_of(scale[J < N0 ? 0 : 1]);
+      lds_u8 *at = tile + (J < N0 ? 0 : kWideTile * R0);
+      *(lds8 *)(at + (to ^ place_of<R0>(0, C) * 16)) = values8<T>(u32x2{raw[J][0], raw[J][1]}, f);
+      *(lds8 *)(at + (to ^ place_of<R0>(0, C + 1) * 16)) =
+          values8<T>(u32x2{raw[J][2], raw[J][3]}, f);
     }
   };
 
+  // As Attend::thirty_two: parts 4 B .. of what runs beside, two with each product.
+  template <int B, int RH, typename L>
+  static __device__ __forceinline__ void thirty_two(const AttendArgs &a, const AttendItem &it,
+                                                    const x8 *q, const lds_u8 *now,
+                                                    const typename Plain::Places &w, int key0,
+                                                    bool whole, const Sight *see, State *st,
+                                                    int half, const L &parts) {
+    f32x16 s[RH];
+    Plain::template products<kWideTile, 4 * B, 2, RH>(q, now, 32 * B, w, parts, s);
+    x8 p[2 * RH];
+#pragma unroll
+    for (int r = 0; r < RH; ++r)
+      Plain::template weigh<1>(a, it, s + r, key0 + 32 * B, whole, see[r], st[r], half, p + 2 * r);
+    Plain::template add_values<2, NT, 4 * B + 2, RH>(p, now + kWideTile * R0 + 32 * B * R1, w, 0, st,
+                                                     parts);
+  }
+
   // As Attend::wide.
   template <bool SCAN>
-  static __device__ __forceinline__ bool wide(const AttendArgs &a, const AttendItem &it,
+  static __device__ __forceinline__ bool wide(const AttendArgs &args, const AttendItem &it,
                                               lds_u8 *lds) {
+    const AttendArgs a = kept(args);
     constexpr int RH = kRows / 128, BUF = kWideTile * ROW;
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int row = wave * 32 * RH + (lane & 31), half = lane >> 5;
@@ -697,49 +868,75 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     Plain::find_places(w, lane);
     bool left = false;  // SCAN: a tile is left to `careful`
     if (it.n_tiles > 0) {
-      Share share;
-      const auto ask = [&](int v) {
-        share.ask(a, it, rows.src + rows.row(v, v, lane >> 2), lane);
-        rows.ask(v + 2, v + 2);
+      Share share(wave, lane);
+      const uint8_t *row_at;
+      lds_u8 *to;
+      // What runs beside a tile's products, in eight parts: the next tile goes to LDS,
+      // then the loads of the one after it go out.
+      int next_v = 0;
+      const auto part = [&](auto i) {
+        constexpr int I = decltype(i)::value, M = Share::N / 2;
+        if constexpr (I < M) {
+          share.template put<2 * I>(to);
+          share.template put<2 * I + 1>(to);
+        }
+        if constexpr (I == 2) {
+          loads_done();  // (the page numbers, asked for behind the rows)
+          row_at = rows.row(next_v + 1, rows.page(next_v + 1, share.i), share.i);
+        }
+        if constexpr (I == 3) share.ask_scales(a, it, row_at);
+        if constexpr (I >= 4 && I < 4 + M) {
+          share.template ask<2 * (I - 4)>(a, it, row_at, lane);
+          share.template ask<2 * (I - 4) + 1>(a, it, row_at, lane);
+        }
+        if constexpr (I == 7) rows.ask(next_v + 3, next_v + 3);
+      };
+      const auto all_parts = [&]() {
+        part(std::integral_constant<int, 0>());
+        part(std::integral_constant<int, 1>());
+        part(std::integral_constant<int, 2>());
+        part(std::integral_constant<int, 3>());
+        part(std::integral_constant<int, 4>());
+        part(std::integral_constant<int, 5>());
+        part(std::integral_constant<int, 6>());
+        part(std::integral_constant<int, 7>());
       };
       loads_done();
-      ask(0);
-      share.put(lds, wave, lane);
-      ask(1);
+      row_at = rows.row(0, rows.page(0, share.i), share.i);
+      share.ask_scales(a, it, row_at);
+      part(std::integral_constant<int, 4>());
+      part(std::integral_constant<int, 5>());
+      rows.ask(2, 2);
+      to = lds;
+      all_parts();
       lds_reads_done();
       loop_aligned();
       for (int v = 0; v < it.n_tiles; ++v) {
         __syncthreads();
         lds_u8 *now = lds + (v & 1) * BUF;
+        to = lds + (~v & 1) * BUF;
+        next_v = v + 1;
         const int key0 = Plain::first_key(it, v, kWideTile);
         const bool whole = Plain::whole_tile(a, it, key0, kWideTile);
         const bool odd =
             SCAN && !whole &&
             __syncthreads_or(Plain::template odd_values<kWideTile>(now, threadIdx.x, 256));
         left |= odd;
-        const auto next = [&]() {
-          share.put(lds + (~v & 1) * BUF, wave, lane);
-          loads_done();  // (the page numbers of tile v + 2)
-          ask(v + 2);
-        };
         if (odd || idle) {
-          next();
+          all_parts();
           continue;
         }
         if constexpr (RH == 1) {
           f32x16 s[2];
-          Plain::template products<kWideTile, 0, 2>(q, now, 0, w, NoLoader(), s);
-          Plain::template products<kWideTile, DK / 32, 2>(q, now, 32, w, NoLoader(), s + 1);
+          Plain::template products<kWideTile, 0, 2>(q, now, 0, w, beside(part), s);
+          Plain::template products<kWideTile, DK / 32, 2>(q, now, 32, w, beside(part), s + 1);
           x8 p[4];
           Plain::template weigh<2>(a, it, s, key0, whole, see[0], st[0], half, p);
-          next();
           Plain::template add_values<4, NT, 0>(p, now + kWideTile * R0, w, 0, st, NoLoader());
         } else {
-          Plain::template thirty_two<0, RH>(a, it, q, now, w, key0, whole, see, st, half,
-                                            NoLoader());
-          next();
-          Plain::template thirty_two<1, RH>(a, it, q, now, w, key0, whole, see, st, half,
-                                            NoLoader());
+          // (of 64-wide heads a product has four steps, and a tile four products)
+          thirty_two<0, RH>(a, it, q, now, w, key0, whole, see, st, half, beside(part));
+          thirty_two<1, RH>(a, it, q, now, w, key0, whole, see, st, half, beside(part));
         }
       }
       loads_done();
