@@ -430,6 +430,57 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     }
   };
 
+  // The rows of a wave's 16 keys of wide tiles.  The page numbers and the places of four
+  // tiles are found at once, a key to a lane: finding them takes some 70 instructions,
+  // which every tile paid for before.  (FOUR_FIGURE)
+  struct FourTiles : Source {
+    const AttendItem &it;
+    lds_u8 *ring;
+    int first, lane;
+    uint64_t off;  // of key lane % 16 of tile 4 b + lane / 16
+
+    __device__ __forceinline__ FourTiles(const AttendArgs &a, const AttendItem &it, lds_u8 *lds,
+                                         int wave, int lane)
+        : Source(a, it), it(it), ring(lds + RING + wave * 1024), first(wave * 16), lane(lane) {
+      keep(this->src);
+      keep(this->pages);
+      keep(this->status);
+      keep(this->stride);
+      keep(this->page_rows);
+      keep(this->page_shift);
+      keep(this->n_pages);
+    }
+    __device__ __forceinline__ int key(int b) const {
+      const int v = 4 * b + (lane >> 4);
+      return v < it.n_tiles ? Plain::first_key(it, v, kWideTile) + first + (lane & 15) : this->lo;
+    }
+    __device__ __forceinline__ void ask(int b) const {
+      if (this->pages) load4_to_lds(this->place(key(b)), ring);
+    }
+    __device__ __forceinline__ void find(int b) {
+      typedef __attribute__((address_space(3))) uint32_t lds_u32;
+      off = this->offset(key(b), this->pages ? ((const lds_u32 *)ring)[lane] : 0);
+    }
+    // Of key i of tile v, one of the four.
+    __device__ __forceinline__ const uint8_t *row(int v, int i) const {
+      const int from = (v & 3) * 16 + i;
+      const uint32_t lo = __shfl(static_cast<uint32_t>(off), from, 64);
+      const uint32_t hi = __shfl(static_cast<uint32_t>(off >> 32), from, 64);
+      return this->src + (lo | static_cast<uint64_t>(hi) << 32);
+    }
+    // Tile v's turn: the row of tile v + 2, and every fourth time the work for the next
+    // four.  `asked` comes before the tile's wait for loads, which is before `found`
+    // of the next.
+    __device__ __forceinline__ void asked(int v) const {
+      if ((v & 3) == 0) ask(v / 4 + 1);
+    }
+    __device__ __forceinline__ const uint8_t *found(int v, int i) {
+      const uint8_t *r = row(v + 2, i);
+      if ((v & 3) == 1) find(v / 4 + 1);
+      return r;
+    }
+  };
+
   // ---- narrow items
 
   // The loads of a wave's tile of 32 keys: rows lane / 4 and 16 + lane / 4, chunk
@@ -595,7 +646,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int part = wave & 1, half = lane >> 5;
     const int row = (wave >> 1) * 32 + (lane & 31);
-    const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
+    FourTiles rows(a, it, lds, wave, lane);
     const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
     constexpr int BUF = kWideTile * 64 * BLOCKS, BY_KEY = SCALES + 3072, XCHG = BY_KEY + 1024;
     static_assert(3 * BUF == SCALES && XCHG + 8 * WAVE_XCHG <= TILES_LDS, "room");
@@ -611,14 +662,12 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
     const float c = in_vector(a.c);
-    const auto loader = [&](int v, int buf) {
-      return LatentLoader(rows.row(v, rows.page(v, lane >> 2), lane >> 2), lds + buf * BUF,
-                          lds + SCALES + buf * 1024, wave, lane);
+    const auto loader = [&](const uint8_t *row, int buf) {
+      return LatentLoader(row, lds + buf * BUF, lds + SCALES + buf * 1024, wave, lane);
     };
     if (it.n_tiles > 0) {
       typedef typename Plain::template Loader<kWideTile, 4> Queries;
-      rows.ask(0, 0);
-      rows.ask(1, 1);
+      rows.ask(0);
       {
         // the queries come as a tile of 16-bit rows, behind the first tile
         const int g = it.row0 + min(wave * 16 + (lane & 15), it.n_rows - 1);
@@ -628,10 +677,9 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
             .all();
       }
       loads_done<Queries::N>();
-      rows.ask(2, 2);
-      loader(0, 0).all();
-      if (rows.pages) loads_done<LatentLoader::N + 1>();
-      else loads_done<LatentLoader::N>();
+      rows.find(0);
+      loader(rows.row(0, lane >> 2), 0).all();
+      loads_done<LatentLoader::N>();
       __syncthreads();
       const int n = 32 * (wave >> 1) + (lane & 31);
       static_assert(BUF + kWideTile * ROW <= TILES_LDS, "room for the queries");
@@ -651,8 +699,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       lds_reads_done();
       loads_done();
       __syncthreads();
-      rows.ask(3, 3);
-      LatentLoader load = loader(1, 1);  // of the tile after this one
+      LatentLoader load = loader(rows.row(1, lane >> 2), 1);  // of the tile after this one
       load.template all<0, EARLY>();
       int buf = 0, odd_turn = 0;
       KeyAhead<kWideTile> keys;
@@ -681,8 +728,8 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
           whole = Plain::whole_tile(a, it, key0, kWideTile);
           load.template all<EARLY>();
           if (!odd && (v == 0 || !whole)) __syncthreads();
-          load = loader(v + 2, after);
-          rows.ask(v + 4, v + 4);
+          load = loader(rows.found(v, lane >> 2), after);
+          rows.asked(v);
           loads_done();
           __syncthreads();
           load.template all<0, EARLY>();
@@ -690,17 +737,15 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
           continue;
         }
         f32x16 s;
-        uint32_t page;
         const uint8_t *next_row;
         products<kWideTile>(
             q, now, 32 * part, w, scale_of(scale), keys, beside([&](auto d) {
               constexpr int D = decltype(d)::value;
               if constexpr (D % 2 == 0) load.template issue<EARLY + D / 2>();
               if constexpr (D == 1) lay_scales(by_key, lane, scale);
-              if constexpr (D == 3) page = rows.page(v + 2, lane >> 2);
               if constexpr (D == 5) whole = Plain::whole_tile(a, it, key0, kWideTile);
-              if constexpr (D == 13) next_row = rows.row(v + 2, page, lane >> 2);
-              if constexpr (D == 15) rows.ask(v + 4, v + 4);
+              if constexpr (D == 13) next_row = rows.found(v, lane >> 2);
+              if constexpr (D == 15) rows.asked(v);
             }),
             &s);
         const bool agree = v == 0 || !whole;
@@ -743,7 +788,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
             for (int j = 0; j < 8; ++j)
               p2[b][j] = static_cast<T>(static_cast<float>(p2[b][j]) * f2);
         }
-        load = LatentLoader(next_row, lds + after * BUF, lds + SCALES + after * 1024, wave, lane);
+        load = loader(next_row, after);
         second.template add<0, 2 * NT - 4>(
             p2, now, 32 * (1 - part), w, part * NT, &st, beside([&](auto i) {
               constexpr int I = decltype(i)::value;
@@ -849,11 +894,8 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int row = wave * 32 * RH + (lane & 31), half = lane >> 5;
     const bool idle = wave * 32 * RH >= it.n_rows;  // a wave without rows only loads
-    const Rows<kWideTile, kWideTile / 4> rows(a, it, lds, wave, lane);
-    if (it.n_tiles > 0) {
-      rows.ask(0, 0);
-      rows.ask(1, 1);
-    }
+    FourTiles rows(a, it, lds, wave, lane);
+    if (it.n_tiles > 0) rows.ask(0);
     x8 q[RH * (DK / 16)];
     Sight see[RH];
     State st[RH];
@@ -882,14 +924,14 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         }
         if constexpr (I == 2) {
           loads_done();  // (the page numbers, asked for behind the rows)
-          row_at = rows.row(next_v + 1, rows.page(next_v + 1, share.i), share.i);
+          row_at = next_v == 0 ? rows.row(1, share.i) : rows.found(next_v - 1, share.i);
         }
         if constexpr (I == 3) share.ask_scales(a, it, row_at);
         if constexpr (I >= 4 && I < 4 + M) {
           share.template ask<2 * (I - 4)>(a, it, row_at, lane);
           share.template ask<2 * (I - 4) + 1>(a, it, row_at, lane);
         }
-        if constexpr (I == 7) rows.ask(next_v + 3, next_v + 3);
+        if constexpr (I == 7) rows.asked(next_v - 1);
       };
       const auto all_parts = [&]() {
         part(std::integral_constant<int, 0>());
@@ -902,11 +944,11 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         part(std::integral_constant<int, 7>());
       };
       loads_done();
-      row_at = rows.row(0, rows.page(0, share.i), share.i);
+      rows.find(0);
+      row_at = rows.row(0, share.i);
       share.ask_scales(a, it, row_at);
       part(std::integral_constant<int, 4>());
       part(std::integral_constant<int, 5>());
-      rows.ask(2, 2);
       to = lds;
       all_parts();
       lds_reads_done();
