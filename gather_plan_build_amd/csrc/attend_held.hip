@@ -44,6 +44,10 @@ __device__ __forceinline__ void load4_to_lds(const uint8_t *from, lds_u8 *to) {
 // the wait for it is one for all that LDS owes as well.  What it then has to lay
 // aside goes to a vector register's lanes, without a wait.  44,600 queries over
 // latent rows: PINNED_FIGURE.
+//
+// Not of a pointer that is read or written through: the compiler would forget that
+// it is one to global memory, and an access to any memory may be one to LDS, so that
+// every wait for LDS becomes one for all of it.
 template <typename V>
 __device__ __forceinline__ void keep(V &x) {
   asm volatile("" : "+s"(x));
@@ -383,7 +387,6 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
           first(TILE == KEYS ? 0 : wave * KEYS), lane(lane) {
       keep(this->src);
       keep(this->pages);
-      keep(this->status);
       keep(this->stride);
       keep(this->page_rows);
       keep(this->page_shift);
@@ -444,7 +447,6 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         : Source(a, it), it(it), ring(lds + RING + wave * 1024), first(wave * 16), lane(lane) {
       keep(this->src);
       keep(this->pages);
-      keep(this->status);
       keep(this->stride);
       keep(this->page_rows);
       keep(this->page_shift);
@@ -709,6 +711,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         keys.read(lds + buf * BUF, 32 * part, w);
       };
       begin();
+      lds_reads_done();
       loop_aligned();
       for (int v = 0; v < it.n_tiles; ++v) {
         const lds_u8 *now = lds + buf * BUF;
