@@ -401,6 +401,37 @@ def test_scales_far_apart(which, hkv, hq, dtype):
     b.check()
 
 
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 14), ("128", 2, 8), ("latent", 1, 16)])
+@pytest.mark.parametrize("dtype,size", [("bf16", 2.0 ** -97), ("bf16", 2.0 ** 110),
+                                        ("fp16", 2.0 ** -12), ("fp16", 2.0 ** 11)])
+@pytest.mark.parametrize("q,kv", [([1, 2], [700, 300]), ([90], [500])])
+def test_scales_at_both_ends(which, hkv, hq, dtype, size, q, kv):
+    """Values near the least and the largest scale; queries so small or large that the
+    scores stay ordinary (of latent rows, whose values are keys too)."""
+    f = fmt(which, dtype, hkv)
+    b = HeldBatch(f, hq, q, kv)
+    key = 0.25 / size if f.values_in_key and dtype == "fp16" else 1.0 / size
+    if f.values_in_key:
+        b.q[..., :512] = (b.q[..., :512].double() * key).to(f.dtype)
+    for r in range(len(kv)):
+        x = normal(70 + r, *b.rows[r].shape, dtype=f.dtype).double()
+        at = f.n_kv_heads * f.k_dim
+        if f.values_in_key:
+            x[:, :512] *= size
+        else:
+            x[:, at:] *= size
+        k = x[:, :at].unflatten(1, (f.n_kv_heads, f.k_dim)).to(f.dtype)
+        v = None if f.values_in_key else x[:, at:].unflatten(1, (f.n_kv_heads, f.v_dim)).to(f.dtype)
+        rows = held_rows(f, k, v)
+        b.rows[r] = plain_rows(f, rows)
+        base = int(b.k_bases[r])
+        b.dense[base:base + len(rows)] = rows
+        for i, p in enumerate(b.lists[r]):
+            part = rows[i * 64:(i + 1) * 64]
+            b.pool[p * 64:p * 64 + len(part)] = part
+    b.check()
+
+
 @pytest.mark.parametrize("which", ["64", "128"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("q,kv,window,sinks,at", [
