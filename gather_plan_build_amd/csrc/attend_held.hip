@@ -43,11 +43,12 @@ __device__ __forceinline__ void load4_to_lds(const uint8_t *from, lds_u8 *to) {
 // compiler, short of scalar registers, asks for the argument again in the loop, and
 // the wait for it is one for all that LDS owes as well.  What it then has to lay
 // aside goes to a vector register's lanes, without a wait.  44,600 queries over
-// latent rows: PINNED_FIGURE.
+// latent rows: 25.6 ms, 25.8 without.
 //
 // Not of a pointer that is read or written through: the compiler would forget that
 // it is one to global memory, and an access to any memory may be one to LDS, so that
-// every wait for LDS becomes one for all of it.
+// every wait for LDS becomes one for all of it (26.2 ms against 25.1 with waits that
+// count).
 template <typename V>
 __device__ __forceinline__ void keep(V &x) {
   asm volatile("" : "+s"(x));
@@ -331,12 +332,6 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       }
     }
   }
-  // In a vector register, where the loops have room for it: else they ask for the
-  // argument again and wait.
-  static __device__ __forceinline__ float in_vector(float x) {
-    asm volatile("" : "+v"(x));
-    return x;
-  }
   // The scores of 32 keys, masked, to units of log2 (fp16: with their scales); returns
   // the largest.
   static __device__ __forceinline__ float top_of(const AttendArgs &a, const AttendItem &it,
@@ -434,8 +429,10 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
   };
 
   // The rows of a wave's 16 keys of wide tiles.  The page numbers and the places of four
-  // tiles are found at once, a key to a lane: finding them takes some 70 instructions,
-  // which every tile paid for before.  (FOUR_FIGURE)
+  // tiles are found at once, a key to a lane: finding them takes some 70 instructions.
+  // 2,723 queries of 128-wide heads, a tile at a time and so: 375 and 351 us; 32
+  // requests behind one prefix: 65 and 60 us; 44,600 queries over latent rows: 26.7
+  // and 26.2 ms.
   struct FourTiles : Source {
     const AttendItem &it;
     lds_u8 *ring;
@@ -541,7 +538,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     State st;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
-    const float c = in_vector(a.c);
+    const float c = a.c;
     const auto load = [&](int v, int n) {
       rows.ask(v + 8, n + 2);
       NarrowLoader::all(a, it, rows.row(v, rows.page(n, lane & 31), lane & 31),
@@ -663,7 +660,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     State st;
     st.clear();
     bool left = false;  // SCAN: a tile is left to `careful`
-    const float c = in_vector(a.c);
+    const float c = a.c;
     const auto loader = [&](const uint8_t *row, int buf) {
       return LatentLoader(row, lds + buf * BUF, lds + SCALES + buf * 1024, wave, lane);
     };
