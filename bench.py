@@ -88,13 +88,13 @@ def _elf_section(data, name):
     return None
 
 
-_OTHER_KERNELS = (b"k_row_append", b"k_attend")
+_OTHER_KERNELS = (b"k_row_append", b"k_rows_read", b"k_attend")
 
 
 def _kernel_digest(lib=None):
     """Digest of the machine code of the library's gfx950 compose kernels: the
     .text of every gfx950 code object in its offload bundles, but for those of
-    the row append and the attention, which no counter here is taken on.  It
+    row append, row read and attention, which no counter here is taken on.  It
     changes when a kernel's code does and not when only host code or comments
     do, so the counters stay attached to the kernels they were taken on."""
     import struct

@@ -202,3 +202,26 @@ def test_rows_of_the_reference(f):
     assert ((x.double() - want.double()).abs() <= 0.07 * want.double().abs() + 0.02).all()
     if v is None:
         assert torch.equal(x[:, f.v_dim:], want[:, f.v_dim:])
+
+
+def test_the_compose_counters_do_not_depend_on_row_kernels():
+    """The digest that ties the compose's counters to its kernels leaves out each code
+    object of kernels that make, read or attend rows."""
+    import glob
+    import os
+    import re
+
+    import bench
+    src = os.path.join(os.path.dirname(B.__file__), "csrc")
+    seen = 0
+    for path in glob.glob(os.path.join(src, "*.hip")):
+        with open(path) as f:
+            text = f.read()
+        if not re.search(r'#include "(held|append|attend_kernel)\.h"', text):
+            continue
+        text += open(os.path.join(src, "attend_kernel.h")).read() if "attend_kernel.h" in text else ""
+        names = re.findall(r"__global__[^;{]*?\b(k_\w+)\(", text)
+        assert names
+        assert all(any(k.decode() in n for k in bench._OTHER_KERNELS) for n in names), names
+        seen += 1
+    assert seen >= 4
