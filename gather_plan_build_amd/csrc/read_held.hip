@@ -4,7 +4,9 @@
 // rounding.  Bound by HBM: a held row is read once, a plain one, twice as long,
 // written once.  A lane takes eight codes, so that its 16 bytes of result are next
 // to its neighbour's; a workgroup takes some rows, the chunks of all of them
-// numbered through.
+// numbered through.  217,280 latent rows (143 MB to 250): 68 us repeated without
+// pause, 5.7 TB/s.  72 with plain stores, 74 and 70 with eight and two chunks of a
+// lane under way, 68 with the divisions as products.
 #include "held.h"
 
 namespace gpb {
