@@ -219,7 +219,8 @@ EXPORTS = ("gpb_plan_sizes", "gpb_plan_build", "gpb_plan_build_clear",
            "gpb_compose_consume_fill", "gpb_compose_layer_ahead_fill",
            "gpb_current_row_fill", "gpb_current_row_scatter_groups",
            "gpb_compose_gather_groups", "gpb_compose_layer_groups", "gpb_row_append",
-           "gpb_rows_read", "gpb_attend_plan_build", "gpb_attend_dense", "gpb_attend_paged", "gpb_strerror")
+           "gpb_rows_read", "gpb_attend_plan_build", "gpb_attend_dense", "gpb_attend_paged",
+           "gpb_strerror")
 
 lib = _load(LIB_PATH)
 

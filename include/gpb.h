@@ -575,7 +575,7 @@ int gpb_compose_layer_noalloc(void *d_dense, const gpb_sources *pools, int32_t n
  * values.  With values_in_key = 1 the row is one key head (n_kv_heads = 1)
  * whose first v_dim values are the value (a latent row).  row_bytes is the
  * distance between rows, a multiple of 16, at least the payload; bytes past
- * the payload belong to the caller and are neither read nor written.  k_dim
+ * the payload belong to the caller and are neither used nor written.  k_dim
  * and v_dim are multiples of 8, at most 1024.
  *
  * With GPB_HELD_E4M3 the row holds a byte for a value: the codes of the key
