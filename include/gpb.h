@@ -582,16 +582,16 @@ int gpb_compose_layer_noalloc(void *d_dense, const gpb_sources *pools, int32_t n
  * heads, then those of the value heads, then one scale byte for each key head
  * and one for each value head.  With values_in_key it holds the codes of the
  * value (the key's first v_dim values), then the key's other k_dim - v_dim
- * values in the row's type, then one scale byte.  A code is an e4m3 number c (a
- * sign, four bits of exponent with bias 7, three of fraction; no infinity, NaN
- * 0x7f and 0xff) and stands for c * 2^(scale - 127).  The scale of a head's values x is
- * the least power of two with which no |x| passes 448, but at least 2^-100
- * (bf16) or 2^-15 (fp16), and the codes are x / scale rounded to nearest, ties
- * to even; |x| beyond 240 * 2^120 or 240 * 2^8, infinity among them, is held as
- * that, and NaN as NaN, which does not count for the scale.  A value so held
- * stands for a number of the row's type, is off by at most 2^-4 of itself or
- * 2^-10 scales, and is exactly what every reader takes it for; what bytes stand
- * for whose scale no append makes is not specified. */
+ * values in the row's type, then one scale byte.  A code is an e4m3 number c
+ * (a sign, four bits of exponent with bias 7, three of fraction; no infinity,
+ * NaN 0x7f and 0xff) and stands for c * 2^(scale - 127).  The scale of a
+ * head's values x is the least power of two with which no |x| passes 448, but
+ * at least 2^-100 (bf16) or 2^-15 (fp16), and the codes are x / scale rounded
+ * to nearest, ties to even; |x| beyond 240 * 2^120 or 240 * 2^8, infinity
+ * among them, is held as that, and NaN as NaN, which does not count for the
+ * scale.  A value so held stands for a number of the row's type, is off by at
+ * most 2^-4 of itself or 2^-10 scales, and is exactly what every reader takes
+ * it for; what bytes stand for whose scale no append makes is not specified. */
 typedef struct gpb_row_format {
   int32_t dtype;                /* GPB_BF16 or GPB_FP16, + GPB_HELD_E4M3       */
   int32_t n_kv_heads;           /* 1 .. 1024                                   */
