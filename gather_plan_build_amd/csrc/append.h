@@ -44,23 +44,31 @@ __device__ __forceinline__ void store16(uint8_t *p, u32x4 v) {
   __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
 }
 
-// Cosines and sines of the token's pairs into LDS, for all its heads; all of the
-// workgroup has them when this returns.
-__device__ __forceinline__ void find_turns(const AppendArgs &a, int64_t t, float *s_cos,
+// Cosines and sines of the token's pairs into LDS, for all its heads, behind the next
+// barrier; lane `id` of the workgroup begins with pair id.  T is the type they are
+// taken in: with double they are rounded once, with float the angle is as well.
+template <typename T>
+__device__ __forceinline__ void find_turns(const AppendArgs &a, int64_t t, int id, float *s_cos,
                                            float *s_sin) {
-  for (int i = threadIdx.x; i < a.pairs; i += kBlock) {
+  for (int i = id; i < a.pairs; i += kBlock) {
     int axis = 0;
 #pragma unroll
     for (int x = 0; x < GPB_MAX_AXES - 1; ++x) axis += i >= a.axis_end[x];
     const double pos = a.positions[axis * a.positions_stride + t];
     double turns = pos * (static_cast<double>(a.inv_freq[i]) * 0.15915494309189533577);
     turns -= __builtin_rint(turns);
-    float sn, cs;
-    sincospif(static_cast<float>(2.0 * turns), &sn, &cs);
-    s_cos[i] = cs;
-    s_sin[i] = sn;
+    if constexpr (__is_same(T, double)) {
+      double sn, cs;
+      sincospi(2.0 * turns, &sn, &cs);
+      s_cos[i] = static_cast<float>(cs);
+      s_sin[i] = static_cast<float>(sn);
+    } else {
+      float sn, cs;
+      sincospif(static_cast<float>(2.0 * turns), &sn, &cs);
+      s_cos[i] = cs;
+      s_sin[i] = sn;
+    }
   }
-  __syncthreads();
 }
 
 // Unit j of a key or query head at src: two chunks of pairs whose halves lie

@@ -27,7 +27,8 @@ template <typename T>
 __global__ __launch_bounds__(kBlock) void k_row_append(AppendArgs a) {
   __shared__ __attribute__((aligned(16))) float s_cos[kMaxPairs], s_sin[kMaxPairs];
   const int64_t t = blockIdx.x;
-  find_turns(a, t, s_cos, s_sin);
+  find_turns<float>(a, t, threadIdx.x, s_cos, s_sin);
+  __syncthreads();
   const int64_t loc = a.locs ? a.locs[t] : -1;
   const bool stored = loc >= 0 && loc < a.n_pool_rows;
   if (a.locs && !stored && loc != -1 && threadIdx.x == 0 && a.status)

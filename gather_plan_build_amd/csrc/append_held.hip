@@ -1,8 +1,12 @@
 // append_held.hip -- cache rows held in 8 bits, made from keys and values
 // (gfx950).
 //
-// The turns are those of k_row_append, computed in fp32; a turned key is not
-// rounded to the row's type on its way: the code is the one rounding.  A head's
+// The turns are computed in fp32, and a turned key is not rounded to the row's type
+// on its way: the code is the one rounding.  Where codes are turned their sines come
+// from 64 bits: a code is an eighth of its value away from the next, so one on the
+// wrong side of the middle is far off, and of 6,144,000 there were 20 with the sines
+// of a 32-bit angle and 12 so, which is what fp32 products leave.  Queries and values
+// in 16 bits have k_row_append's sines, and so its very bits.  A head's
 // values share a scale, the least power of two 2^e with max |x| <= 448 2^e,
 // found by an exchange between the lanes that hold them; x 2^-e is exact, and
 // the conversion to e4m3 rounds it to nearest, ties to even.
@@ -13,9 +17,10 @@
 // start of a wave, so that the exchange has all its lanes.  A lane whose pairs'
 // other halves are with another lane reads those again, which the caches hold.
 // Queries, and a latent's values in 16 bits, go as in the plain append.  44,600
-// latent rows to the pool and packed, 16 query heads: 1.75 GB in 299 us, 5.9 TB/s;
-// 4,099 tokens of 28 + 4 + 4 heads of 64: 14.0 us, 2.6 TB/s, of which 12.4 on the
-// GPU; eight tokens: 4.9 us there.
+// latent rows to the pool and packed, 16 query heads: 1.75 GB in 298 us, 5.9 TB/s;
+// 4,099 tokens of 28 + 4 + 4 heads of 64: 14.0 us a call, 13.4 on the GPU (12.5
+// without sines in 64 bits, 14.1 with both kinds by the same waves); eight tokens:
+// 4.6 us there.
 #include "append.h"
 #include "held.h"
 
@@ -63,8 +68,12 @@ __device__ __forceinline__ f32x8 turned8(const AppendArgs &a, const uint16_t *sr
 template <typename T>
 __global__ __launch_bounds__(kBlock) void k_row_append_held(AppendArgs a, HeldArgs h) {
   __shared__ __attribute__((aligned(16))) float s_cos[kMaxPairs], s_sin[kMaxPairs];
+  __shared__ __attribute__((aligned(16))) float c_cos[kMaxPairs], c_sin[kMaxPairs];
   const int64_t t = blockIdx.x;
-  find_turns(a, t, s_cos, s_sin);
+  find_turns<float>(a, t, threadIdx.x, s_cos, s_sin);
+  if (a.rot_start < h.k_codes)  // (beside them, by other waves if there are few pairs)
+    find_turns<double>(a, t, (threadIdx.x + kBlock / 2) % kBlock, c_cos, c_sin);
+  __syncthreads();
   const int64_t loc = a.locs ? a.locs[t] : -1;
   const bool stored = loc >= 0 && loc < a.n_pool_rows;
   if (a.locs && !stored && loc != -1 && threadIdx.x == 0 && a.status)
@@ -83,8 +92,8 @@ __global__ __launch_bounds__(kBlock) void k_row_append_held(AppendArgs a, HeldAr
       f32x8 lo = {}, hi = {};
       if (key) {
         const uint16_t *src = a.k + t * a.k_ts + head * a.k_hs;
-        if (one) lo = turned8<T>(a, src, e, s_cos, s_sin);
-        if (two) hi = turned8<T>(a, src, e + 8, s_cos, s_sin);
+        if (one) lo = turned8<T>(a, src, e, c_cos, c_sin);
+        if (two) hi = turned8<T>(a, src, e + 8, c_cos, c_sin);
       } else {
         const uint16_t *src = a.v + t * a.v_ts + head * a.v_hs;
         if (one) lo = widen<T>(load16(src + e));

@@ -140,6 +140,37 @@ def one_nan(rows, codes):
     return out
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_codes_of_turned_keys_are_the_nearest_but_for_ties_within_32_bits(dtype, interleaved):
+    """x cos - y sin in fp32 with sines rounded once: each sine is off by 2^-25, the
+    product by 2^-24 of itself, the fused sum by 2^-24 of the result, together at
+    most 2.5 2^-24 (|x| + |y|).  A code other than the nearest then lies no further
+    away than the nearest and twice that."""
+    f = fmt("128", dtype, 8)
+    n = 3000
+    k, v = normal(91, n, 8, 128, dtype=f.dtype), normal(92, n, 8, 128, dtype=f.dtype)
+    freq = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().cuda()
+    pos = ints(np.random.default_rng(5).integers(0, 1000000, n))
+    rows = torch.zeros(n, f.row_bytes, dtype=torch.uint8, device="cuda")
+    gpb.row_append(f, k, v, None, None, gpb.Rotation(freq, interleaved=interleaved), pos, rows=rows)
+    x, a = k.cpu().double(), pos.cpu().double()[:, None] * freq.cpu().double()
+    c, s = a.cos()[:, None], a.sin()[:, None]
+    p, q = (x[..., 0::2], x[..., 1::2]) if interleaved else x.chunk(2, -1)
+    turned, size = [p * c - q * s, q * c + p * s], [p.abs() + q.abs()] * 2
+    if interleaved:
+        turned, size = (torch.stack(t, -1).flatten(-2) for t in (turned, size))
+    else:
+        turned, size = (torch.cat(t, -1) for t in (turned, size))
+    scale = rows[:, 2048:2056].cpu().int()[..., None] - 127
+    got = plain_rows(f, rows)[:, :1024].cpu().double().unflatten(1, (8, 128))
+    y, g = torch.ldexp(turned, -scale), torch.ldexp(got, -scale)
+    step = torch.ldexp(torch.ones_like(y), torch.frexp(y)[1].clamp(min=-5) - 4)
+    off = (torch.round(y / step) * step - y).abs()
+    bound = torch.ldexp(2.5 * 2.0 ** -24 * size, -scale)
+    assert ((g - y).abs() <= off + 2 * bound).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_append_of_every_16_bit_pattern(dtype):
     """Every value of the type, infinities, NaN and subnormals among them, beside
