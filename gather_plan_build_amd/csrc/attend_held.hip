@@ -647,7 +647,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     const int row = (wave >> 1) * 32 + (lane & 31);
     FourTiles rows(a, it, lds, wave, lane);
     const bool idle = (wave >> 1) * 32 >= it.n_rows;  // a pair without rows only loads
-    constexpr int BUF = kWideTile * 64 * BLOCKS, BY_KEY = SCALES + 3072, XCHG = BY_KEY + 1024;
+    constexpr int BUF = kWideTile * 64 * BLOCKS, BY_KEY = SCALES + 3 * 1024, XCHG = BY_KEY + 1024;
     static_assert(3 * BUF == SCALES && XCHG + 8 * WAVE_XCHG <= TILES_LDS, "room");
     constexpr int EARLY = 5;  // loads of a tile that go out before its turn begins
     lds_u8 *by_key = lds + BY_KEY + wave * 256;
