@@ -45,11 +45,10 @@ __device__ __forceinline__ void store16(uint8_t *p, u32x4 v) {
 }
 
 // Cosines and sines of the token's pairs into LDS, for all its heads, behind the next
-// barrier; lane `id` of the workgroup begins with pair id.  T is the type they are
-// taken in: with double they are rounded once, with float the angle is as well.
+// barrier; lane `id` of the workgroup begins with pair id.
 template <typename T>
-__device__ __forceinline__ void find_turns(const AppendArgs &a, int64_t t, int id, float *s_cos,
-                                           float *s_sin) {
+__device__ __forceinline__ void find_turns(const AppendArgs &a, int64_t t, int id, T *s_cos,
+                                           T *s_sin) {
   for (int i = id; i < a.pairs; i += kBlock) {
     int axis = 0;
 #pragma unroll
@@ -60,8 +59,8 @@ __device__ __forceinline__ void find_turns(const AppendArgs &a, int64_t t, int i
     if constexpr (__is_same(T, double)) {
       double sn, cs;
       sincospi(2.0 * turns, &sn, &cs);
-      s_cos[i] = static_cast<float>(cs);
-      s_sin[i] = static_cast<float>(sn);
+      s_cos[i] = cs;
+      s_sin[i] = sn;
     } else {
       float sn, cs;
       sincospif(static_cast<float>(2.0 * turns), &sn, &cs);

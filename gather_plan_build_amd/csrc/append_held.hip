@@ -1,12 +1,11 @@
 // append_held.hip -- cache rows held in 8 bits, made from keys and values
 // (gfx950).
 //
-// The turns are computed in fp32, and a turned key is not rounded to the row's type
-// on its way: the code is the one rounding.  Where codes are turned their sines come
-// from 64 bits: a code is an eighth of its value away from the next, so one on the
-// wrong side of the middle is far off, and of 6,144,000 there were 20 with the sines
-// of a 32-bit angle and 12 so, which is what fp32 products leave.  Queries and values
-// in 16 bits have k_row_append's sines, and so its very bits.  A head's
+// A turned key is not rounded to the row's type on its way: the code is the one
+// rounding.  A code on the wrong side of a middle is an eighth of its value off, so
+// the turns of coded values are computed in 64 bits: of 6,144,000 codes 20 were not
+// the nearest in fp32, 12 with sines in 64 bits alone, none so.  Queries and values
+// in 16 bits have k_row_append's turns, and so its very bits.  A head's
 // values share a scale, the least power of two 2^e with max |x| <= 448 2^e,
 // found by an exchange between the lanes that hold them; x 2^-e is exact, and
 // the conversion to e4m3 rounds it to nearest, ties to even.
@@ -18,9 +17,8 @@
 // other halves are with another lane reads those again, which the caches hold.
 // Queries, and a latent's values in 16 bits, go as in the plain append.  44,600
 // latent rows to the pool and packed, 16 query heads: 1.75 GB in 298 us, 5.9 TB/s;
-// 4,099 tokens of 28 + 4 + 4 heads of 64: 14.0 us a call, 13.4 on the GPU (12.5
-// without sines in 64 bits, 14.1 with both kinds by the same waves); eight tokens:
-// 4.6 us there.
+// 4,099 tokens of 28 + 4 + 4 heads of 64: 15.3 us, 2.3 TB/s (14.0 with turns in fp32);
+// eight tokens: 5.7 us on the GPU (4.9).
 #include "append.h"
 #include "held.h"
 
@@ -35,10 +33,21 @@ struct HeldArgs {
   int32_t plain_at, scales_at;  // bytes from a row's start
 };
 
-// Eight values at e of a key head, turned.
-template <typename T>
+// x in fp32, for a rounding to fewer bits that is to come out as if from x: where fp32
+// does not have x, of its two neighbours the one whose last bit is 1.
+__device__ __forceinline__ float odd(double x) {
+  const float f = static_cast<float>(x);
+  const double rest = x - static_cast<double>(f);
+  const uint32_t bits = __builtin_bit_cast(uint32_t, f);
+  if (!(rest > 0.0 || rest < 0.0) || (bits & 1) || f == 0.0f) return f;
+  return __builtin_bit_cast(float, (rest > 0.0) == (f > 0.0f) ? bits + 1 : bits - 1);
+}
+__device__ __forceinline__ float odd(float x) { return x; }
+
+// Eight values at e of a key head, turned in A.
+template <typename T, typename A>
 __device__ __forceinline__ f32x8 turned8(const AppendArgs &a, const uint16_t *src, int e,
-                                         const float *s_cos, const float *s_sin) {
+                                         const A *s_cos, const A *s_sin) {
   const u32x4 own = *reinterpret_cast<const u32x4 *>(src + e);
   f32x8 x = widen<T>(own);
   const int at = e - a.rot_start;
@@ -47,9 +56,9 @@ __device__ __forceinline__ f32x8 turned8(const AppendArgs &a, const uint16_t *sr
     f32x8 y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float cs = s_cos[at / 2 + i], sn = s_sin[at / 2 + i];
-      y[2 * i] = x[2 * i] * cs - x[2 * i + 1] * sn;
-      y[2 * i + 1] = x[2 * i + 1] * cs + x[2 * i] * sn;
+      const A cs = s_cos[at / 2 + i], sn = s_sin[at / 2 + i];
+      y[2 * i] = odd(x[2 * i] * cs - x[2 * i + 1] * sn);
+      y[2 * i + 1] = odd(x[2 * i + 1] * cs + x[2 * i] * sn);
     }
     return y;
   }
@@ -59,8 +68,8 @@ __device__ __forceinline__ f32x8 turned8(const AppendArgs &a, const uint16_t *sr
       widen<T>(*reinterpret_cast<const u32x4 *>(src + (first ? e + a.pairs : e - a.pairs)));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float cs = s_cos[pair + i], sn = s_sin[pair + i];
-    x[i] = first ? x[i] * cs - other[i] * sn : x[i] * cs + other[i] * sn;
+    const A cs = s_cos[pair + i], sn = s_sin[pair + i];
+    x[i] = odd(first ? x[i] * cs - other[i] * sn : x[i] * cs + other[i] * sn);
   }
   return x;
 }
@@ -68,7 +77,7 @@ __device__ __forceinline__ f32x8 turned8(const AppendArgs &a, const uint16_t *sr
 template <typename T>
 __global__ __launch_bounds__(kBlock) void k_row_append_held(AppendArgs a, HeldArgs h) {
   __shared__ __attribute__((aligned(16))) float s_cos[kMaxPairs], s_sin[kMaxPairs];
-  __shared__ __attribute__((aligned(16))) float c_cos[kMaxPairs], c_sin[kMaxPairs];
+  __shared__ __attribute__((aligned(16))) double c_cos[kMaxPairs], c_sin[kMaxPairs];
   const int64_t t = blockIdx.x;
   find_turns<float>(a, t, threadIdx.x, s_cos, s_sin);
   if (a.rot_start < h.k_codes)  // (beside them, by other waves if there are few pairs)

@@ -142,11 +142,11 @@ def one_nan(rows, codes):
 
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_codes_of_turned_keys_are_the_nearest_but_for_ties_within_32_bits(dtype, interleaved):
-    """x cos - y sin in fp32 with sines rounded once: each sine is off by 2^-25, the
-    product by 2^-24 of itself, the fused sum by 2^-24 of the result, together at
-    most 2.5 2^-24 (|x| + |y|).  A code other than the nearest then lies no further
-    away than the nearest and twice that."""
+def test_codes_of_turned_keys_are_the_nearest(dtype, interleaved):
+    """The turn is taken in 64 bits, there as here: sines, products and sum are off by
+    less than 2^-48 (|x| + |y|) in all (angles to 10^6 rounded to 2^-34 apart: their
+    product with 1 / 2 pi is off by 2^-36).  A code other than the nearest then lies
+    no further away than the nearest and twice 2^-33 (|x| + |y|)."""
     f = fmt("128", dtype, 8)
     n = 3000
     k, v = normal(91, n, 8, 128, dtype=f.dtype), normal(92, n, 8, 128, dtype=f.dtype)
@@ -167,7 +167,7 @@ def test_codes_of_turned_keys_are_the_nearest_but_for_ties_within_32_bits(dtype,
     y, g = torch.ldexp(turned, -scale), torch.ldexp(got, -scale)
     step = torch.ldexp(torch.ones_like(y), torch.frexp(y)[1].clamp(min=-5) - 4)
     off = (torch.round(y / step) * step - y).abs()
-    bound = torch.ldexp(2.5 * 2.0 ** -24 * size, -scale)
+    bound = torch.ldexp(2.0 ** -33 * size, -scale)
     assert ((g - y).abs() <= off + 2 * bound).all()
 
 
