@@ -13,11 +13,16 @@
 // each key: there a wave turns its share of a tile on its way to LDS, once.
 //
 // A key's scale goes with the conversion, since a lane has one key of an operand.
-// A value operand holds eight keys to a lane, so there codes are taken at scale 1
-// and the scale goes to the key's weight.  bf16 has the exponents for that.  fp16
-// does not: its m is the maximum of s + log2 scale, the weight 2^(s + log2 scale -
-// m) at most 1 again, and l sums it over the scale.  Powers of two throughout: the
-// weight is rounded as it would be without.
+// A value operand holds eight keys to a lane, so there codes are taken at scale 1.
+// bf16: the scale goes to the key's weight, which is rounded as it would be without.
+// Only a weight below 2^-18 of the largest, of a scale near 2^-100, comes out below
+// the least normal number, 2^-126, and loses places: a result is off by less than
+// 2^-109 a key for that.  fp16 has not the exponents: scales of 2^-15 and 2^8 side
+// by side would leave the one key's weight nothing.  There the eight codes are
+// multiplied by their keys' scales, four vector instructions more, which round
+// nothing: the products are those of the rows read back (44,600 queries over latent
+// rows: 30.5 ms so, 28.6 with the scales in the weights; 32 single tokens: 39 and 37.5
+// us; narrow items the same within 1%).
 #include <type_traits>
 
 #include "attend_kernel.h"
@@ -92,7 +97,7 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
   using Plain::kRows;
   static constexpr bool kHalf = __is_same(T, _Float16);
   // Behind the plain kernel's LDS, a KiB a wave: scales as they come (two tiles of
-  // 256 bytes), and by key (three times 32 floats).  A latent's tiles leave room.
+  // 256 bytes), and by key, as lay_scale has them.  A latent's tiles leave room.
   static constexpr int SCALES = IN_KEY ? 3 * kWideTile * 640 : Plain::LDS;
   static constexpr int LDS = IN_KEY ? Plain::LDS : Plain::LDS + 4096;
 
@@ -112,6 +117,16 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
   static __device__ __forceinline__ int64_t value_scale_at(const AttendArgs &a,
                                                            const AttendItem &it) {
     return key_scale_at(a, it) + (IN_KEY ? 0 : a.hkv);
+  }
+
+  // The largest scale byte an append makes.  A larger one is taken for it in tiles
+  // of codes, so that a weight of 0 meets no infinity.
+  static constexpr uint32_t kMostByte = Held<T>::kMost + 127;
+  // Whether a code comes out of a tile of codes as infinity or NaN (of fp16 a code
+  // beyond 240 does at the largest scale, which no append makes).
+  static __device__ __forceinline__ bool odd_code(uint32_t code, uint32_t scale) {
+    code &= 127;
+    return code == 127 || (kHalf && code > 0x77 && scale >= kMostByte);
   }
 
   // For `careful`.  A tile is odd where its codes are (tiles of codes), or where the
@@ -137,10 +152,9 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       return static_cast<float>(one(src[off + val_at + e], src[off + val_scale]));
     }
     __device__ __forceinline__ bool odd(int64_t off, int e) const {
-      const uint8_t code = src[off + val_at + e];
-      return codes ? (code & 127) == 127
-                   : Plain::not_finite(__builtin_bit_cast(
-                         uint16_t, one(code, src[off + val_scale])));
+      const uint8_t code = src[off + val_at + e], scale = src[off + val_scale];
+      return codes ? odd_code(code, scale)
+                   : Plain::not_finite(__builtin_bit_cast(uint16_t, one(code, scale)));
     }
   };
 
@@ -246,9 +260,16 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
     }
   }
 
-  // Sums of N output tiles (values 32 t0 ..) += weights p of 16 NP keys, from row0 on:
-  // the first codes, then steps FROM .. TO, with each of which one of the loads of
-  // `next` goes out.
+  // Value operand of eight codes; fp16: times their keys' scales.
+  static __device__ __forceinline__ x8 value_operand(u32x2 codes, const x8 &by) {
+    const x8 x = values8<T>(codes, 1.0f);
+    if constexpr (kHalf) return x * by;
+    else return x;
+  }
+
+  // Sums of N output tiles (values 32 t0 ..) += weights p of 16 NP keys, from row0 on,
+  // fp16: with their scales `by`: the first codes, then steps FROM .. TO, with each of
+  // which one of the loads of `next` goes out.
   template <int TILE, int NP, int N>
   struct ValueAhead {
     static constexpr int AHEAD = NP * N < 6 ? NP * N : 6;
@@ -262,109 +283,101 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       return value_codes<TILE>(tile + t0 / 2 * TILE * 64 + row0 * 64, w, i / N * 16, i % N);
     }
     template <int FROM, int TO, typename L>
-    __device__ __forceinline__ void add(const x8 *p, const lds_u8 *tile, int row0,
-                                        const Spots &w, int t0, State *st, const L &next) {
-      steps<FROM, TO>(p, tile, row0, w, t0, st, next, values8<T>(raw[FROM % AHEAD], 1.0f));
+    __device__ __forceinline__ void add(const x8 *p, const x8 *by, const lds_u8 *tile,
+                                        int row0, const Spots &w, int t0, State *st,
+                                        const L &next) {
+      steps<FROM, TO>(p, by, tile, row0, w, t0, st, next,
+                      value_operand(raw[FROM % AHEAD], by[FROM / N]));
     }
     template <int I, int TO, typename L>
-    __device__ __forceinline__ void steps(const x8 *p, const lds_u8 *tile, int row0,
-                                          const Spots &w, int t0, State *st, const L &next,
-                                          x8 now) {
+    __device__ __forceinline__ void steps(const x8 *p, const x8 *by, const lds_u8 *tile,
+                                          int row0, const Spots &w, int t0, State *st,
+                                          const L &next, x8 now) {
       if constexpr (I < TO) {
         st->o[I % N] = mma<T>(now, p[I / N], st->o[I % N]);
         in_order();
-        if constexpr (I + 1 < TO) now = values8<T>(raw[(I + 1) % AHEAD], 1.0f);
+        if constexpr (I + 1 < TO) now = value_operand(raw[(I + 1) % AHEAD], by[(I + 1) / N]);
         if constexpr (I + AHEAD < NP * N) raw[I % AHEAD] = codes(tile, row0, w, t0, I + AHEAD);
         next.template issue<I>();
         in_order();
-        steps<I + 1, TO>(p, tile, row0, w, t0, st, next, now);
+        steps<I + 1, TO>(p, by, tile, row0, w, t0, st, next, now);
       }
     }
   };
 
-  // Whether these lanes' share of a tile's value codes holds a NaN.
-  template <int TILE>
-  static __device__ __forceinline__ bool odd_codes(const lds_u8 *tile, int id, int ids) {
+  // Whether these lanes' share of a tile's value codes holds an odd one (see odd_code);
+  // scale(r) is the scale byte of row r's values.
+  template <int TILE, typename S>
+  static __device__ __forceinline__ bool odd_codes(const lds_u8 *tile, int id, int ids,
+                                                   const S &scale) {
     typedef __attribute__((address_space(3))) u32x4 lds16;
     const lds_u8 *v = tile + VALUES_FROM * TILE * 64;
     bool odd = false;
     for (int c = id; c < TILE * DV / 16; c += ids) {
       const u32x4 x = *(const lds16 *)(v + c * 16);
+      const uint32_t by = kHalf ? scale(c / 4 % TILE) : 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t y = (x[j] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;  // a byte of it 0: NaN
-        odd |= ((y - 0x01010101u) & ~y & 0x80808080u) != 0;
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd |= odd_code(x[j] >> 8 * i, by);
     }
     return odd;
   }
 
-  // Scales of the values of a lane's 16 keys of 32, as weights take them: bf16 the
-  // scale; fp16 its log2 and its inverse.
+  // Scales of the values of a lane's 16 keys of 32: bf16, as its weights take them,
+  // fp16, as its value operands do.
   struct ValueScales {
-    f32x16 a, b;
+    f32x16 a;
+    x8 by[2];
   };
-  // Lane n % 32 has the scale byte of key n's values; `room` is 256 bytes of LDS.
-  static __device__ __forceinline__ void lay_scales(lds_u8 *room, int lane, uint32_t byte) {
+  // The lane has the scale byte of key `lane`'s values, of 32 keys in bf16 and up to 64 in
+  // fp16; `room` is 128 bytes of LDS.
+  static __device__ __forceinline__ void lay_scale(lds_u8 *room, int lane, uint32_t byte) {
     typedef __attribute__((address_space(3))) float lds_float;
-    if (lane >= 32) return;
-    // (a byte of 255, which no append writes, must not make a weight of 0 NaN)
-    const int e = static_cast<int>(min(byte, 254u)) - 127;
-    if constexpr (kHalf) {
-      ((lds_float *)room)[lane] = static_cast<float>(e);
-      ((lds_float *)room)[32 + lane] = __builtin_amdgcn_ldexpf(1.0f, -e);
-    } else {
-      ((lds_float *)room)[lane] = __builtin_amdgcn_ldexpf(1.0f, e);
-    }
+    typedef __attribute__((address_space(3))) T lds_value;
+    if (!kHalf && lane >= 32) return;
+    const float x = __builtin_amdgcn_ldexpf(1.0f, static_cast<int>(min(byte, kMostByte)) - 127);
+    if constexpr (kHalf) ((lds_value *)room)[lane] = static_cast<T>(x);
+    else ((lds_float *)room)[lane] = x;
   }
-  static __device__ __forceinline__ void take_scales(const lds_u8 *room, int half,
+  // Of the 32 keys from key0 on.
+  static __device__ __forceinline__ void take_scales(const lds_u8 *room, int key0, int half,
                                                      ValueScales *x) {
-    typedef __attribute__((address_space(3))) f32x4 lds16;
+    if constexpr (kHalf) {
+      typedef typename Vec<T>::x4 x4;
+      typedef __attribute__((address_space(3))) x4 lds8;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const f32x4 u = *(const lds16 *)(room + (8 * y + 4 * half) * 4);
+      for (int b = 0; b < 2; ++b) {
+        const lds_u8 *at = room + (key0 + 16 * b + 4 * half) * 2;
+        x->by[b] = __builtin_shufflevector(*(const lds8 *)at, *(const lds8 *)(at + 16), 0, 1, 2, 3,
+                                           4, 5, 6, 7);
+      }
+    } else {
+      typedef __attribute__((address_space(3))) f32x4 lds16;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x->a[4 * y + j] = u[j];
-      if constexpr (kHalf) {
-        const f32x4 z = *(const lds16 *)(room + 128 + (8 * y + 4 * half) * 4);
+      for (int y = 0; y < 4; ++y) {
+        const f32x4 u = *(const lds16 *)(room + (key0 + 8 * y + 4 * half) * 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x->b[4 * y + j] = z[j];
+        for (int j = 0; j < 4; ++j) x->a[4 * y + j] = u[j];
       }
     }
   }
-  // The scores of 32 keys, masked, to units of log2 (fp16: with their scales); returns
-  // the largest.
-  static __device__ __forceinline__ float top_of(const AttendArgs &a, const AttendItem &it,
-                                                 float c, f32x16 *s, int key0, bool whole,
-                                                 const Sight &see, int half,
-                                                 const ValueScales &scales) {
-    if (!whole) Plain::mask(a, it, see, key0, half, *s);
-    if constexpr (kHalf) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) (*s)[i] = __builtin_fmaf((*s)[i], c, scales.a[i]);
-    }
-    float top = Plain::largest(*s);
-    if constexpr (!kHalf) top *= c;
-    return fmaxf(top, other_half(top, half));
-  }
-  // As Attend::weights, of what top_of left.
+  // As Attend::weights, bf16: as operands times their keys' scales.
   static __device__ __forceinline__ float weights(const f32x16 &s, float c, float m,
                                                   const ValueScales &scales, x8 *p) {
-    float sum[4] = {};
-    const float ref = Plain::finite_m(m) - SHIFT;
+    if constexpr (kHalf) {
+      return Plain::weights(s, c, m, p);
+    } else {
+      float sum[4] = {};
+      const float ref = Plain::finite_m(m) - SHIFT;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if constexpr (kHalf) {
-        const float x = __builtin_amdgcn_exp2f(s[i] - ref);
-        sum[i % 4] = __builtin_fmaf(x, scales.b[i], sum[i % 4]);
-        p[i / 8][i % 8] = static_cast<T>(x);
-      } else {
+      for (int i = 0; i < 16; ++i) {
         const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ref));
         sum[i % 4] += x;
         p[i / 8][i % 8] = static_cast<T>(x * scales.a[i]);
       }
+      return (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
-    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 
   // The rows of a wave's KEYS keys of tiles of TILE (see Attend::Rows).  Where they
@@ -561,25 +574,28 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         if (v + 4 >= it.n_tiles) loads_done();
         else if (rows.pages) loads_done<NarrowLoader::N + 1>();
         else loads_done<NarrowLoader::N>();
-        if (SCAN && !whole && __any(odd_codes<kNarrowTile>(now, lane, 64))) {
+        const lds_u8 *sc = scales + (n & 1) * 256;
+        const auto value_scale = [&](int r) {
+          return ((const lds_u32 *)sc)[32 + r] >> value_shift & 255;
+        };
+        if (SCAN && !whole && __any(odd_codes<kNarrowTile>(now, lane, 64, value_scale))) {
           left = true;
         } else {
-          const lds_u8 *sc = scales + (n & 1) * 256;
           const uint32_t ks = ((const lds_u32 *)sc)[row] >> key_shift & 255;
-          const uint32_t vs = ((const lds_u32 *)sc)[32 + row] >> value_shift & 255;
-          lay_scales(scales + 512, lane, vs);
+          lay_scale(scales + 512, lane, value_scale(row));
           KeyAhead<kNarrowTile> keys;
           keys.read(now, 0, w);
           f32x16 s;
           products<kNarrowTile>(q, now, 0, w, scale_of(ks), keys, NoLoader(), &s);
           ValueAhead<kNarrowTile, 2, NT> values;
           values.read(now, 0, w, 0);
-          ValueScales by;
-          take_scales(scales + 512, half, &by);
-          Plain::take_top(st, top_of(a, it, c, &s, key0, whole, see, half, by), false);
+          ValueScales scale;
+          take_scales(scales + 512, 0, half, &scale);
+          Plain::take_top(
+              st, Plain::template masked_top<1>(a, it, &s, key0, whole, see, half), false);
           x8 p[2];
-          st.l += weights(s, c, st.m, by, p);
-          values.template add<0, 2 * NT>(p, now, 0, w, 0, &st, NoLoader());
+          st.l += weights(s, c, st.m, scale, p);
+          values.template add<0, 2 * NT>(p, scale.by, now, 0, w, 0, &st, NoLoader());
         }
         lds_reads_done();
         if (v + 8 < it.n_tiles) load(v + 8, n + 2);
@@ -702,9 +718,13 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
       load.template all<0, EARLY>();
       int buf = 0, odd_turn = 0;
       KeyAhead<kWideTile> keys;
-      uint32_t scale;
+      uint32_t scale, laid;  // of the lane's key; of the one that it lays (fp16: of all 64)
+      const auto scale_in = [&](int b, int key) {
+        return ((const lds_u32 *)(lds + SCALES + b * 1024))[key * 4] & 255;
+      };
       const auto begin = [&]() {  // the first reads of the tile in `buf`
-        scale = ((const lds_u32 *)(lds + SCALES + buf * 1024))[(32 * part + (lane & 31)) * 4] & 255;
+        scale = scale_in(buf, 32 * part + (lane & 31));
+        laid = kHalf ? scale_in(buf, lane) : scale;
         keys.read(lds + buf * BUF, 32 * part, w);
       };
       begin();
@@ -716,12 +736,13 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         const lds_u8 *theirs = lds + XCHG + (odd_turn * 4 + (wave ^ 1)) * WAVE_XCHG;
         odd_turn ^= 1;
         const int key0 = Plain::first_key(it, v, kWideTile);
-        const int after = buf == 0 ? 2 : buf - 1;  // of tile v + 2, and v - 1
+        const int used = buf, after = buf == 0 ? 2 : buf - 1;  // after: of tile v + 2, and v - 1
         buf = buf == 2 ? 0 : buf + 1;
         bool whole, odd = false;
         if constexpr (SCAN) {
           whole = Plain::whole_tile(a, it, key0, kWideTile);
-          odd = !whole && __syncthreads_or(odd_codes<kWideTile>(now, threadIdx.x, 256));
+          odd = !whole && __syncthreads_or(odd_codes<kWideTile>(
+                              now, threadIdx.x, 256, [&](int r) { return scale_in(used, r); }));
           left |= odd;
         }
         if (odd || idle) {
@@ -742,18 +763,19 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
             q, now, 32 * part, w, scale_of(scale), keys, beside([&](auto d) {
               constexpr int D = decltype(d)::value;
               if constexpr (D % 2 == 0) load.template issue<EARLY + D / 2>();
-              if constexpr (D == 1) lay_scales(by_key, lane, scale);
+              if constexpr (D == 1) lay_scale(by_key, lane, laid);
               if constexpr (D == 5) whole = Plain::whole_tile(a, it, key0, kWideTile);
               if constexpr (D == 13) next_row = rows.found(v, lane >> 2);
               if constexpr (D == 15) rows.asked(v);
             }),
             &s);
         const bool agree = v == 0 || !whole;
-        ValueScales by;
-        take_scales(by_key, half, &by);
+        ValueScales mine_by;
+        take_scales(by_key, kHalf ? 32 * part : 0, half, &mine_by);
         ValueAhead<kWideTile, 2, NT> first;
         first.read(now, 32 * part, w, part * NT);
-        float top = top_of(a, it, c, &s, key0 + 32 * part, whole, see, half, by);
+        float top =
+            Plain::template masked_top<1>(a, it, &s, key0 + 32 * part, whole, see, half);
         if (agree) {
           if (half == 0) ((lds_float *)(mine + 2048 + 128))[lane] = top;
           __syncthreads();
@@ -761,12 +783,13 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         }
         Plain::take_top(st, top, !agree);
         x8 p[2];
-        st.l += weights(s, c, st.m, by, p);
+        st.l += weights(s, c, st.m, mine_by, p);
         const float m = st.m;
         ((lds8 *)mine)[lane] = p[0];
         ((lds8 *)mine)[64 + lane] = p[1];
         if (half == 0) ((lds_float *)(mine + 2048))[lane] = m;
-        first.template add<0, 2 * NT - 4>(p, now, 32 * part, w, part * NT, &st, NoLoader());
+        first.template add<0, 2 * NT - 4>(p, mine_by.by, now, 32 * part, w, part * NT, &st,
+                                          NoLoader());
         ValueAhead<kWideTile, 2, NT> second;
         second.read(now, 32 * (1 - part), w, part * NT);
         loads_done();
@@ -775,7 +798,10 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         p2[0] = ((const lds8 *)theirs)[lane];
         p2[1] = ((const lds8 *)theirs)[64 + lane];
         const float m2 = ((const lds_float *)(theirs + 2048))[lane & 31];
-        first.template add<2 * NT - 4, 2 * NT>(p, now, 32 * part, w, part * NT, &st, NoLoader());
+        ValueScales their_by;  // (bf16: in the weights)
+        if constexpr (kHalf) take_scales(by_key, 32 * (1 - part), half, &their_by);
+        first.template add<2 * NT - 4, 2 * NT>(p, mine_by.by, now, 32 * part, w, part * NT, &st,
+                                               NoLoader());
         if (__any(m2 != m)) {
           const float both = fmaxf(m, m2);
           const float f2 = __builtin_amdgcn_exp2f(m2 - Plain::finite_m(both));
@@ -790,13 +816,13 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
         }
         load = loader(next_row, after);
         second.template add<0, 2 * NT - 4>(
-            p2, now, 32 * (1 - part), w, part * NT, &st, beside([&](auto i) {
+            p2, their_by.by, now, 32 * (1 - part), w, part * NT, &st, beside([&](auto i) {
               constexpr int I = decltype(i)::value;
               if constexpr (I % 2 == 0 && I / 2 < EARLY) load.template issue<I / 2>();
             }));
         begin();
-        second.template add<2 * NT - 4, 2 * NT>(p2, now, 32 * (1 - part), w, part * NT, &st,
-                                                NoLoader());
+        second.template add<2 * NT - 4, 2 * NT>(p2, their_by.by, now, 32 * (1 - part), w,
+                                                part * NT, &st, NoLoader());
       }
       loads_done();
     }

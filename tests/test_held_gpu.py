@@ -463,6 +463,95 @@ def test_scales_at_both_ends(which, hkv, hq, dtype, size, q, kv):
     b.check()
 
 
+@pytest.mark.parametrize("which,hkv,hq", [("64", 2, 14), ("128", 2, 8), ("latent", 1, 16)])
+@pytest.mark.parametrize("dtype,small,large", [("bf16", 2.0 ** -95, 2.0 ** 100),
+                                               ("fp16", 2.0 ** -10, 240.0 * 2.0 ** 8)])
+@pytest.mark.parametrize("q,kv", [([1, 2], [9, 40]), ([1, 2], [700, 300]), ([1], [3001]),
+                                  ([90], [500])])
+def test_least_scales_beside_the_largest(which, hkv, hq, dtype, small, large, q, kv):
+    """Rows of the least scale between rows of the largest, which hold zeros but for
+    one value: all other results are of the small rows alone, and as near as without
+    the large ones.  (Scores are spread over 2^-19 at most, so that no weight ends
+    where its type does.)"""
+    f = fmt(which, dtype, hkv)
+    b = HeldBatch(f, hq, q, kv)
+    b.q *= 1.5
+    if f.values_in_key:
+        b.q[..., :512] = (b.q[..., :512].double() / small).to(f.dtype)
+        b.q[..., 3] = 0
+    for r in range(len(kv)):
+        x = normal(80 + r, *b.rows[r].shape, dtype=f.dtype).double()
+        at = f.n_kv_heads * f.k_dim
+        k = x[:, :at].unflatten(1, (f.n_kv_heads, f.k_dim))
+        v = k[..., :512] if f.values_in_key else x[:, at:].unflatten(1, (f.n_kv_heads, f.v_dim))
+        v *= small
+        v[1::2] = 0
+        v[1::2, :, 3] = large
+        rows = held_rows(f, k, None if f.values_in_key else v)
+        scales = rows[:, -16] if f.values_in_key else \
+            rows[:, 2 * at + f.n_kv_heads:2 * at + 2 * f.n_kv_heads]
+        assert (scales[::2].long() == LEAST[f.dtype] + 127).all()
+        b.rows[r] = plain_rows(f, rows)
+        base = int(b.k_bases[r])
+        b.dense[base:base + len(rows)] = rows
+        for i, p in enumerate(b.lists[r]):
+            part = rows[i * 64:(i + 1) * 64]
+            b.pool[p * 64:p * 64 + len(part)] = part
+    b.check()
+
+
+@pytest.mark.parametrize("which", ["64", "128", "latent"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("above", [0, 2, 4, 6])
+@pytest.mark.parametrize("q,kv", [(1, 2), (1, 130), (1, 1500), (70, 130)])
+def test_a_weight_beside_that_of_a_larger_scale(which, dtype, above, q, kv):
+    """The last key but q has the largest scale, a score `above` those of the others,
+    and one value that is not zero; the others have the least scale."""
+    f = fmt(which, dtype, 1)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(above)
+    at, d = kv - q, 512 if f.values_in_key else 0
+    k = torch.zeros(kv, 1, f.k_dim, dtype=torch.float64, device="cuda")
+    v = torch.randn(kv, 1, f.v_dim, generator=g, dtype=torch.float64, device="cuda")
+    v *= power(torch.tensor([LEAST[f.dtype] + 5], device="cuda"))
+    v[at] = 0
+    v[at, 0, 3] = 240.0 * 2.0 ** (8 if dtype == "fp16" else 100)
+    if f.values_in_key:
+        k[..., :512] = v
+    k[at, 0, d] = above
+    rows = held_rows(f, k, None if f.values_in_key else v)
+    query = torch.zeros(q, 4, f.k_dim, dtype=f.dtype, device="cuda")
+    query[..., d] = 1
+    x, y = split(f, plain_rows(f, rows))
+    want = attention(query, x, y, torch.arange(kv - q, kv, device="cuda"), 0, 0, 1.0)
+    plan = gpb.AttendPlan(f, 4, [q], [kv])
+    check(*gpb.attend_dense(plan, query, rows, ints([0]), 1.0), want)
+
+
+@pytest.mark.parametrize("which", ["64", "128", "latent"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("q,kv", [(3, 20), (3, 2000), (60, 200)])
+def test_bytes_that_no_append_makes_reach_those_that_see_them_only(which, dtype, q, kv):
+    """Codes past the largest value at the largest scale, and scales past that (of
+    fp16 both may come out infinite): queries before that row keep their values."""
+    f = fmt(which, dtype, 1)
+    b = HeldBatch(f, 4, [q], [kv])
+    at, n = kv - q // 2, q - q // 2
+    values = slice(0, 512) if f.values_in_key else slice(f.k_dim, 2 * f.k_dim)
+    scale = 640 if f.values_in_key else 2 * f.k_dim + 1
+    clean = b.rows[0].clone()
+    clean[at] = 0
+    k, v = split(f, clean)
+    want = attention(b.q[:q], k, v, torch.arange(kv - q, kv, device="cuda"), 0, 0, 0.05)
+    plan = b.plan()
+    for byte in (MOST[f.dtype] + 127, MOST[f.dtype] + 128, 144, 200, 254, 255):
+        for code in (0, 0x08, 0x7e, 0xfe):
+            b.dense[at, values] = code
+            b.dense[at, scale] = byte
+            out, lse = gpb.attend_dense(plan, b.q, b.dense, b.k_bases, 0.05)
+            check(out[:n], lse[:n], [w[:n] for w in want])
+
+
 @pytest.mark.parametrize("which", ["64", "128"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("q,kv,window,sinks,at", [
