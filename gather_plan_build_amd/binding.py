@@ -702,6 +702,13 @@ def _int32(t, numel, what):
     return t.data_ptr()
 
 
+def _in_32_bits(n, what):
+    """n, which the C call takes as int32: ctypes would cut it without a word."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError("%s: %d does not fit in 32 bits" % (what, n))
+    return n
+
+
 def _rows_of(t, row_bytes, what):
     """Number of whole rows in a contiguous tensor of any type."""
     if not t.is_contiguous():
@@ -820,7 +827,8 @@ def rows_read(fmt, rows, locs=None, n_rows=None, out=None, status=None, stream=N
     is what row ``locs[i]`` of ``rows`` (a pool, a dense buffer, packed rows) stands
     for, a row of zeros where ``locs[i]`` is -1; without ``locs`` (int32) row i of
     ``rows``, all of them or the first ``n_rows``.  Exact.  ``out``'s rows may lie
-    apart; without ``out`` one is allocated.  One launch.  Returns ``out``."""
+    apart, by less than 2^31 bytes; without ``out`` one is allocated.  One launch.
+    Returns ``out``."""
     import torch
     if fmt.held is None:
         raise ValueError("rows of 16 bits a value need no reading back")
@@ -830,7 +838,7 @@ def rows_read(fmt, rows, locs=None, n_rows=None, out=None, status=None, stream=N
     n = (n_src if locs is None else locs.numel()) if n_rows is None else int(n_rows)
     if n < 0 or (locs is None and n > n_src):
         raise ValueError("%d rows of %d" % (n, n_src))
-    locs_ptr = None if locs is None else _int32(locs, n, "locs")
+    locs_ptr = None if locs is None else _int32(locs, _in_32_bits(n, "rows to read"), "locs")
     on = _on(dev, stream)
     with on as st:
         if out is None:
@@ -841,7 +849,8 @@ def rows_read(fmt, rows, locs=None, n_rows=None, out=None, status=None, stream=N
             raise ValueError("out: need %s [>= %d, %d] with its last dimension contiguous, got "
                              "%s %s, strides %s" % (fmt.dtype, n, fmt.values, out.dtype,
                                                     tuple(out.shape), out.stride()))
-        apart = 2 * (out.stride(0) if out.shape[0] > 1 else fmt.values)
+        apart = _in_32_bits(2 * (out.stride(0) if out.shape[0] > 1 else fmt.values),
+                            "bytes from one row of out to the next")
         rc = lib.gpb_rows_read(fmt.ref, rows.data_ptr(), n_src, locs_ptr, n, out.data_ptr(), apart,
                                None if status is None else status.data_ptr(), st)
     if rc != OK:

@@ -112,6 +112,50 @@ def test_read_refuses_plain_formats_and_none():
         gpb.rows_read(latent(), torch.zeros(3, 656, dtype=torch.uint8))
 
 
+@pytest.mark.parametrize("n,stride,locs,ok", [
+    (3, 2 ** 30 - 8, None, True),                      # rows 2^31 - 16 bytes apart
+    (3, 2 ** 30, None, False),
+    (3, 2 ** 31 + 576, None, False),                   # 1,152 bytes in the low 32 bits
+    (3, 2 ** 32 + 576, None, False),
+    (1, 2 ** 31 + 576, None, True),                    # one row has no next one
+    (3, 576, 3, True),
+    (2 ** 31, 576, 2 ** 31, False),
+    (2 ** 32 + 3, 576, 2 ** 32 + 3, False),            # 3 in the low 32 bits
+])
+def test_read_refuses_numbers_past_32_bits(monkeypatch, n, stride, locs, ok):
+    """The C call takes the number of rows and their distance as int32.  (Tensors
+    without memory, on a device that is not there.)"""
+    class Here:
+        used = None
+
+        def __init__(self, *a):
+            pass
+
+        def __enter__(self):
+            return None
+
+        def __exit__(self, *a):
+            pass
+
+    calls = []
+    monkeypatch.setattr(B, "_device_index", lambda t, what: 0)
+    monkeypatch.setattr(B, "_same_device", lambda index, **tensors: None)
+    monkeypatch.setattr(B, "_on", Here)
+    monkeypatch.setattr(B.lib, "gpb_rows_read", lambda *a: calls.append(a) or B.OK)
+    f = latent()
+    rows = torch.empty(3, f.row_bytes, dtype=torch.uint8, device="meta")
+    out = torch.empty_strided((n, 576), (stride, 1), dtype=f.dtype, device="meta")
+    at = None if locs is None else torch.empty(locs, dtype=torch.int32, device="meta")
+    if ok:
+        gpb.rows_read(f, rows, at, n_rows=n, out=out)
+        (_, _, n_src, _, n_rows, _, apart, _, _), = calls
+        assert (n_src, n_rows, apart) == (3, n, 1152 if n == 1 else 2 * stride)
+    else:
+        with pytest.raises(ValueError, match="32 bits"):
+            gpb.rows_read(f, rows, at, n_rows=n, out=out)
+        assert not calls
+
+
 def test_a_call_of_another_format_is_refused():
     """The plan's format is the rows': their rows hold other bytes."""
     f = gpb.RowFormat("bf16", 2, 128, 128, held="e4m3")
