@@ -615,6 +615,13 @@ def compose_layer_groups(groups, plan, n_slots, n_cur_pages, n_rows, page_rows, 
 # ---- making the rows, and reading them ---------------------------------------
 
 
+def _in_32_bits(n, what):
+    """n, which the C call takes as int32: ctypes would cut it without a word."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError("%s: %d does not fit in 32 bits" % (what, n))
+    return n
+
+
 class RowFormat:
     """What a token row holds: ``n_kv_heads`` key heads of ``k_dim`` values, then
     as many value heads of ``v_dim``; with ``values_in_key`` one key head whose
@@ -633,7 +640,8 @@ class RowFormat:
         if dtype not in codes:
             raise ValueError("a row's type is bf16 or fp16, not %r" % (dtype,))
         self.dtype = torch.bfloat16 if codes[dtype] == BF16 else torch.float16
-        self.n_kv_heads, self.k_dim, self.v_dim = int(n_kv_heads), int(k_dim), int(v_dim)
+        self.n_kv_heads = _in_32_bits(int(n_kv_heads), "n_kv_heads")
+        self.k_dim, self.v_dim = _in_32_bits(int(k_dim), "k_dim"), _in_32_bits(int(v_dim), "v_dim")
         self.values_in_key = bool(values_in_key)
         if held not in (None, "e4m3"):
             raise ValueError("rows are held in their type (None) or in e4m3, not in %r" % (held,))
@@ -646,7 +654,8 @@ class RowFormat:
             payload = self.v_dim + 2 * (self.k_dim - self.v_dim) + 1
         else:
             payload = self.values + 2 * self.n_kv_heads
-        self.row_bytes = (payload + 15) // 16 * 16 if row_bytes is None else int(row_bytes)
+        self.row_bytes = _in_32_bits(
+            (payload + 15) // 16 * 16 if row_bytes is None else int(row_bytes), "row_bytes")
         self.c = gpb_row_format(codes[dtype] | (HELD_E4M3 if held else 0), self.n_kv_heads,
                                 self.k_dim, self.v_dim, int(self.values_in_key), self.row_bytes)
         self.ref = ctypes.byref(self.c)
@@ -664,7 +673,8 @@ class Rotation:
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq: a contiguous float32 vector, got %s %s"
                              % (inv_freq.dtype, tuple(inv_freq.shape)))
-        self.inv_freq, self.start, self.interleaved = inv_freq, int(start), int(bool(interleaved))
+        self.inv_freq, self.interleaved = inv_freq, int(bool(interleaved))
+        self.start = _in_32_bits(int(start), "start")
         self.pairs = pairs = inv_freq.numel()
         self.index_dtype = torch.int32
         self.sections = [pairs] if sections is None else [int(n) for n in sections]
@@ -700,13 +710,6 @@ def _int32(t, numel, what):
         raise ValueError("%s: need a contiguous int32 tensor of %d, got %s %s"
                          % (what, numel, t.dtype, tuple(t.shape)))
     return t.data_ptr()
-
-
-def _in_32_bits(n, what):
-    """n, which the C call takes as int32: ctypes would cut it without a word."""
-    if not -2 ** 31 <= n < 2 ** 31:
-        raise ValueError("%s: %d does not fit in 32 bits" % (what, n))
-    return n
 
 
 def _rows_of(t, row_bytes, what):
@@ -763,7 +766,7 @@ def row_append(fmt, k, v, pool, pool_locs, rotation=None, positions=None, rows=N
     ``q`` [T, heads, k_dim] are rotated into ``q_out`` (``q`` itself by default).
     A held format quantises the rows as it writes them.  One launch.  T is the length
     of ``pool_locs`` (of ``k`` without a pool)."""
-    T = k.shape[0] if pool_locs is None else pool_locs.numel()
+    T = _in_32_bits(k.shape[0] if pool_locs is None else pool_locs.numel(), "rows to append")
     dev = _device_index(k, "k")
     if q is not None and q_out is None:
         q_out = q
@@ -884,8 +887,10 @@ class AttendPlan:
             raise ValueError("%d q_lens, %d kv_lens" % (h_q.size, h_kv.size))
         if h_g.size % 3:
             raise ValueError("groups: (first request, number of requests, shared keys) each")
-        shape = gpb_attend_shape(h_q.size, int(n_heads), int(window), int(sinks),
-                                 int(page_size), h_q.ctypes.data if h_q.size else None,
+        shape = gpb_attend_shape(h_q.size, _in_32_bits(int(n_heads), "n_heads"),
+                                 _in_32_bits(int(window), "window"),
+                                 _in_32_bits(int(sinks), "sinks"),
+                                 _in_32_bits(int(page_size), "page_size"), h_q.ctypes.data if h_q.size else None,
                                  h_kv.ctypes.data if h_q.size else None, h_g.size // 3,
                                  h_g.ctypes.data if h_g.size else None)
         _lists_in_use[:] = [x for x in _lists_in_use if any(not e.query() for e in x[1].values())]

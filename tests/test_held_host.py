@@ -156,6 +156,29 @@ def test_read_refuses_numbers_past_32_bits(monkeypatch, n, stride, locs, ok):
         assert not calls
 
 
+@pytest.mark.parametrize("past", [2 ** 31, 2 ** 32 + 64, 2 ** 62, -2 ** 31 - 1])
+def test_sizes_past_32_bits_are_refused(past):
+    """They would reach the C call as their low 32 bits (2^32 + 64 as 64)."""
+    wrong = [
+        lambda: gpb.RowFormat("bf16", past, 64, 64),
+        lambda: gpb.RowFormat("bf16", 1, past, 64, held="e4m3"),
+        lambda: gpb.RowFormat("bf16", 1, 64, past, held="e4m3"),
+        lambda: gpb.RowFormat("bf16", 1, 64, 64, row_bytes=past, held="e4m3"),
+        lambda: gpb.Rotation(torch.ones(32), start=past),
+    ]
+    f = gpb.RowFormat("bf16", 1, 64, 64)
+    wrong += [lambda: gpb.AttendPlan(f, past, [1], [1]),
+              lambda: gpb.AttendPlan(f, 4, [1], [1], window=past),
+              lambda: gpb.AttendPlan(f, 4, [1], [1], sinks=past),
+              lambda: gpb.AttendPlan(f, 4, [1], [1], page_size=past)]
+    if 0 < past < 2 ** 40:                     # (what a tensor can have)
+        k = torch.empty(1, 1, 64, dtype=f.dtype, device="meta").expand(past, 1, 64)
+        wrong.append(lambda: gpb.row_append(f, k, k, None, None, rows=k))
+    for call in wrong:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
 def test_a_call_of_another_format_is_refused():
     """The plan's format is the rows': their rows hold other bytes."""
     f = gpb.RowFormat("bf16", 2, 128, 128, held="e4m3")
