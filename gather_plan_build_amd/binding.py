@@ -631,7 +631,8 @@ class RowFormat:
     latent row, the value; the rest of its key stays in 16 bits): half the memory,
     and values off by up to 1/16.  Keys, values and queries are given, and results
     come, in ``dtype``; the rows' tensors are of any type, uint8 [rows, row_bytes]
-    say."""
+    say.  The layout is this library's (gpb.h); other caches' rows in 8 bits, which
+    may be of the same size, cannot be told from them and come out as wrong numbers."""
 
     def __init__(self, dtype, n_kv_heads, k_dim, v_dim, values_in_key=False, row_bytes=None,
                  held=None):

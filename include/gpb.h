@@ -591,7 +591,11 @@ int gpb_compose_layer_noalloc(void *d_dense, const gpb_sources *pools, int32_t n
  * among them, is held as that, and NaN as NaN, which does not count for the
  * scale.  A value so held stands for a number of the row's type, is off by at
  * most 2^-4 of itself or 2^-10 scales, and is exactly what every reader takes
- * it for; what bytes stand for whose scale no append makes is not specified. */
+ * it for; what bytes stand for whose scale no append makes is not specified.
+ * Rows of this layout come from gpb_row_append (or a caller that writes the
+ * same bytes).  No call can tell them from other rows of their size: a cache
+ * row of 512 e4m3 values, four fp32 scales and 64 bf16 values has 656 bytes as
+ * well, can be composed as any row can, and is not to be read or attended. */
 typedef struct gpb_row_format {
   int32_t dtype;                /* GPB_BF16 or GPB_FP16, + GPB_HELD_E4M3       */
   int32_t n_kv_heads;           /* 1 .. 1024                                   */
