@@ -852,8 +852,10 @@ struct AttendHeld : Attend<T, DK, DV, IN_KEY, NARROW> {
   // A wave's share of a tile, 16 keys: its codes come to registers while an earlier
   // tile is worked on, and go to LDS as the values they stand for, to where a tile of
   // 16-bit rows has them.  Four lanes have a row, chunk lane % 4 of 64 bytes at a time,
-  // of keys and then of values; the rows are dealt to the lanes so that four of them
-  // next to each other write to all banks (row lane / 4: four writes' time for one).
+  // of keys and then of values.  A wave's write of 1 KiB then takes 16 clocks of LDS, and
+  // of rows of 256 bytes 32 with row lane / 4 (of 128 bytes 16 as well).  8 would do: lanes
+  // next to each other meet in a bank twice, which are the conflicts that the counters of
+  // these kernels show.
   struct Share {
     static constexpr int N0 = DK / 64, N = (DK + DV) / 64;
     u32x4 raw[N];
