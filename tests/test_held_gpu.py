@@ -502,6 +502,44 @@ def test_least_scales_beside_the_largest(which, hkv, hq, dtype, small, large, q,
 
 @pytest.mark.parametrize("which", ["64", "128", "latent"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("narrow", [True, False])
+def test_every_code_at_every_scale_has_its_value(which, dtype, narrow):
+    """Queries that see one key, over every code that an append makes at every scale
+    (of fp16, down to the least subnormal number).  The weight of an only key is a
+    power of two, so the result is its value.  One request a row: narrow items; one
+    request of all rows: wide ones.  (Of latent rows they are one kernel.)"""
+    dt = DT[dtype]
+    f = fmt(which, dtype, 1)
+    dim = f.v_dim
+    codes = torch.arange(256, device="cuda")
+    codes = codes[(codes & 127) != 127]
+    at = 0 if f.values_in_key else f.k_dim
+    parts = []
+    for e in range(LEAST[dt], MOST[dt] + 1):
+        some = codes if e < MOST[dt] else codes[(codes & 127) <= 0x77]
+        row = some.repeat(-(-dim // len(some)) + 1)
+        for first in range(0, len(some) if dim < len(some) else 1, dim):
+            r = torch.zeros(f.row_bytes, dtype=torch.uint8, device="cuda")
+            if not f.values_in_key:
+                r[2 * dim] = 127                    # the key's scale: its values are zeros
+            r[at:at + dim] = row[first:first + dim].to(torch.uint8)
+            r[640 if f.values_in_key else 2 * dim + 1] = e + 127
+            parts.append(r)
+    rows = torch.stack(parts)
+    n = len(rows)
+    want = split(f, plain_rows(f, rows))[1].expand(-1, 4, -1)
+    q = torch.zeros(n, 4, f.k_dim, dtype=dt, device="cuda")
+    if narrow:
+        plan = gpb.AttendPlan(f, 4, [1] * n, [1] * n)
+        out, _ = gpb.attend_dense(plan, q, rows, ints(range(n)), 1.0)
+    else:
+        plan = gpb.AttendPlan(f, 4, [n], [n], window=1)
+        out, _ = gpb.attend_dense(plan, q, rows, ints([0]), 1.0)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("which", ["64", "128", "latent"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("above", [0, 2, 4, 6])
 @pytest.mark.parametrize("q,kv", [(1, 2), (1, 130), (1, 1500), (70, 130)])
 def test_a_weight_beside_that_of_a_larger_scale(which, dtype, above, q, kv):
